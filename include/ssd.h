@@ -273,6 +273,160 @@ ssd_status ssd_backward(const ssd_problem* prob, const void* x, const float* dt,
                         float* dx, float* ddt, float* dA, float* dB, float* dC, float* dD,
                         float* dinitial_state, void* stream);
 
+/* ---- The operators around the scan in a state space block. ----------------------------------
+ * A block that holds the scan has a short causal convolution in front of it (over x, B and C
+ * together), a gated norm behind it, and a residual sum with a norm before the next block; blocks
+ * of the earlier form use a selective scan whose decay differs for every channel and state entry.
+ *
+ * Tokens: activations are rows of `channels` values, batch * seqlen of them, io dtype. Dense
+ * (seq_starts NULL): `batch` sequences of `seqlen` tokens, nseq must equal batch. Packed: batch
+ * must be 1, and sequence s of the nseq holds the rows [seq_starts[s], seq_starts[s + 1]);
+ * seq_starts is nseq + 1 non-decreasing int32 offsets in device memory. A sequence may be empty.
+ * Rows outside every sequence are neither read nor written. Offsets outside [0, seqlen] or out of
+ * order are not reported (the host does not read them): which rows are computed is then
+ * undefined, but no access leaves the tensors.
+ *
+ * Strides: an input with a `stride` argument has rows that many elements apart (at least its own
+ * width, a multiple of 8), so a slice of a wider projection is taken as it is; 0 means dense.
+ * Everything else is dense. Every pointer is 16-byte aligned.
+ *
+ * Arithmetic is fp32; activations and their gradients are rounded once to the io dtype;
+ * parameters, their gradients, scan states and state gradients are fp32. Results are bitwise
+ * reproducible (fixed reduction order, no atomics). Gradient outputs are overwritten. No output
+ * may overlap an input or another output, but for the states of the single-token entry points
+ * (state_out may be state_in). No call allocates: where a workspace is needed the caller gives
+ * it (the matching _workspace query tells its bytes), and calls that overlap in time need one
+ * each; so every entry point can be captured into a graph, which then holds that workspace.
+ * The current device must be the one that holds the tensors.
+ *
+ * Limits (beyond them SSD_ERR_UNSUPPORTED): channels a multiple of 8 up to 2^20, rows below
+ * 2^31. Errors as for ssd_forward: every check on the host before any HIP call. */
+typedef struct {
+    int64_t batch, seqlen, channels, nseq;
+    const int32_t* seq_starts; /* optional, device memory */
+    int32_t io_dtype;          /* ssd_dtype */
+    int32_t reserved;          /* must be 0 */
+} ssd_tokens;
+
+/* Depthwise causal convolution of width 2 to 4, with the SiLU that follows it (silu nonzero):
+ *     v[t,c] = bias[c] + sum_k weight[c,k] x[t - width + 1 + k, c];   y = v / (1 + exp(-v))
+ * where x before a sequence's first token is its initial state (zeros when NULL). weight
+ * [channels, width] and bias [channels] (nullable) f32; initial_state, final_state [nseq,
+ * width - 1, channels] io dtype: the last width - 1 inputs, oldest first (nullable).
+ * y: the channels in up to three dense tensors y[i] [rows, split[i]], in order (the scan's x, B and
+ * C); the splits are multiples of 8 that sum to channels, unused ones 0 with y[i] NULL. */
+ssd_status ssd_conv(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                    const float* weight, const float* bias, int32_t width, int32_t silu,
+                    const void* initial_state, void* const y[3], const int64_t split[3],
+                    void* final_state, void* stream);
+
+/* One token of it for each of `batch` sequences (seqlen 1, not packed): y from the state and x,
+ * state_out = the state with x appended and its oldest input dropped; may be state_in. */
+ssd_status ssd_conv_step(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                         const float* weight, const float* bias, int32_t width, int32_t silu,
+                         const void* state_in, void* state_out, void* const y[3],
+                         const int64_t split[3], void* stream);
+
+/* Gradients of ssd_conv. dy[i] [rows, split[i]] of dy_dtype (ssd_dtype; f32 as ssd_backward
+ * gives them, or the io dtype), dfinal [nseq, width - 1, channels] f32 (nullable: zero). With
+ * dv = dy * silu'(v): dx[t] = sum_k weight[k] dv[t + width - 1 - k] (io dtype, dense);
+ * dweight[c,k] = sum_t dv[t,c] x[t - width + 1 + k, c]; dbias = sum_t dv (nullable);
+ * dinitial_state [nseq, width - 1, channels] f32 (nullable). */
+ssd_status ssd_conv_backward_workspace(const ssd_tokens* tokens, int32_t width, int64_t* bytes);
+ssd_status ssd_conv_backward(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                             const float* weight, const float* bias, int32_t width, int32_t silu,
+                             const void* initial_state, const void* const dy[3],
+                             const int64_t split[3], int32_t dy_dtype, const float* dfinal,
+                             void* dx, float* dweight, float* dbias, float* dinitial_state,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Selective scan with a decay for every channel d and state entry n. For each sequence, with
+ * g(d) = d / (channels / ngroups) and delta = dt + dt_bias, then softplus if dt_softplus:
+ *     h[t,d,n] = exp(delta[t,d] A[d,n]) h[t-1,d,n] + delta[t,d] x[t,d] B[t,g,n]
+ *     y[t,d] = (sum_n h[t,d,n] C[t,g,n] + D[d] x[t,d]) * z[t,d] / (1 + exp(-z[t,d]))
+ * x, dt, z (nullable: no gate) [rows, channels]; B, C [rows, ngroups, dstate]; io dtype; each with
+ * its row stride. A [channels, dstate], D and dt_bias (nullable) [channels], initial_state
+ * (nullable: zeros), final_state [nseq, channels, dstate] f32. channels / ngroups a multiple of
+ * 8, dstate a multiple of 4 up to 64 (else SSD_ERR_UNSUPPORTED). A softplus of an argument above
+ * 20 is the argument. */
+typedef struct {
+    int64_t dstate, ngroups;
+    const void *x, *dt, *B, *C, *z;
+    int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;
+    const float *A, *D, *dt_bias, *initial_state;
+    int32_t dt_softplus;
+    int32_t reserved; /* must be 0 */
+} ssd_selective;
+
+/* y [rows, channels] io dtype, dense; final_state nullable. */
+ssd_status ssd_selective_scan_workspace(const ssd_tokens* tokens, const ssd_selective* in,
+                                        int64_t* bytes);
+ssd_status ssd_selective_scan(const ssd_tokens* tokens, const ssd_selective* in, void* y,
+                              float* final_state, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
+/* One token for each of `batch` sequences (seqlen 1, not packed): in->initial_state is the state
+ * [batch, channels, dstate], state_out the new one (may be the same). */
+ssd_status ssd_selective_step(const ssd_tokens* tokens, const ssd_selective* in, float* state_out,
+                              void* y, void* stream);
+
+/* Gradients of ssd_selective_scan from dy [rows, channels] (io dtype, dense) and dfinal [nseq,
+ * channels, dstate] f32 (nullable: zero). */
+typedef struct {
+    void *dx, *ddt;             /* [rows, channels] io dtype */
+    void* dz;                   /* the same; required with z, else NULL */
+    void *dB, *dC;              /* [rows, ngroups, dstate] io dtype */
+    float *dA, *dD, *ddt_bias;  /* as A, D, dt_bias; dD and ddt_bias nullable */
+    float* dinitial_state;      /* [nseq, channels, dstate], nullable */
+} ssd_selective_grads;
+ssd_status ssd_selective_backward_workspace(const ssd_tokens* tokens, const ssd_selective* in,
+                                            int64_t* bytes);
+ssd_status ssd_selective_backward(const ssd_tokens* tokens, const ssd_selective* in,
+                                  const void* dy, const float* dfinal,
+                                  const ssd_selective_grads* out, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/* Gated RMS norm over each of ngroups equal runs of the channels (channels / ngroups a multiple of
+ * 8 up to 8192):
+ *     norm_before_gate 0: v = x silu(z), y = weight v / sqrt(mean(v^2) + eps)
+ *     norm_before_gate 1: y = weight silu(z) x / sqrt(mean(x^2) + eps)
+ * x, z (nullable: no gate) [rows, channels] io dtype with row strides, weight [channels] f32,
+ * y dense. Sequences play no part: tokens->seq_starts must be NULL. */
+ssd_status ssd_gated_norm(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                          const void* z, int64_t z_stride, const float* weight, int64_t ngroups,
+                          float eps, int32_t norm_before_gate, void* y, void* stream);
+
+/* Its gradients from dy (io dtype, dense): dx and dz (required with z, else NULL) io dtype,
+ * dweight f32. */
+ssd_status ssd_gated_norm_backward_workspace(const ssd_tokens* tokens, int64_t ngroups,
+                                             int64_t* bytes);
+ssd_status ssd_gated_norm_backward(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                                   const void* z, int64_t z_stride, const float* weight,
+                                   int64_t ngroups, float eps, int32_t norm_before_gate,
+                                   const void* dy, void* dx, void* dz, float* dweight,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Residual sum and the RMS norm of the block that follows:
+ *     r = residual + scale * x (scale [channels] f32, nullable: 1); y = weight r / sqrt(mean(r^2) + eps)
+ * x, y io dtype; residual (nullable: zero) and residual_out of res_dtype (f32 or the io dtype), all
+ * dense but x. The norm is of r in fp32, before it is rounded to res_dtype. channels up to 8192. */
+ssd_status ssd_residual_norm(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                             const void* residual, int32_t res_dtype, const float* scale,
+                             const float* weight, float eps, void* y, void* residual_out,
+                             void* stream);
+
+/* Its gradients from dy (io dtype) and dres (gradient of residual_out, res_dtype; nullable: zero).
+ * residual_sum is the residual_out that the forward wrote; x is read only with a scale (else it
+ * may be NULL). dx io dtype; dresidual res_dtype (nullable); dweight, dscale (required with a
+ * scale, else NULL) f32. */
+ssd_status ssd_residual_norm_backward_workspace(const ssd_tokens* tokens, int64_t* bytes);
+ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* residual_sum,
+                                      int32_t res_dtype, const void* x, int64_t x_stride,
+                                      const float* scale, const float* weight, float eps,
+                                      const void* dy, const void* dres, void* dx,
+                                      void* dresidual, float* dweight, float* dscale,
+                                      void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* ssd_status_string(ssd_status status);
 

@@ -7,30 +7,23 @@
 #include <cstring>
 
 #include "../../include/ssd.h"
+#include "ssd_checks.h"
 #include "ssd_launch.h"
 
 namespace {
 
+using ssd::aligned16;
+using ssd::device_ready;
 using ssd::Dims;
+using ssd::from_hip;
+using ssd::kMaxIndex;
+using ssd::overlap;
+using ssd::Range;
+using ssd::range_of;
 
 constexpr int kVersion = 1 * 10000 + 5 * 100 + 0;  // 1.2: ssd_backward; 1.3: quadratic variant;
                                                    // 1.4: kernel_mask; 1.5: fused forward as run
                                                    // states, chain and fused scan
-constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, int64_t bytes) {
-  uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
 // Shape checks shared by every entry point.
@@ -104,18 +97,6 @@ ssd_status check_options(const ssd_options* o) {
       (o->dt_max > 0.f && !(o->dt_min <= o->dt_max)))  // also rejects NaN
     return SSD_ERR_INVALID_ARGUMENT;
   return SSD_OK;
-}
-
-ssd_status device_ready() {
-  int n = 0;
-  if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) return SSD_ERR_NO_DEVICE;
-  return SSD_OK;
-}
-
-ssd_status from_hip(hipError_t e) {
-  if (e == hipSuccess) return SSD_OK;
-  if (e == hipErrorOutOfMemory) return SSD_ERR_OUT_OF_MEMORY;
-  return SSD_ERR_HIP;
 }
 
 ssd_status check_forward_args(const ssd_problem* prob, const void* x, const float* dt,

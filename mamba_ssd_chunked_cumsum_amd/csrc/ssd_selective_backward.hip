@@ -1,0 +1,571 @@
+// Backward of the selective scan.
+//
+// With e = dy silu(z), a_t = exp(delta_t A) and G_t = e_t C_t + a_{t+1} G_{t+1} (plus the final
+// state's gradient at a sequence's last token), for every (token, channel, state entry):
+//   dC_t[n] = sum_d e h_t      dB_t[n] = sum_d G delta x      q = sum_n G B
+//   w = G a h_{t-1}            dx = D e + delta q             ddelta = x q + sum_n w A
+//   dA = sum_t w delta         dz = dy (sum_n h C + D x) silu'(z)
+//   dD = sum_t e x             ddt = ddelta softplus'         dh0 = a_0 G_0
+// h runs forward and G backward. Rows are cut into chunks; a first kernel computes for every chunk
+// both its end state from a zero state and the gradient of its entering state from a zero gradient
+// at its end, in one pass forward (the second as sum_t (a_0 .. a_t) C_t e_t: the exponentials are
+// shared); a second kernel chains both over the chunks. Then every chunk is independent: the main
+// kernel walks it forward, keeping the states at the start of each quarter in registers, and takes
+// the quarters from the last to the first: forward once more, now keeping h and a of every token
+// in registers, and back. So each exponential is evaluated three times, nothing of size tokens x
+// channels x dstate ever goes to memory, and the vector units bound it.
+//
+// dB and dC sum over channels, i.e. over lanes: sums over the 16 channels of a wave are formed 16
+// values at a time, each step adding two lanes' values and merging two registers into one, so
+// that they cost under two instructions a value; the four waves' sums meet in LDS and the blocks'
+// in memory, added by another kernel in a fixed order.
+#include "ssd_selective.h"
+
+namespace ssd {
+
+namespace {
+
+// States a lane; rows a chunk and a quarter of it, so that a quarter's h and a take 128 registers.
+constexpr int NPL = 4, kQuarter = 16, kChunk = 4 * kQuarter;
+
+struct Work {
+  int chunks;
+  float *state, *adj;  // [chunks, C, N]: end states, entering gradients; then the chained ones
+  float *sums;         // [chunks, C]: sums of delta
+  float *bc;           // [tiles, R, 2, N]: dB and dC over a block's channels
+  float *part;         // [chunks, C N + 2 C]: dA, dD, ddt_bias of a chunk
+};
+
+struct Tile {  // the channels of a block
+  int ct, g, base, stop;
+  __device__ __forceinline__ Tile(const SelArgs& q, int ch, int id) {
+    const int cg = q.C / q.G, tiles = (cg + ch - 1) / ch;
+    ct = id;
+    g = id / tiles;
+    base = g * cg + id % tiles * ch;
+    stop = (g + 1) * cg;
+  }
+};
+
+// T rows from r on in LDS: delta, delta x and e (zero outside every sequence), B and C.
+template <typename IO, int T, int CH, int NP>
+__device__ __forceinline__ void stage(const SelArgs& q, const IO* dy, const Tile& b, int r, int r1,
+                                      uint64_t inside, float (&s_dl)[T][CH], float (&s_du)[T][CH],
+                                      float (&s_e)[T][CH], float (&s_b)[T][NP],
+                                      float (&s_c)[T][NP]) {
+  constexpr int V = 8, NV = T * CH / V;
+#pragma unroll
+  for (int i = 0; i < (NV + kSelThreads - 1) / kSelThreads; ++i) {
+    const int v = threadIdx.x + i * kSelThreads, t = v / (CH / V), cl = v % (CH / V) * V;
+    if (v < NV) {
+      const int64_t row = r + t;
+      const int c = b.base + cl;
+      float dl[V], du[V], e[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) dl[j] = du[j] = e[j] = 0.f;
+      if (((inside >> t) & 1) && c < b.stop) {
+        Vec<IO, V> xr, tr, dr, zr;
+        xr.load((const IO*)q.x + row * q.xs + c);
+        tr.load((const IO*)q.dt + row * q.dts + c);
+        dr.load(dy + row * q.C + c);
+        if (q.z) zr.load((const IO*)q.z + row * q.zs + c);
+        if (q.dt_bias) load_f32<V>(q.dt_bias + c, dl);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          dl[j] += tr.get(j);
+          if (q.softplus) dl[j] = softplus(dl[j]);
+          du[j] = dl[j] * xr.get(j);
+          e[j] = dr.get(j);
+          if (q.z) e[j] *= zr.get(j) * sigmoid(zr.get(j));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        *reinterpret_cast<float4*>(&s_dl[t][cl + j]) = make_float4(dl[j], dl[j + 1], dl[j + 2], dl[j + 3]);
+        *reinterpret_cast<float4*>(&s_du[t][cl + j]) = make_float4(du[j], du[j + 1], du[j + 2], du[j + 3]);
+        *reinterpret_cast<float4*>(&s_e[t][cl + j]) = make_float4(e[j], e[j + 1], e[j + 2], e[j + 3]);
+      }
+    }
+  }
+  constexpr int BV = T * NP / 4;
+#pragma unroll
+  for (int i = 0; i < (BV + kSelThreads - 1) / kSelThreads; ++i) {
+    const int v = threadIdx.x + i * kSelThreads, t = v / (NP / 4), n = v % (NP / 4) * 4;
+    if (v < BV) {
+      Vec<IO, 4> br, cr;
+      br.zero();
+      cr.zero();
+      if (((inside >> t) & 1) && n < q.N) {
+        br.load((const IO*)q.B + (r + t) * q.bs + b.g * q.N + n);
+        cr.load((const IO*)q.Cm + (r + t) * q.cs + b.g * q.N + n);
+      }
+      *reinterpret_cast<float4*>(&s_b[t][n]) = make_float4(br.get(0), br.get(1), br.get(2), br.get(3));
+      *reinterpret_cast<float4*>(&s_c[t][n]) = make_float4(cr.get(0), cr.get(1), cr.get(2), cr.get(3));
+    }
+  }
+}
+
+__device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int row, int c, int k,
+                                           bool live, float (&h)[NPL]) {
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) h[j] = 0.f;
+  if (p && live) {
+    const int s = seq_of(q.rows, row);
+    load_states<NPL>(p + ((int64_t)s * q.C + c) * q.N, k, q.N, h);
+  }
+}
+
+// ---- chunk ends ----------------------------------------------------------------------------------
+template <typename IO, int K>
+__global__ __launch_bounds__(kSelThreads) void k_bwd_ends(SelArgs q, Work w, const IO* dy,
+                                                          const float* dfinal, int tiles) {
+  constexpr int T = 32, NP = NPL * K, CH = kSelThreads / K;
+  __shared__ __attribute__((aligned(16))) float s_dl[T][CH], s_du[T][CH], s_e[T][CH];
+  __shared__ __attribute__((aligned(16))) float s_b[T][NP], s_c[T][NP];
+  const Tile b(q, CH, blockIdx.x % tiles);
+  const int u = blockIdx.x / tiles, k = threadIdx.x % K, ch = threadIdx.x / K, c = b.base + ch;
+  const bool live = c < b.stop;
+  const int r0 = u * kChunk, r1 = min(r0 + kChunk, q.rows.R);
+  float A[NPL], h[NPL], p[NPL], gl[NPL], sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) {
+    A[j] = h[j] = gl[j] = 0.f;
+    p[j] = 1.f;
+  }
+  if (live) load_states<NPL>(q.A + (int64_t)c * q.N, k, q.N, A);
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) A[j] *= kLog2e;
+  for (int r = r0; r < r1; r += T) {
+    uint64_t starts, ends, inside;
+    mark_rows(q.rows, r, min(r + T, r1), starts, ends, inside);
+    __syncthreads();
+    stage<IO, T, CH, NP>(q, dy, b, r, r1, inside, s_dl, s_du, s_e, s_b, s_c);
+    __syncthreads();
+#pragma unroll 4
+    for (int t = 0; t < T; ++t) {
+      if ((starts >> t) & 1) {  // what came before belongs to another sequence
+        seq_states(q, q.h0, r + t, c, k, live, h);
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) p[j] = 0.f;
+      }
+      const float dl = s_dl[t][ch], du = s_du[t][ch], e = s_e[t][ch];
+      sum += dl;
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) {
+        const float a = exp2_fast(dl * A[j]);
+        h[j] = fmaf(a, h[j], du * s_b[t][k * NPL + j]);
+        p[j] *= a;
+        gl[j] = fmaf(p[j], e * s_c[t][k * NPL + j], gl[j]);
+      }
+      if ((ends >> t) & 1) {
+        if (dfinal) {
+          float d[NPL];
+          seq_states(q, dfinal, r + t, c, k, live, d);
+#pragma unroll
+          for (int j = 0; j < NPL; ++j) gl[j] = fmaf(p[j], d[j], gl[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) p[j] = 0.f;
+      }
+    }
+  }
+  if (live) {
+    const int64_t at = ((int64_t)u * q.C + c) * q.N;
+    store_states<NPL>(w.state + at, k, q.N, h);
+    store_states<NPL>(w.adj + at, k, q.N, gl);
+    if (k == 0) w.sums[(int64_t)u * q.C + c] = sum;
+  }
+}
+
+// Chains both ways, in place: state[u] becomes the state entering chunk u, adj[u] the gradient of
+// the state after its last row that comes from later rows of the same sequence. blockIdx.y 0:
+// states, 1: gradients. Where the chunk's rows are not all of one sequence that goes on across it,
+// nothing passes through.
+__global__ __launch_bounds__(256) void k_bwd_chain(SelArgs q, Work w) {
+  constexpr int len = kChunk;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t CN = (int64_t)q.C * q.N;
+  if (id >= CN) return;
+  const int c = (int)(id / q.N);
+  const float A = q.A[id] * kLog2e;
+  float h = 0.f;
+  if (blockIdx.y == 0) {
+    for (int u = 0; u < w.chunks; ++u) {
+      const int r0 = u * len, r1 = min(r0 + len, q.rows.R);
+      const float e = w.state[u * CN + id], d = w.sums[(int64_t)u * q.C + c];
+      w.state[u * CN + id] = h;
+      const int s = seq_of(q.rows, r1 - 1);
+      h = s >= 0 && seq_begin(q.rows, s) < r0 ? fmaf(exp2_fast(A * d), h, e) : e;
+    }
+  } else {
+    for (int u = w.chunks - 1; u >= 0; --u) {
+      const int r0 = u * len, r1 = min(r0 + len, q.rows.R);
+      const float e = w.adj[u * CN + id], d = w.sums[(int64_t)u * q.C + c];
+      w.adj[u * CN + id] = h;
+      const int s = seq_of(q.rows, r0);
+      const bool through = s >= 0 && seq_begin(q.rows, s) < r0 && seq_end(q.rows, s) > r1;
+      h = through ? fmaf(exp2_fast(A * d), h, e) : e;
+    }
+  }
+}
+
+// ---- sums over the channels of a wave --------------------------------------------------------------
+// Four registers to one: sums over the four channels of each row of 16 lanes; quads 1, 3, 0, 2 of
+// the row hold those of v0, v1, v2, v3. Each instruction adds a lane's value and a rotated one, the
+// masked ones only in the quads that take the other register's sum. (The waits in front of a
+// rotated read of a register just written are inside: the assembler does not add them.)
+__device__ __forceinline__ float merge4(float v0, float v1, float v2, float v3) {
+  float o, a, b;
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %1, %3, %3 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %2, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %1, %4, %4 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %0, %1, %1 row_ror:4 row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %0, %2, %2 row_ror:12 row_mask:0xf bank_mask:0x5\n\t"
+      "s_nop 1"
+      : "=&v"(o), "=&v"(a), "=&v"(b)
+      : "v"(v0), "v"(v1), "v"(v2), "v"(v3));
+  return o;
+}
+
+// Two registers to one: sums over the two channels of each row; quads 0 and 1 hold v0's, 2 and 3
+// v1's.
+__device__ __forceinline__ float merge2(float v0, float v1) {
+  float o;
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %0, %1, %1 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %0, %2, %2 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "s_nop 1"
+      : "=&v"(o)
+      : "v"(v0), "v"(v1));
+  return o;
+}
+
+// 64 / K registers to one: lane (row p of 16 lanes, K lanes of a channel b in the row, k) holds the
+// sum over the wave's channels of the value with index merged_value().
+template <int K>
+__device__ __forceinline__ float merge(const float (&v)[64 / K]) {
+  float r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (K == 4) r[i] = merge4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    else if constexpr (K == 8) r[i] = merge2(v[2 * i], v[2 * i + 1]);
+    else r[i] = v[i];
+  }
+  auto add32 = [](float x, float y) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false,
+                                                    false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  };
+  const float lo = add32(r[0], r[1]), hi = add32(r[2], r[3]);
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false,
+                                                  false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+template <int K>
+__device__ __forceinline__ int merged_value() {
+  const int p = (threadIdx.x >> 4) & 3, r = p == 1 ? 2 : p == 2 ? 1 : p;  // r of merge()
+  const int b = (threadIdx.x & 15) / K;
+  if constexpr (K == 4) return 4 * r + (b == 0 ? 2 : b == 1 ? 0 : b == 2 ? 3 : 1);
+  else if constexpr (K == 8) return 2 * r + b;
+  else return r;
+}
+
+// ---- main ----------------------------------------------------------------------------------------
+template <typename IO, int K, bool GATE>
+__global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, SelGrads o,
+                                                             const IO* dy, const float* dfinal,
+                                                             int tiles) {
+  constexpr int T = kQuarter, TC = kChunk, NP = NPL * K, CH = kSelThreads / K;
+  constexpr int MV = 64 / K;  // values of a merge
+  __shared__ __attribute__((aligned(16))) float s_dl[TC][CH], s_du[TC][CH], s_e[TC][CH];
+  __shared__ float s_y[GATE ? TC : 1][CH];
+  __shared__ __attribute__((aligned(16))) float s_b[TC][NP], s_c[TC][NP];
+  __shared__ float s_bc[kSelThreads / 64][T][2][NP];
+  const Tile b(q, CH, blockIdx.x % tiles);
+  const int u = blockIdx.x / tiles, k = threadIdx.x % K, ch = threadIdx.x / K, c = b.base + ch;
+  const int wave = threadIdx.x >> 6;
+  const bool live = c < b.stop;
+  const int r0 = u * TC, r1 = min(r0 + TC, q.rows.R);
+  uint64_t starts, ends, inside;
+  mark_rows(q.rows, r0, r1, starts, ends, inside);
+  stage<IO, TC, CH, NP>(q, dy, b, r0, r1, inside, s_dl, s_du, s_e, s_b, s_c);
+  float A[NPL], h[4][NPL], g[NPL], dA[NPL];
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) A[j] = h[0][j] = g[j] = dA[j] = 0.f;
+  const int64_t at = ((int64_t)u * q.C + c) * q.N;
+  if (live) {
+    load_states<NPL>(q.A + (int64_t)c * q.N, k, q.N, A);
+    load_states<NPL>(w.state + at, k, q.N, h[0]);
+    load_states<NPL>(w.adj + at, k, q.N, g);
+  }
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) A[j] *= kLog2e;
+  __syncthreads();
+  // forward to the start of the last quarter
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) h[s + 1][j] = h[s][j];
+#pragma unroll 4
+    for (int i = 0; i < T; ++i) {
+      const int t = s * T + i;
+      if ((starts >> t) & 1) seq_states(q, q.h0, r0 + t, c, k, live, h[s + 1]);
+      const float dl = s_dl[t][ch], du = s_du[t][ch];
+#pragma unroll
+      for (int j = 0; j < NPL; ++j)
+        h[s + 1][j] = fmaf(exp2_fast(dl * A[j]), h[s + 1][j], du * s_b[t][k * NPL + j]);
+    }
+  }
+  const int mine = merged_value<K>();
+#pragma unroll
+  for (int s = 3; s >= 0; --s) {
+    float hn[T][NPL], a[T][NPL];  // h after each token, its decay
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      const int t = s * T + i;
+      float prev[NPL];
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
+      if ((starts >> t) & 1) seq_states(q, q.h0, r0 + t, c, k, live, prev);
+      const float dl = s_dl[t][ch], du = s_du[t][ch];
+      float y = 0.f;
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) {
+        a[i][j] = exp2_fast(dl * A[j]);
+        hn[i][j] = fmaf(a[i][j], prev[j], du * s_b[t][k * NPL + j]);
+        if (GATE) y = fmaf(hn[i][j], s_c[t][k * NPL + j], y);
+      }
+      if (GATE) {
+        y = sum_lanes<K>(y);
+        if (k == t % K) s_y[t][ch] = y;
+      }
+      __builtin_amdgcn_sched_barrier(0);  // loads of later tokens would cost registers here
+    }
+    float vals[MV < 8 ? 8 : MV];  // dB of the four entries, then dC; K 4: of two tokens
+#pragma unroll
+    for (int i = T - 1; i >= 0; --i) {
+      const int t = s * T + i;
+      if ((ends >> t) & 1) seq_states(q, dfinal, r0 + t, c, k, live, g);
+      float prev[NPL];
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
+      const bool start = (starts >> t) & 1;
+      if (start) seq_states(q, q.h0, r0 + t, c, k, live, prev);
+      const float dl = s_dl[t][ch], du = s_du[t][ch], e = s_e[t][ch];
+      float qs = 0.f, sa = 0.f;
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) {
+        const float G = fmaf(s_c[t][k * NPL + j], e, g[j]);
+        const float aG = a[i][j] * G, wv = aG * prev[j];
+        qs = fmaf(G, s_b[t][k * NPL + j], qs);
+        sa = fmaf(wv, A[j], sa);
+        dA[j] = fmaf(wv, dl, dA[j]);
+        g[j] = aG;
+        const int slot = K == 4 ? (i & 1) * 8 + j : j;
+        vals[slot] = G * du;
+        vals[slot + 4] = hn[i][j] * e;
+      }
+      if constexpr (K == 4) {
+        if ((i & 1) == 0)
+          s_bc[wave][i + (mine >> 3)][(mine >> 2) & 1][k * NPL + (mine & 3)] = merge<K>(vals);
+      } else if constexpr (K == 8) {
+        s_bc[wave][i][mine >> 2][k * NPL + (mine & 3)] = merge<K>(vals);
+      } else {
+        const float vb[4] = {vals[0], vals[1], vals[2], vals[3]};
+        const float vc[4] = {vals[4], vals[5], vals[6], vals[7]};
+        s_bc[wave][i][0][k * NPL + mine] = merge<K>(vb);
+        s_bc[wave][i][1][k * NPL + mine] = merge<K>(vc);
+      }
+      qs = sum_lanes<K>(qs);
+      sa = sum_lanes<K>(sa);
+      // this token's delta x and e have no further reader: q and sum w A take their places
+      if (k < 2) (k ? s_e : s_du)[t][ch] = k ? sa : qs;
+      if (start) {
+        if (o.dh0 && live) {
+          const int sq = seq_of(q.rows, r0 + t);
+          store_states<NPL>(o.dh0 + ((int64_t)sq * q.C + c) * q.N, k, q.N, g);
+        }
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) g[j] = 0.f;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < T * 2 * NP; v += kSelThreads) {
+      const int i = v / (2 * NP), rest = v % (2 * NP), which = rest / NP, n = rest % NP;
+      const int row = r0 + s * T + i;
+      if (row < r1 && n < q.N) {
+        float m = s_bc[0][i][which][n];
+#pragma unroll
+        for (int x = 1; x < kSelThreads / 64; ++x) m += s_bc[x][i][which][n];
+        w.bc[(((int64_t)b.ct * q.rows.R + row) * 2 + which) * q.N + n] = m;
+      }
+    }
+    __syncthreads();
+  }
+  float* part = w.part + (int64_t)u * q.C * (q.N + 2);
+  if (live) store_states<NPL>(part + (int64_t)c * q.N, k, q.N, dA);
+  // outputs of the chunk: a thread takes 8 channels of every 32nd row; e x and ddt are summed over
+  // its rows, then over the threads of the same channels
+  constexpr int V = 8, TR = kSelThreads / (CH / V);
+  const int cl = threadIdx.x % (CH / V) * V, cc = b.base + cl;
+  float sd[V], sb[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) sd[j] = sb[j] = 0.f;
+  if (cc < b.stop) {
+    float D[V], bias[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) D[j] = bias[j] = 0.f;
+    if (q.D) load_f32<V>(q.D + cc, D);
+    if (q.dt_bias) load_f32<V>(q.dt_bias + cc, bias);
+    for (int t = threadIdx.x / (CH / V); t < TC; t += TR) {
+      if (!((inside >> t) & 1)) continue;
+      const int64_t row = r0 + t;
+      Vec<IO, V> xr, tr, dr, zr;
+      xr.load((const IO*)q.x + row * q.xs + cc);
+      tr.load((const IO*)q.dt + row * q.dts + cc);
+      dr.load(dy + row * q.C + cc);
+      if (GATE) zr.load((const IO*)q.z + row * q.zs + cc);
+      float ox[V], ot[V], oz[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float x = xr.get(j), qv = s_du[t][cl + j], sa = s_e[t][cl + j] * 0.6931471805599453f;
+        float e = dr.get(j);
+        if (GATE) {
+          const float zv = zr.get(j), sg = sigmoid(zv);
+          oz[j] = e * fmaf(D[j], x, s_y[t][cl + j]) * (sg * fmaf(zv, 1.f - sg, 1.f));
+          e *= zv * sg;
+        }
+        ox[j] = fmaf(s_dl[t][cl + j], qv, D[j] * e);
+        float dd = fmaf(x, qv, sa);
+        if (q.softplus) dd *= sigmoid(tr.get(j) + bias[j]);
+        ot[j] = dd;
+        sd[j] = fmaf(e, x, sd[j]);
+        sb[j] += dd;
+      }
+      store_vec<IO, V>((IO*)o.dx + row * q.C + cc, ox);
+      store_vec<IO, V>((IO*)o.ddt + row * q.C + cc, ot);
+      if (GATE) store_vec<IO, V>((IO*)o.dz + row * q.C + cc, oz);
+    }
+  }
+  __syncthreads();
+  float* red = &s_dl[0][0];  // [wave][dD, ddt_bias][CH]: the staged rows are done with
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int m = CH / V; m < 64; m <<= 1) {
+      sd[j] += __shfl_xor(sd[j], m, kWave);
+      sb[j] += __shfl_xor(sb[j], m, kWave);
+    }
+    if ((threadIdx.x & 63) < CH / V) {
+      red[(wave * 2 + 0) * CH + cl + j] = sd[j];
+      red[(wave * 2 + 1) * CH + cl + j] = sb[j];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 2 * CH) {
+    const int which = threadIdx.x / CH, x = threadIdx.x % CH;
+    if (b.base + x < b.stop) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSelThreads / 64; ++i) m += red[(i * 2 + which) * CH + x];
+      part[(int64_t)q.C * q.N + (int64_t)which * q.C + b.base + x] = m;
+    }
+  }
+}
+
+// dB and dC: the sums over the tiles of a group, rounded once.
+template <typename IO>
+__global__ __launch_bounds__(256) void k_bwd_bc(SelArgs q, Work w, SelGrads o, int per_group) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t RN = (int64_t)q.rows.R * 2 * q.N;
+  if (id >= RN * q.G) return;
+  const int g = (int)(id / RN);
+  const int64_t at = id % RN, row = at / (2 * q.N);
+  if (seq_of(q.rows, (int)row) < 0) return;
+  const int which = (int)(at / q.N) & 1, n = (int)(at % q.N);
+  const float* p = w.bc + (int64_t)g * per_group * RN + at;
+  float m = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < per_group; ++i) m += p[i * RN];
+  Io<IO>::store((IO*)(which ? o.dC : o.dB), (row * q.G + g) * q.N + n, m);
+}
+
+// Gradients of the initial states of empty sequences: the final states' own.
+__global__ __launch_bounds__(256) void k_bwd_empty(SelArgs q, const float* dfinal, float* dh0) {
+  const int64_t CN = (int64_t)q.C * q.N, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= CN * q.rows.S) return;
+  const int s = (int)(id / CN);
+  if (seq_end(q.rows, s) <= seq_begin(q.rows, s)) dh0[id] = dfinal ? dfinal[id] : 0.f;
+}
+
+int64_t round64(int64_t v) { return (v + 63) / 64 * 64; }
+
+int tiles_of(const SelArgs& a) {  // channel tiles of a group
+  const int ch = kSelThreads / (a.N <= 16 ? 4 : a.N <= 32 ? 8 : 16), cg = a.C / a.G;
+  return (cg + ch - 1) / ch;
+}
+
+// The workspace's parts from `ws` on; its floats.
+int64_t lay_out(const SelArgs& a, float* ws, Work* w) {
+  w->chunks = (a.rows.R + kChunk - 1) / kChunk;
+  const int64_t tiles = (int64_t)tiles_of(a) * a.G, n = w->chunks;
+  const int64_t st = round64(n * a.C * a.N), sm = round64(n * a.C);
+  const int64_t bc = round64(tiles * a.rows.R * 2 * a.N), pt = round64(n * a.C * (a.N + 2));
+  w->state = ws;
+  w->adj = w->state + st;
+  w->sums = w->adj + st;
+  w->bc = w->sums + sm;
+  w->part = w->bc + bc;
+  return 2 * st + sm + bc + pt;
+}
+
+}  // namespace
+
+int64_t selective_backward_bytes(const SelArgs& a) {
+  Work w;
+  return 4 * lay_out(a, nullptr, &w);
+}
+
+hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const float* dfinal,
+                                     const SelGrads& g, float* ws, hipStream_t s) {
+  Work w;
+  lay_out(a, ws, &w);
+  const int per_group = tiles_of(a), tiles = per_group * a.G;
+  const unsigned blocks = (unsigned)((int64_t)tiles * w.chunks);
+  const int64_t CN = (int64_t)a.C * a.N;
+  const hipError_t e = by_states(a.N, [&](auto lanes) {
+    constexpr int K = decltype(lanes)::value;
+    auto run = [&](auto io) {
+      using IO = decltype(io);
+      hipLaunchKernelGGL((k_bwd_ends<IO, K>), dim3(blocks), dim3(kSelThreads), 0, s, a, w,
+                         (const IO*)dy, dfinal, tiles);
+      hipLaunchKernelGGL(k_bwd_chain, dim3((unsigned)((CN + 255) / 256), 2), dim3(256), 0, s, a, w);
+      if (a.z)
+        hipLaunchKernelGGL((k_bwd_main<IO, K, true>), dim3(blocks), dim3(kSelThreads), 0, s, a,
+                           w, g, (const IO*)dy, dfinal, tiles);
+      else
+        hipLaunchKernelGGL((k_bwd_main<IO, K, false>), dim3(blocks), dim3(kSelThreads), 0, s, a,
+                           w, g, (const IO*)dy, dfinal, tiles);
+      const int64_t n = (int64_t)a.rows.R * 2 * a.N * a.G;
+      hipLaunchKernelGGL((k_bwd_bc<IO>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, w,
+                         g, per_group);
+      return hipGetLastError();
+    };
+    return a.io == kIoBf16 ? run(u16{}) : run(float{});
+  });
+  if (e != hipSuccess) return e;
+  if (g.dh0 && a.rows.starts) {
+    hipLaunchKernelGGL(k_bwd_empty, dim3((unsigned)((CN * a.rows.S + 255) / 256)), dim3(256), 0, s,
+                       a, dfinal, g.dh0);
+    const hipError_t e2 = hipGetLastError();
+    if (e2 != hipSuccess) return e2;
+  }
+  return launch_column_sums(w.part, w.chunks, CN, g.dA, (int)CN, 0, 1, a.C, g.dD, a.C, g.ddtb, s);
+}
+
+}  // namespace ssd

@@ -25,7 +25,13 @@ DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 EXPORTS = ("ssd_forward", "ssd_forward_ex", "ssd_forward_noalloc", "ssd_chunk_cumsum",
            "ssd_bmm_chunk",
            "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan", "ssd_workspace_sizes",
-           "ssd_step", "ssd_backward", "ssd_status_string", "ssd_version")
+           "ssd_step", "ssd_backward", "ssd_status_string", "ssd_version",
+           # bound in block.py
+           "ssd_conv", "ssd_conv_step", "ssd_conv_backward_workspace", "ssd_conv_backward",
+           "ssd_selective_scan_workspace", "ssd_selective_scan", "ssd_selective_step",
+           "ssd_selective_backward_workspace", "ssd_selective_backward", "ssd_gated_norm",
+           "ssd_gated_norm_backward_workspace", "ssd_gated_norm_backward", "ssd_residual_norm",
+           "ssd_residual_norm_backward_workspace", "ssd_residual_norm_backward")
 
 
 class SSDProblem(ctypes.Structure):
