@@ -288,7 +288,8 @@ ssd_status ssd_backward(const ssd_problem* prob, const void* x, const float* dt,
  *
  * Strides: an input with a `stride` argument has rows that many elements apart (at least its own
  * width, a multiple of 8), so a slice of a wider projection is taken as it is; 0 means dense.
- * Everything else is dense. Every pointer is 16-byte aligned.
+ * Everything else is dense. Every pointer is 16-byte aligned. (The selective scan's B and C: to
+ * four elements, their strides a multiple of 4; seq_starts: to 4 bytes.)
  *
  * Arithmetic is fp32; activations and their gradients are rounded once to the io dtype;
  * parameters, their gradients, scan states and state gradients are fp32. Results are bitwise

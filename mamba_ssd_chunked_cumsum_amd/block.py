@@ -6,7 +6,7 @@ time. Argument marshalling only, as in libssd.py.
 Activations are [batch, seqlen, channels] of float32 or bfloat16, weights and scan states
 float32. An activation may be a slice of wider rows (one projection's output) as long as its
 channels are adjacent, its rows evenly spaced, the offset 16-byte aligned and the row stride a
-multiple of 8 elements. Packed prompts: batch 1 and cu_seqlens, int32 offsets [nseq + 1] on the
+multiple of 8 elements (the selective scan's B and C: of 4 elements each). Packed prompts: batch 1 and cu_seqlens, int32 offsets [nseq + 1] on the
 device, sequence s being the tokens [cu_seqlens[s], cu_seqlens[s + 1]) (it may be empty); states
 then have nseq entries. Tokens outside every sequence are left as they are in given outputs and
 undefined in fresh ones. cu_seqlens is not read on the host: offsets that decrease or leave
@@ -87,18 +87,22 @@ def _function(name):
 
 # ---- checks ------------------------------------------------------------------------------------
 
-def _tensor(t, name, shape, dtype, dev):
-    """A dense input or output: shape, dtype, device."""
-    if t is None:
-        return None
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _place(t, name, dtype, dev):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _tensor(t, name, shape, dtype, dev):
+    """A dense input or output: shape, dtype, device."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _place(t, name, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -113,12 +117,6 @@ def _rows(t, name, shape, dtype, dev, lead=2):
         return _tensor(t, name, shape, dtype, dev), 0
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
     size, stride = t.shape, t.stride()
     width = 1
     for i in range(len(size) - 1, lead - 1, -1):
@@ -133,6 +131,7 @@ def _rows(t, name, shape, dtype, dev, lead=2):
                 raise ValueError(f"{name}: the rows of tokens must be evenly spaced")
             row = stride[i] // step if row is None else row
         step *= size[i]
+    _place(t, name, dtype, dev)
     return t.data_ptr(), 0 if row is None else row
 
 

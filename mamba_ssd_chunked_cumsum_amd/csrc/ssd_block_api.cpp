@@ -33,9 +33,7 @@ ssd_status check_tokens(const ssd_tokens* t, bool sequences) {
       !is_dtype(t->io_dtype))
     return SSD_ERR_INVALID_ARGUMENT;
   if (t->seq_starts) {
-    if (!sequences || t->batch != 1 || t->nseq <= 0 ||
-        (reinterpret_cast<uintptr_t>(t->seq_starts) & 3u))
-      return SSD_ERR_INVALID_ARGUMENT;
+    if (!sequences || t->batch != 1 || t->nseq <= 0) return SSD_ERR_INVALID_ARGUMENT;
   } else if (sequences && t->nseq != t->batch) {
     return SSD_ERR_INVALID_ARGUMENT;
   }
@@ -50,9 +48,9 @@ ssd_status check_tokens(const ssd_tokens* t, bool sequences) {
 int64_t rows_of(const ssd_tokens* t) { return t->batch * t->seqlen; }
 
 // Effective row stride: 0 means dense. Negative where it is not acceptable.
-int64_t stride_of(int64_t given, int64_t width) {
+int64_t stride_of(int64_t given, int64_t width, int64_t multiple = 8) {
   if (given == 0) return width;
-  return given >= width && given % 8 == 0 && given < (int64_t(1) << 32) ? given : -1;
+  return given >= width && given % multiple == 0 && given < (int64_t(1) << 32) ? given : -1;
 }
 
 // Bytes of `rows` rows of `width` elements at `stride`.
@@ -71,9 +69,9 @@ struct Buffers {
   Range in[kMost], out[kMost];
   int n_in = 0, n_out = 0;
   bool ok = true;
-  void input(const void* p, int64_t bytes) {
+  void input(const void* p, int64_t bytes, uintptr_t align = 16) {
     if (!p) return;
-    ok = ok && aligned16(p);
+    ok = ok && reinterpret_cast<uintptr_t>(p) % align == 0;
     in[n_in++] = range_of(p, bytes);
   }
   void output(const void* p, int64_t bytes) {
@@ -95,9 +93,8 @@ struct Buffers {
 
 int64_t starts_bytes(const ssd_tokens* t) { return (t->nseq + 1) * 4; }
 
-// Offsets need 4-byte alignment only, so they are no `input`.
 void starts_input(Buffers& b, const ssd_tokens* t) {
-  if (t->seq_starts) b.in[b.n_in++] = range_of(t->seq_starts, starts_bytes(t));
+  b.input(t->seq_starts, starts_bytes(t), 4);
 }
 
 // ---- convolution -----------------------------------------------------------------------------------
@@ -163,8 +160,8 @@ ssd_status selective_args(const ssd_tokens* t, const ssd_selective* in, ssd::Sel
   const int64_t e = bytes_of(t->io_dtype);
   const int64_t xs = stride_of(in->x_stride, C), ts = stride_of(in->dt_stride, C),
                 zs = stride_of(in->z_stride, C);
-  // dense rows of B and C need not be a multiple of 8 elements, only of 4
-  const int64_t bs = stride_of(in->b_stride, G * N), cs = stride_of(in->c_stride, G * N);
+  // B and C are read four elements at a time
+  const int64_t bs = stride_of(in->b_stride, G * N, 4), cs = stride_of(in->c_stride, G * N, 4);
   if (xs < 0 || ts < 0 || zs < 0 || bs < 0 || cs < 0) return SSD_ERR_INVALID_ARGUMENT;
   const int64_t widest = xs > ts ? (xs > zs ? xs : zs) : (ts > zs ? ts : zs);
   if (double(R) * double(widest) * 4 > kMaxBytes || double(R) * double(bs > cs ? bs : cs) * 4 > kMaxBytes ||
@@ -176,8 +173,8 @@ ssd_status selective_args(const ssd_tokens* t, const ssd_selective* in, ssd::Sel
   b->input(in->x, span(R, C, xs, e));
   b->input(in->dt, span(R, C, ts, e));
   b->input(in->z, span(R, C, zs, e));
-  b->input(in->B, span(R, G * N, bs, e));
-  b->input(in->C, span(R, G * N, cs, e));
+  b->input(in->B, span(R, G * N, bs, e), 4 * e);
+  b->input(in->C, span(R, G * N, cs, e), 4 * e);
   b->input(in->A, C * N * 4);
   b->input(in->D, C * 4);
   b->input(in->dt_bias, C * 4);
