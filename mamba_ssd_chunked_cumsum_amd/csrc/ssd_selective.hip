@@ -5,227 +5,212 @@
 //
 // For each (token, channel, state entry) one exponential, two products and two fused
 // multiply-adds. With a different decay for every state entry no matrix product covers several
-// tokens, so the vector units and their transcendental rate bound it: 16 + 4 * 4 cycles of a SIMD
-// for 64 entries. The tokens of a sequence are sequential; parallel are the channels, the states of
-// a channel over K lanes, and, where those do not fill the card, chunks of rows (split variant): one
-// kernel computes each chunk's end state from a zero state and the sum of its delta, one chains the
-// chunks (the decay of a whole chunk is exp(A sum delta)), and the scan itself starts every chunk
-// from the state entering it.
+// tokens, so the vector units and their transcendental rate bound it (measured at four waves a
+// SIMD: an exponential of 64 lanes takes 10.6 cycles, another operation 3.1: 23 cycles for 64
+// entries of one token).
 //
-// A block stages a tile of kTile rows in LDS in fp32 (delta and delta x for its channels, B and C),
-// scans it and writes its outputs with D, gate and rounding applied. The loads of the next tile are
-// issued before the scan of the current one.
+// A lane holds one channel with all its states in registers and a wave 64 neighbouring channels, so
+// the sum over n needs no exchange between lanes, and B and C of a token are the same for the whole
+// wave: they come through scalar loads and are unpacked by the scalar unit, beside the vector
+// work. There is no LDS and no barrier. The tokens of a sequence are sequential; parallel are only
+// channels and sequences, and where those do not fill the card the rows are cut into chunks (split
+// variant): one kernel computes each chunk's end state from a zero state and the sum of its delta,
+// one chains the chunks (the decay of a whole chunk is exp(A sum delta)), and the scan starts every
+// chunk from the state entering it. That evaluates the exponentials twice.
+#include <cmath>
+
 #include "ssd_selective.h"
 
 namespace ssd {
 
 namespace {
 
-constexpr int kTile = 32;
+constexpr int kWaves = 4;  // of a block, on neighbouring channel tiles: they share B and C
 
-// The rows a block walks. direct: sequence u, or with the split variant chunk u of `len` rows.
-struct Split2 {
-  int len;      // rows of a chunk; 0: direct
-  int chunks;   // number of chunks
-  float* state; // [chunks, C, N]: end states, then the states entering the chunks
-  float* sums;  // [chunks, C]: sums of delta
+// How the rows are divided: a wave takes sequence u (len 0), or chunk u of `len` rows.
+struct Plan {
+  int len, chunks;
+  float* state;  // [chunks, C, N]: end states, then the states entering the chunks
+  float* sums;   // [chunks, C]: sums of delta; NaN where a sequence begins in the chunk
 };
 
-template <typename IO, int NPL, int K, bool STATES>
-__global__ __launch_bounds__(kSelThreads) void k_scan(SelArgs q, Split2 sp, IO* __restrict__ y,
-                                                      float* __restrict__ fin) {
-  constexpr int CH = kSelThreads / K, NP = NPL * K;
-  constexpr int VS = 8, NV = kTile * CH / VS, PV = (NV + kSelThreads - 1) / kSelThreads;
-  constexpr int BV = kTile * NP / 4, PB = (BV + kSelThreads - 1) / kSelThreads;
-  __shared__ float s_dl[kTile][CH], s_du[kTile][CH];
-  __shared__ float s_y[STATES ? 1 : kTile][CH];
-  __shared__ __attribute__((aligned(16))) float s_b[kTile][NP];
-  __shared__ __attribute__((aligned(16))) float s_c[STATES ? 1 : kTile][NP];
-  const int cg = q.C / q.G, tiles = (cg + CH - 1) / CH;
-  const int ct = blockIdx.x % (tiles * q.G), u = blockIdx.x / (tiles * q.G);
-  const int g = ct / tiles, base = g * cg + (ct % tiles) * CH, stop_c = (g + 1) * cg;
-  const int tid = threadIdx.x, k = tid % K, ch = tid / K, c = base + ch;
-  const bool live = c < stop_c;
+// B or C of a token: N state entries at p, uniform over the wave. NT: N rounded up to a template's
+// size; entries past N read the last ones again (never past the row) and are set to zero.
+template <typename IO, int NT, bool EXACT>
+struct Row {
+  static constexpr int kW = 4 * sizeof(IO) / 4;  // words of four entries
+  uint32_t u[NT / 4][kW];
+  __device__ __forceinline__ void load(const IO* p, int N) {
+    typedef const __attribute__((address_space(4))) uint32_t* Words;  // read through scalar loads
+#pragma unroll
+    for (int i = 0; i < NT / 4; ++i) {
+      const Words w = (Words)(uintptr_t)(p + (EXACT ? 4 * i : min(4 * i, N - 4)));
+#pragma unroll
+      for (int j = 0; j < kW; ++j) u[i][j] = w[j];
+      if (!EXACT && 4 * i >= N) {
+#pragma unroll
+        for (int j = 0; j < kW; ++j) u[i][j] = 0;
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int n) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(u[n / 4][n % 4]);
+    else return __uint_as_float(n & 1 ? u[n / 4][n % 4 / 2] & 0xffff0000u : u[n / 4][n % 4 / 2] << 16);
+  }
+};
+
+template <int NT>
+__device__ __forceinline__ void load_all(const float* p, int N, float (&h)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; i += 4) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < N) v = *reinterpret_cast<const float4*>(p + i);
+    h[i] = v.x; h[i + 1] = v.y; h[i + 2] = v.z; h[i + 3] = v.w;
+  }
+}
+template <int NT>
+__device__ __forceinline__ void store_all(float* p, int N, const float (&h)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; i += 4)
+    if (i < N) *reinterpret_cast<float4*>(p + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+}
+
+// STATES: only the end state and sum of delta of each chunk.
+template <typename IO, int NT, bool EXACT, bool STATES>
+__global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int units,
+                                                      IO* __restrict__ y, float* __restrict__ fin) {
+  constexpr int U = 4;  // tokens whose loads are in flight while the U before them are computed
+  const int cg = q.C / q.G, tiles = (cg + 63) / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = (int64_t)blockIdx.x * kWaves + wave;
+  const int ct = (int)(id % (tiles * q.G)), u = (int)(id / (tiles * q.G));
+  if (u >= units) return;
+  const int g = ct / tiles, c0 = g * cg + ct % tiles * 64, c1 = (g + 1) * cg;
+  const bool live = c0 + (threadIdx.x & 63) < c1;
+  const int c = live ? c0 + (threadIdx.x & 63) : c1 - 1;  // idle lanes compute the last one again
   int r0, r1;
-  if (sp.len && u < sp.chunks) {
-    r0 = u * sp.len;
-    r1 = min(r0 + sp.len, q.rows.R);
+  if (pl.len && u < pl.chunks) {
+    r0 = u * pl.len;
+    r1 = min(r0 + pl.len, q.rows.R);
   } else {
-    const int s = sp.len ? u - sp.chunks : u;
+    const int s = pl.len ? u - pl.chunks : u;
     r0 = seq_begin(q.rows, s);
     r1 = seq_end(q.rows, s);
     if (r1 <= r0) {  // an empty sequence: its state passes through
       if (!STATES && fin && live) {
-        float h[NPL];
         const int64_t at = ((int64_t)s * q.C + c) * q.N;
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) h[j] = 0.f;
-        if (q.h0) load_states<NPL>(q.h0 + at, k, q.N, h);
-        store_states<NPL>(fin + at, k, q.N, h);
+        for (int n = 0; n < q.N; ++n) fin[at + n] = q.h0 ? q.h0[at + n] : 0.f;
       }
       return;
     }
-    if (sp.len) return;
+    if (pl.len) return;
   }
-  float A[NPL], h[NPL], sum = 0.f;
+  float A[NT], h[NT], sum = 0.f;
+  load_all<NT>(q.A + (int64_t)c * q.N, q.N, A);
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) A[j] = h[j] = 0.f;
-  if (live) {
-    load_states<NPL>(q.A + (int64_t)c * q.N, k, q.N, A);
-    if (!STATES && sp.len) load_states<NPL>(sp.state + ((int64_t)u * q.C + c) * q.N, k, q.N, h);
+  for (int n = 0; n < NT; ++n) {
+    A[n] *= kLog2e;
+    h[n] = 0.f;
   }
-#pragma unroll
-  for (int j = 0; j < NPL; ++j) A[j] *= kLog2e;
-
-  // tile loads: vectors of 8 channels of a row, of 4 state entries of a row's B and C
-  Vec<IO, VS> xr[PV], dr[PV];
-  Vec<IO, 4> br[PB], cr[PB];
-  auto fetch = [&](int r) {
-#pragma unroll
-    for (int i = 0; i < PV; ++i) {
-      const int v = tid + i * kSelThreads, row = r + v / (CH / VS), cc = base + v % (CH / VS) * VS;
-      xr[i].zero();
-      dr[i].zero();
-      if (v < NV && row < r1 && cc < stop_c) {
-        xr[i].load((const IO*)q.x + row * q.xs + cc);
-        dr[i].load((const IO*)q.dt + row * q.dts + cc);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < PB; ++i) {
-      const int v = tid + i * kSelThreads, row = r + v / (NP / 4), n = v % (NP / 4) * 4;
-      br[i].zero();
-      cr[i].zero();
-      if (v < BV && row < r1 && n < q.N) {
-        br[i].load((const IO*)q.B + row * q.bs + g * q.N + n);
-        if (!STATES) cr[i].load((const IO*)q.Cm + row * q.cs + g * q.N + n);
-      }
-    }
+  if (!STATES && pl.len) load_all<NT>(pl.state + ((int64_t)u * q.C + c) * q.N, q.N, h);
+  const float bias = q.dt_bias ? q.dt_bias[c] : 0.f, D = q.D ? q.D[c] : 0.f;
+  const IO *x = (const IO*)q.x + c, *dt = (const IO*)q.dt + c, *z = (const IO*)q.z + c;
+  const IO *B = (const IO*)q.B + g * q.N, *C = (const IO*)q.Cm + g * q.N;
+  bool began = false;
+  struct Token {
+    IO x, dt, z;
   };
-  fetch(r0);
-  for (int r = r0; r < r1; r += kTile) {
-    uint64_t starts, ends, inside;
-    mark_rows(q.rows, r, min(r + kTile, r1), starts, ends, inside);
-    float xk[PV][VS];
-#pragma unroll
-    for (int i = 0; i < PV; ++i) {
-      const int v = tid + i * kSelThreads, t = v / (CH / VS), cl = v % (CH / VS) * VS;
-      if (v < NV) {
-        float dl[VS], bias[VS];
-        xr[i].get(xk[i]);
-#pragma unroll
-        for (int j = 0; j < VS; ++j) bias[j] = 0.f;
-        if (q.dt_bias && base + cl < stop_c) load_f32<VS>(q.dt_bias + base + cl, bias);
-        const bool in = (inside >> t) & 1;
-#pragma unroll
-        for (int j = 0; j < VS; ++j) {
-          float d = dr[i].get(j) + bias[j];
-          if (q.softplus) d = softplus(d);
-          dl[j] = in ? d : 0.f;
-        }
-        *reinterpret_cast<float4*>(&s_dl[t][cl]) = make_float4(dl[0], dl[1], dl[2], dl[3]);
-        *reinterpret_cast<float4*>(&s_dl[t][cl + 4]) = make_float4(dl[4], dl[5], dl[6], dl[7]);
-#pragma unroll
-        for (int j = 0; j < VS; ++j) dl[j] = in ? dl[j] * xk[i][j] : 0.f;
-        *reinterpret_cast<float4*>(&s_du[t][cl]) = make_float4(dl[0], dl[1], dl[2], dl[3]);
-        *reinterpret_cast<float4*>(&s_du[t][cl + 4]) = make_float4(dl[4], dl[5], dl[6], dl[7]);
-      }
+  for (int r = r0; r < r1;) {  // sequence by sequence
+    const int s = seq_of(q.rows, r);
+    if (s < 0) {
+      ++r;
+      continue;
     }
+    const int end = seq_end(q.rows, s), b = min(end, r1);
+    if (r == seq_begin(q.rows, s)) {
+      began = true;
 #pragma unroll
-    for (int i = 0; i < PB; ++i) {
-      const int v = tid + i * kSelThreads, t = v / (NP / 4), n = v % (NP / 4) * 4;
-      if (v < BV) {
-        *reinterpret_cast<float4*>(&s_b[t][n]) =
-            make_float4(br[i].get(0), br[i].get(1), br[i].get(2), br[i].get(3));
-        if (!STATES)
-          *reinterpret_cast<float4*>(&s_c[t][n]) =
-              make_float4(cr[i].get(0), cr[i].get(1), cr[i].get(2), cr[i].get(3));
-      }
+      for (int n = 0; n < NT; ++n) h[n] = 0.f;
+      if (q.h0) load_all<NT>(q.h0 + ((int64_t)s * q.C + c) * q.N, q.N, h);
     }
-    __syncthreads();
-    if (r + kTile < r1) fetch(r + kTile);
-#pragma unroll 4
-    for (int t = 0; t < kTile; ++t) {
-      if ((starts >> t) & 1) {  // a sequence begins: its state replaces the one before
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) h[j] = 0.f;
-        sum = 0.f;
-        if (q.h0 && live) {
-          const int s = seq_of(q.rows, r + t);
-          load_states<NPL>(q.h0 + ((int64_t)s * q.C + c) * q.N, k, q.N, h);
-        }
-      }
-      const float dl = s_dl[t][ch], du = s_du[t][ch];
-      float acc = 0.f;
+    auto fetch = [&](int t) {
+      Token k;
+      k.x = x[t * q.xs];
+      k.dt = dt[t * q.dts];
+      if (!STATES && q.z) k.z = z[t * q.zs];
+      return k;
+    };
+    auto token = [&](int t, const Token& k) {
+      Row<IO, NT, EXACT> Bt, Ct;
+      Bt.load(B + t * q.bs, q.N);
+      if (!STATES) Ct.load(C + t * q.cs, q.N);
+      const float xv = Io<IO>::load(&k.x, 0);
+      float dl = Io<IO>::load(&k.dt, 0) + bias;
+      if (q.softplus) dl = softplus(dl);
+      const float du = dl * xv;
+      float acc[2] = {0.f, 0.f};
       if (STATES) sum += dl;
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) {
-        const float a = exp2_fast(dl * A[j]);
-        h[j] = fmaf(a, h[j], du * s_b[t][k * NPL + j]);
-        if (!STATES) acc = fmaf(h[j], s_c[t][k * NPL + j], acc);
+      for (int n = 0; n < NT; ++n) {
+        h[n] = fmaf(exp2_fast(dl * A[n]), h[n], du * Bt.get(n));
+        if (!STATES) acc[n & 1] = fmaf(h[n], Ct.get(n), acc[n & 1]);
       }
       if (!STATES) {
-        acc = sum_lanes<K>(acc);
-        if (k == t % K) s_y[t][ch] = acc;
-        if (fin && ((ends >> t) & 1) && live) {
-          const int s = seq_of(q.rows, r + t);
-          store_states<NPL>(fin + ((int64_t)s * q.C + c) * q.N, k, q.N, h);
+        float o = fmaf(D, xv, acc[0] + acc[1]);
+        if (q.z) {
+          const float zv = Io<IO>::load(&k.z, 0);
+          o *= zv * sigmoid(zv);
         }
+        if (live) Io<IO>::store(y, (int64_t)t * q.C + c, o);
       }
+    };
+    Token cur[U], next[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) cur[i] = fetch(min(r + i, b - 1));
+    for (; r + U <= b; r += U) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) next[i] = fetch(min(r + U + i, b - 1));
+#pragma unroll
+      for (int i = 0; i < U; ++i) token(r + i, cur[i]);
+#pragma unroll
+      for (int i = 0; i < U; ++i) cur[i] = next[i];
     }
-    __syncthreads();
-    if (!STATES) {
 #pragma unroll
-      for (int i = 0; i < PV; ++i) {
-        const int v = tid + i * kSelThreads, t = v / (CH / VS), cl = v % (CH / VS) * VS;
-        if (v < NV && ((inside >> t) & 1) && base + cl < stop_c) {
-          float o[VS], d[VS];
-#pragma unroll
-          for (int j = 0; j < VS; ++j) {
-            o[j] = s_y[t][cl + j];
-            d[j] = 0.f;
-          }
-          if (q.D) load_f32<VS>(q.D + base + cl, d);
-#pragma unroll
-          for (int j = 0; j < VS; ++j) o[j] = fmaf(d[j], xk[i][j], o[j]);
-          if (q.z) {
-            Vec<IO, VS> zr;
-            zr.load((const IO*)q.z + (int64_t)(r + t) * q.zs + base + cl);
-#pragma unroll
-            for (int j = 0; j < VS; ++j) {
-              const float zv = zr.get(j);
-              o[j] *= zv * sigmoid(zv);
-            }
-          }
-          store_vec<IO, VS>(y + (int64_t)(r + t) * q.C + base + cl, o);
-        }
-      }
-    }
+    for (int i = 0; i < U - 1; ++i)
+      if (r + i < b) token(r + i, cur[i]);
+    r = b;
+    if (!STATES && fin && b == end && live)
+      store_all<NT>(fin + ((int64_t)s * q.C + c) * q.N, q.N, h);
   }
   if (STATES && live) {
-    store_states<NPL>(sp.state + ((int64_t)u * q.C + c) * q.N, k, q.N, h);
-    if (k == 0) sp.sums[(int64_t)u * q.C + c] = sum;
+    store_all<NT>(pl.state + ((int64_t)u * q.C + c) * q.N, q.N, h);
+    pl.sums[(int64_t)u * q.C + c] = began ? __builtin_nanf("") : sum;
   }
 }
 
-// Chain over the chunks, in place: state[u] from chunk u's end state (from zero, or from the last
-// sequence that begins in it) to the state entering it. A chunk in which a sequence begins after its
-// first row passes nothing on; at a first row that begins a sequence the scan itself starts anew.
-__global__ __launch_bounds__(256) void k_scan_chain(SelArgs q, Split2 sp) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t CN = (int64_t)q.C * q.N;
+// Chain over the chunks, in place: state[u] from chunk u's end state to the state entering it. Where
+// a sequence begins in a chunk (its sum is NaN, as is the end state where delta was NaN) nothing
+// passes through it. The loads of kAhead chunks are issued together.
+__global__ __launch_bounds__(256) void k_scan_chain(SelArgs q, Plan pl) {
+  constexpr int kAhead = 16;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, CN = (int64_t)q.C * q.N;
   if (id >= CN) return;
   const int c = (int)(id / q.N);
   const float A = q.A[id] * kLog2e;
   float h = 0.f;
-  for (int u = 0; u < sp.chunks; ++u) {
-    const int r0 = u * sp.len, r1 = min(r0 + sp.len, q.rows.R);
-    const float e = sp.state[u * CN + id], d = sp.sums[(int64_t)u * q.C + c];
-    sp.state[u * CN + id] = h;
-    // the sequence of the chunk's last row (-1: none) and whether it began before the chunk
-    const int s = seq_of(q.rows, r1 - 1);
-    const bool through = s >= 0 && seq_begin(q.rows, s) < r0;
-    h = through ? fmaf(exp2_fast(A * d), h, e) : e;
+  for (int u = 0; u < pl.chunks; u += kAhead) {
+    float e[kAhead], d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int v = min(u + i, pl.chunks - 1);
+      e[i] = pl.state[v * CN + id];
+      d[i] = pl.sums[(int64_t)v * q.C + c];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (u + i < pl.chunks) pl.state[(u + i) * CN + id] = h;
+      h = d[i] == d[i] ? fmaf(exp2_fast(A * d[i]), h, e[i]) : e[i];
+    }
   }
 }
 
@@ -274,63 +259,71 @@ __global__ __launch_bounds__(256) void k_sel_step(SelArgs q, float* state_out, I
   }
 }
 
-// The split that a scan takes.
-Split2 plan(const SelArgs& a, int n_cu) {
-  const int K = a.N <= 16 ? 4 : a.N <= 32 ? 8 : 16;
-  Split2 sp{0, 0, nullptr, nullptr};
-  const int ch = kSelThreads / K, cg = a.C / a.G;
-  const int64_t tiles = (int64_t)((cg + ch - 1) / ch) * a.G;
-  const int64_t direct = tiles * a.rows.S;
-  if (direct >= n_cu / 2 || a.rows.R < 512) return sp;
-  // about two blocks a compute unit, chunks of at least 128 rows
-  int64_t chunks = (2 * (int64_t)n_cu + tiles - 1) / tiles;
-  int64_t len = (a.rows.R + chunks - 1) / chunks;
-  len = len < 128 ? 128 : (len + kTile - 1) / kTile * kTile;
-  sp.len = (int)len;
-  sp.chunks = (int)((a.rows.R + len - 1) / len);
-  if (sp.chunks < 3) sp.len = sp.chunks = 0;
-  return sp;
+int64_t tiles_of(const SelArgs& a) { return (int64_t)((a.C / a.G + 63) / 64) * a.G; }
+
+// Direct or split, in cycles of a SIMD. A wave alone on its SIMD issues about half of what several
+// together do; a row costs about 28 cycles a state entry with the SIMD full, as much again for the
+// split's first pass, whose chain and extra launches cost about 15 us more. Chunks are as long as
+// leaves four waves a SIMD, and at least 32 rows.
+Plan plan(const SelArgs& a, int n_cu) {
+  Plan pl{0, 0, nullptr, nullptr};
+  const double simds = 4.0 * n_cu, row = 28.0 * (a.N < 8 ? 8 : a.N);
+  const double tiles = (double)tiles_of(a);
+  const double longest = a.rows.starts ? a.rows.R : a.rows.L;
+  const double waves = std::ceil(tiles * a.rows.S / simds);
+  const double direct = longest * row * (waves < 2 ? 2 : waves);
+  const double split = a.rows.R * tiles * row * 2 / simds + 36000;
+  if (direct <= split) return pl;
+  double len = a.rows.R * tiles / (4 * simds);
+  len = len < 32 ? 32 : std::ceil(len / 8) * 8;
+  pl.len = (int)len;
+  pl.chunks = (int)((a.rows.R + (int64_t)len - 1) / (int64_t)len);
+  if (pl.chunks < 2) pl.len = pl.chunks = 0;
+  return pl;
 }
 
-int64_t state_floats(const SelArgs& a, const Split2& sp) {
-  return ((int64_t)sp.chunks * a.C * a.N + 63) / 64 * 64;
+int64_t state_floats(const SelArgs& a, const Plan& pl) {
+  return ((int64_t)pl.chunks * a.C * a.N + 63) / 64 * 64;
 }
 
 }  // namespace
 
 int64_t selective_bytes(const SelArgs& a, int n_cu) {
-  const Split2 sp = plan(a, n_cu);
-  return sp.len ? 4 * (state_floats(a, sp) + (int64_t)sp.chunks * a.C) : 0;
+  const Plan pl = plan(a, n_cu);
+  return pl.len ? 4 * (state_floats(a, pl) + (int64_t)pl.chunks * a.C) : 0;
 }
 
 hipError_t launch_selective(const SelArgs& a, void* y, float* fin, float* ws, int n_cu,
                             hipStream_t s) {
-  Split2 sp = plan(a, n_cu);
-  sp.state = ws;
-  sp.sums = ws ? ws + state_floats(a, sp) : nullptr;
-  return by_states(a.N, [&](auto lanes) {
-    constexpr int NPL = 4, K = decltype(lanes)::value;
-    const int ch = kSelThreads / K, cg = a.C / a.G;
-    const int64_t tiles = (int64_t)((cg + ch - 1) / ch) * a.G;
-    auto run = [&](auto io) {
-      using IO = decltype(io);
-      if (!sp.len) {
-        hipLaunchKernelGGL((k_scan<IO, NPL, K, false>), dim3((unsigned)(tiles * a.rows.S)),
-                           dim3(kSelThreads), 0, s, a, sp, (IO*)y, fin);
-        return hipGetLastError();
-      }
-      hipLaunchKernelGGL((k_scan<IO, NPL, K, true>), dim3((unsigned)(tiles * sp.chunks)),
-                         dim3(kSelThreads), 0, s, a, sp, (IO*)nullptr, (float*)nullptr);
+  Plan pl = plan(a, n_cu);
+  pl.state = ws;
+  pl.sums = ws ? ws + state_floats(a, pl) : nullptr;
+  auto blocks = [&](int64_t units) { return dim3((unsigned)((tiles_of(a) * units + kWaves - 1) / kWaves)); };
+  auto run = [&](auto io, auto size, auto exact) {
+    using IO = decltype(io);
+    constexpr int NT = decltype(size)::value;
+    constexpr bool EX = decltype(exact)::value;
+    if (pl.len) {
+      hipLaunchKernelGGL((k_scan<IO, NT, EX, true>), blocks(pl.chunks), dim3(64 * kWaves), 0, s, a,
+                         pl, pl.chunks, (IO*)nullptr, (float*)nullptr);
       hipLaunchKernelGGL(k_scan_chain, dim3((unsigned)(((int64_t)a.C * a.N + 255) / 256)),
-                         dim3(256), 0, s, a, sp);
-      // the units behind the chunks pass on the states of empty sequences
-      const int64_t units = sp.chunks + (fin && a.rows.starts ? a.rows.S : 0);
-      hipLaunchKernelGGL((k_scan<IO, NPL, K, false>), dim3((unsigned)(tiles * units)),
-                         dim3(kSelThreads), 0, s, a, sp, (IO*)y, fin);
-      return hipGetLastError();
-    };
-    return a.io == kIoBf16 ? run(u16{}) : run(float{});
-  });
+                         dim3(256), 0, s, a, pl);
+    }
+    // the units behind the chunks pass on the states of empty sequences
+    const int64_t units = pl.len ? pl.chunks + (fin && a.rows.starts ? a.rows.S : 0) : a.rows.S;
+    hipLaunchKernelGGL((k_scan<IO, NT, EX, false>), blocks(units), dim3(64 * kWaves), 0, s, a, pl,
+                       (int)units, (IO*)y, fin);
+    return hipGetLastError();
+  };
+  auto sizes = [&](auto io) {
+    using std::integral_constant;
+    if (a.N == 16) return run(io, integral_constant<int, 16>{}, std::true_type{});
+    if (a.N <= 8) return run(io, integral_constant<int, 8>{}, std::false_type{});
+    if (a.N <= 16) return run(io, integral_constant<int, 16>{}, std::false_type{});
+    if (a.N <= 32) return run(io, integral_constant<int, 32>{}, std::false_type{});
+    return run(io, integral_constant<int, 64>{}, std::false_type{});
+  };
+  return a.io == kIoBf16 ? sizes(u16{}) : sizes(float{});
 }
 
 hipError_t launch_selective_step(const SelArgs& a, float* state_out, void* y, hipStream_t s) {
