@@ -67,6 +67,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf2));
 }
 
+// One value, rounded as pack_bf16 does.
+__device__ __forceinline__ void store_io(float* p, int i, float v) { p[i] = v; }
+__device__ __forceinline__ void store_io(u16* p, int i, float v) { p[i] = (u16)pack_bf16(v, v); }
+
 template <typename IO, int V>
 __device__ __forceinline__ void store_vec(IO* p, const float (&v)[V]) {
   uint32_t u[Vec<IO, V>::kWords];

@@ -59,6 +59,11 @@ struct Row {
   }
 };
 
+template <typename IO>
+__device__ __forceinline__ const char* row_at(const IO* p, int64_t elements) {
+  return (const char*)(p + elements);
+}
+
 template <int NT>
 __device__ __forceinline__ void load_all(const float* p, int N, float (&h)[NT]) {
 #pragma unroll
@@ -114,7 +119,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
   }
   if (!STATES && pl.len) load_all<NT>(pl.state + ((int64_t)u * q.C + c) * q.N, q.N, h);
   const float bias = q.dt_bias ? q.dt_bias[c] : 0.f, D = q.D ? q.D[c] : 0.f;
-  const IO *x = (const IO*)q.x + c, *dt = (const IO*)q.dt + c, *z = (const IO*)q.z + c;
+  const unsigned off = (unsigned)c * sizeof(IO);
   const IO *B = (const IO*)q.B + g * q.N, *C = (const IO*)q.Cm + g * q.N;
   bool began = false;
   struct Token {
@@ -133,17 +138,36 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
       for (int n = 0; n < NT; ++n) h[n] = 0.f;
       if (q.h0) load_all<NT>(q.h0 + ((int64_t)s * q.C + c) * q.N, q.N, h);
     }
-    auto fetch = [&](int t) {
+    // rows that are read next: a row's address is scalar, the channel the lane's offset
+    const char *px = row_at((const IO*)q.x, r * q.xs), *pt = row_at((const IO*)q.dt, r * q.dts),
+               *pz = row_at((const IO*)q.z, r * q.zs), *pb = row_at(B, r * q.bs), *pc = row_at(C, r * q.cs);
+    int ahead = r, ahead_bc = r;  // their indices, held at the last row of the sequence
+    auto fetch = [&] {
       Token k;
-      k.x = x[t * q.xs];
-      k.dt = dt[t * q.dts];
-      if (!STATES && q.z) k.z = z[t * q.zs];
+      k.x = *(const IO*)(px + off);
+      k.dt = *(const IO*)(pt + off);
+      if (!STATES && q.z) k.z = *(const IO*)(pz + off);
+      if (++ahead < b) {
+        px += q.xs * sizeof(IO);
+        pt += q.dts * sizeof(IO);
+        if (!STATES) pz += q.zs * sizeof(IO);
+      }
       return k;
     };
-    auto token = [&](int t, const Token& k) {
-      Row<IO, NT, EXACT> Bt, Ct;
-      Bt.load(B + t * q.bs, q.N);
-      if (!STATES) Ct.load(C + t * q.cs, q.N);
+    struct Rows2 {
+      Row<IO, NT, EXACT> B, C;
+    };
+    auto rows = [&] {
+      Rows2 w;
+      w.B.load((const IO*)pb, q.N);
+      if (!STATES) w.C.load((const IO*)pc, q.N);
+      if (++ahead_bc < b) {
+        pb += q.bs * sizeof(IO);
+        if (!STATES) pc += q.cs * sizeof(IO);
+      }
+      return w;
+    };
+    auto token = [&](int t, const Token& k, const Rows2& w) {
       const float xv = Io<IO>::load(&k.x, 0);
       float dl = Io<IO>::load(&k.dt, 0) + bias;
       if (q.softplus) dl = softplus(dl);
@@ -152,8 +176,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
       if (STATES) sum += dl;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        h[n] = fmaf(exp2_fast(dl * A[n]), h[n], du * Bt.get(n));
-        if (!STATES) acc[n & 1] = fmaf(h[n], Ct.get(n), acc[n & 1]);
+        h[n] = fmaf(exp2_fast(dl * A[n]), h[n], du * w.B.get(n));
+        if (!STATES) acc[n & 1] = fmaf(h[n], w.C.get(n), acc[n & 1]);
       }
       if (!STATES) {
         float o = fmaf(D, xv, acc[0] + acc[1]);
@@ -161,23 +185,30 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
           const float zv = Io<IO>::load(&k.z, 0);
           o *= zv * sigmoid(zv);
         }
-        if (live) Io<IO>::store(y, (int64_t)t * q.C + c, o);
+        // (idle lanes write the last channel's value once more)
+        store_io((IO*)((char*)(y + (int64_t)t * q.C) + off), 0, o);
       }
     };
-    Token cur[U], next[U];
+    Token cur[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) cur[i] = fetch(min(r + i, b - 1));
+    for (int i = 0; i < U; ++i) cur[i] = fetch();
+    Rows2 w = rows();
     for (; r + U <= b; r += U) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) next[i] = fetch(min(r + U + i, b - 1));
-#pragma unroll
-      for (int i = 0; i < U; ++i) token(r + i, cur[i]);
-#pragma unroll
-      for (int i = 0; i < U; ++i) cur[i] = next[i];
+      for (int i = 0; i < U; ++i) {
+        const Rows2 wn = rows();  // a token ahead
+        const Token k = cur[i];
+        cur[i] = fetch();
+        token(r + i, k, w);
+        w = wn;
+      }
     }
 #pragma unroll
     for (int i = 0; i < U - 1; ++i)
-      if (r + i < b) token(r + i, cur[i]);
+      if (r + i < b) {
+        token(r + i, cur[i], w);
+        w = rows();
+      }
     r = b;
     if (!STATES && fin && b == end && live)
       store_all<NT>(fin + ((int64_t)s * q.C + c) * q.N, q.N, h);
@@ -263,21 +294,27 @@ int64_t tiles_of(const SelArgs& a) { return (int64_t)((a.C / a.G + 63) / 64) * a
 
 // Direct or split, in cycles of a SIMD. A wave alone on its SIMD issues about half of what several
 // together do; a row costs about 28 cycles a state entry with the SIMD full, as much again for the
-// split's first pass, whose chain and extra launches cost about 15 us more. Chunks are as long as
-// leaves four waves a SIMD, and at least 32 rows.
+// split's first pass, whose chain and extra launches cost about 15 us more. The chunks make the
+// largest number of waves up to four a SIMD that leaves them 32 rows or more: just over a whole
+// number of waves a SIMD would leave most of the card idle for the last of them.
 Plan plan(const SelArgs& a, int n_cu) {
   Plan pl{0, 0, nullptr, nullptr};
   const double simds = 4.0 * n_cu, row = 28.0 * (a.N < 8 ? 8 : a.N);
-  const double tiles = (double)tiles_of(a);
+  const int64_t tiles = tiles_of(a);
   const double longest = a.rows.starts ? a.rows.R : a.rows.L;
-  const double waves = std::ceil(tiles * a.rows.S / simds);
+  const double waves = std::ceil(double(tiles) * a.rows.S / simds);
   const double direct = longest * row * (waves < 2 ? 2 : waves);
-  const double split = a.rows.R * tiles * row * 2 / simds + 36000;
+  const double split = double(a.rows.R) * tiles * row * 2 / simds + 36000;
   if (direct <= split) return pl;
-  double len = a.rows.R * tiles / (4 * simds);
-  len = len < 32 ? 32 : std::ceil(len / 8) * 8;
-  pl.len = (int)len;
-  pl.chunks = (int)((a.rows.R + (int64_t)len - 1) / (int64_t)len);
+  for (int w = 4; w >= 1; --w) {
+    const int64_t chunks = (int64_t)(w * simds) / tiles;
+    if (chunks < 2) break;
+    const int64_t len = ((a.rows.R + chunks - 1) / chunks + 3) / 4 * 4;
+    if (len < 32 && w > 1) continue;
+    pl.len = (int)(len < 32 ? 32 : len);
+    pl.chunks = (a.rows.R + pl.len - 1) / pl.len;
+    break;
+  }
   if (pl.chunks < 2) pl.len = pl.chunks = 0;
   return pl;
 }
