@@ -105,21 +105,13 @@ __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
-// log(1 + exp(v)) = max(v, 0) + log1p(exp(-|v|)), and with e = exp(-|v|) <= 1,
-// log1p(e) = 2 artanh(s) at s = e / (2 + e) <= 1/3: the odd power series of artanh, whose first
-// term left out is s^17 / 17 < 2^-29 s. Exact to a few fp32 roundings also where it is small.
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|) <= 1. With w = 1 + e rounded, what the
+// rounding lost, e - (w - 1), is exact, and log(1 + e) = log(w) + that / w; the 1 / w is left out:
+// where it is not near 1 the whole term is below the result's last place. (Measured against
+// double over [-24, 24]: at most 6e-7 relative above -8, 1.7e-6 at -24, from the argument of exp.)
 __device__ __forceinline__ float softplus(float v) {
-  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
-  const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-  float p = 1.f / 15.f;
-  p = fmaf(p, q, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  p = fmaf(p, q, 1.f);
-  return fmaxf(v, 0.f) + 2.f * s * p;
+  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), w = 1.f + e;
+  return fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(w), 0.6931471805599453f, e - (w - 1.f));
 }
 
 }  // namespace ssd

@@ -84,7 +84,7 @@ __device__ __forceinline__ void store_all(float* p, int N, const float (&h)[NT])
 template <typename IO, int NT, bool EXACT, bool STATES>
 __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int units,
                                                       IO* __restrict__ y, float* __restrict__ fin) {
-  constexpr int U = 4;  // tokens whose loads are in flight while the U before them are computed
+  constexpr int GR = 8, U = 4;  // tokens whose loads are in flight while the U before them are computed
   const int cg = q.C / q.G, tiles = (cg + 63) / 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t id = (int64_t)blockIdx.x * kWaves + wave;
@@ -109,6 +109,18 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
       return;
     }
     if (pl.len) return;
+  }
+  if (STATES) {  // only what follows the last sequence start in the chunk reaches its end, and only
+                 // a sequence that goes on behind the chunk needs it
+    const int s = seq_of(q.rows, r1 - 1);
+    if (s < 0 || seq_end(q.rows, s) <= r1) {
+      if (live) {
+        for (int n = 0; n < q.N; ++n) pl.state[((int64_t)u * q.C + c) * q.N + n] = 0.f;
+        pl.sums[(int64_t)u * q.C + c] = __builtin_nanf("");
+      }
+      return;
+    }
+    r0 = max(r0, seq_begin(q.rows, s));
   }
   float A[NT], h[NT], sum = 0.f;
   load_all<NT>(q.A + (int64_t)c * q.N, q.N, A);
@@ -174,10 +186,23 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
       const float du = dl * xv;
       float acc[2] = {0.f, 0.f};
       if (STATES) sum += dl;
+      // in groups of GR state entries, so that no instruction waits for the one before it
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        h[n] = fmaf(exp2_fast(dl * A[n]), h[n], du * w.B.get(n));
-        if (!STATES) acc[n & 1] = fmaf(h[n], w.C.get(n), acc[n & 1]);
+      for (int n = 0; n < NT; n += GR) {
+        float a[GR], v[GR];
+#pragma unroll
+        for (int j = 0; j < GR; ++j) a[j] = dl * A[n + j];
+#pragma unroll
+        for (int j = 0; j < GR; ++j) a[j] = exp2_fast(a[j]);
+#pragma unroll
+        for (int j = 0; j < GR; ++j) v[j] = du * w.B.get(n + j);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < GR; ++j) h[n + j] = fmaf(a[j], h[n + j], v[j]);
+        if (!STATES) {
+#pragma unroll
+          for (int j = 0; j < GR; ++j) acc[j & 1] = fmaf(h[n + j], w.C.get(n + j), acc[j & 1]);
+        }
       }
       if (!STATES) {
         float o = fmaf(D, xv, acc[0] + acc[1]);
@@ -290,6 +315,8 @@ __global__ __launch_bounds__(256) void k_sel_step(SelArgs q, float* state_out, I
   }
 }
 
+constexpr int kMinLen = 16;  // rows of a chunk
+
 int64_t tiles_of(const SelArgs& a) { return (int64_t)((a.C / a.G + 63) / 64) * a.G; }
 
 // Direct or split, in cycles of a SIMD. A wave alone on its SIMD issues about half of what several
@@ -310,8 +337,8 @@ Plan plan(const SelArgs& a, int n_cu) {
     const int64_t chunks = (int64_t)(w * simds) / tiles;
     if (chunks < 2) break;
     const int64_t len = ((a.rows.R + chunks - 1) / chunks + 3) / 4 * 4;
-    if (len < 32 && w > 1) continue;
-    pl.len = (int)(len < 32 ? 32 : len);
+    if (len < kMinLen && w > 1) continue;
+    pl.len = (int)(len < kMinLen ? kMinLen : len);
     pl.chunks = (a.rows.R + pl.len - 1) / pl.len;
     break;
   }
