@@ -31,7 +31,7 @@ constexpr int NPL = 4, kQuarter = 16, kChunk = 4 * kQuarter;
 struct Work {
   int chunks;
   float *state, *adj;  // [chunks, C, N]: end states, entering gradients; then the chained ones
-  float *sums;         // [chunks, C]: sums of delta
+  float *sums;         // [2, chunks, C]: sums of delta, for either direction
   float *bc;           // [tiles, R, 2, N]: dB and dC over a block's channels
   float *part;         // [chunks, C N + 2 C]: dA, dD, ddt_bias of a chunk
 };
@@ -174,38 +174,45 @@ __global__ __launch_bounds__(kSelThreads) void k_bwd_ends(SelArgs q, Work w, con
     const int64_t at = ((int64_t)u * q.C + c) * q.N;
     store_states<NPL>(w.state + at, k, q.N, h);
     store_states<NPL>(w.adj + at, k, q.N, gl);
-    if (k == 0) w.sums[(int64_t)u * q.C + c] = sum;
+    if (k == 0) {
+      // what passes: the state through rows of one sequence that began before the chunk, its
+      // gradient if that sequence also goes on behind it
+      const int s = seq_of(q.rows, r1 - 1);
+      const bool fwd = s >= 0 && seq_begin(q.rows, s) < r0;
+      const bool bwd = fwd && seq_end(q.rows, s) > r1;
+      const float none = __builtin_nanf("");
+      w.sums[(int64_t)u * q.C + c] = fwd ? sum : none;
+      w.sums[((int64_t)w.chunks + u) * q.C + c] = bwd ? sum : none;
+    }
   }
 }
 
 // Chains both ways, in place: state[u] becomes the state entering chunk u, adj[u] the gradient of
 // the state after its last row that comes from later rows of the same sequence. blockIdx.y 0:
-// states, 1: gradients. Where the chunk's rows are not all of one sequence that goes on across it,
-// nothing passes through.
+// states, 1: gradients. Where the chunk's rows are not all of one sequence that goes on across it
+// (sums: NaN), nothing passes through. The loads of kAhead chunks are issued together.
 __global__ __launch_bounds__(256) void k_bwd_chain(SelArgs q, Work w) {
-  constexpr int len = kChunk;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t CN = (int64_t)q.C * q.N;
+  constexpr int kAhead = 16;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, CN = (int64_t)q.C * q.N;
   if (id >= CN) return;
-  const int c = (int)(id / q.N);
+  const int c = (int)(id / q.N), back = blockIdx.y;
   const float A = q.A[id] * kLog2e;
+  const float* sums = w.sums + (back ? (int64_t)w.chunks * q.C : 0);
+  float* state = back ? w.adj : w.state;
   float h = 0.f;
-  if (blockIdx.y == 0) {
-    for (int u = 0; u < w.chunks; ++u) {
-      const int r0 = u * len, r1 = min(r0 + len, q.rows.R);
-      const float e = w.state[u * CN + id], d = w.sums[(int64_t)u * q.C + c];
-      w.state[u * CN + id] = h;
-      const int s = seq_of(q.rows, r1 - 1);
-      h = s >= 0 && seq_begin(q.rows, s) < r0 ? fmaf(exp2_fast(A * d), h, e) : e;
+  for (int i0 = 0; i0 < w.chunks; i0 += kAhead) {
+    float e[kAhead], d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int v = min(i0 + i, w.chunks - 1), u = back ? w.chunks - 1 - v : v;
+      e[i] = state[u * CN + id];
+      d[i] = sums[(int64_t)u * q.C + c];
     }
-  } else {
-    for (int u = w.chunks - 1; u >= 0; --u) {
-      const int r0 = u * len, r1 = min(r0 + len, q.rows.R);
-      const float e = w.adj[u * CN + id], d = w.sums[(int64_t)u * q.C + c];
-      w.adj[u * CN + id] = h;
-      const int s = seq_of(q.rows, r0);
-      const bool through = s >= 0 && seq_begin(q.rows, s) < r0 && seq_end(q.rows, s) > r1;
-      h = through ? fmaf(exp2_fast(A * d), h, e) : e;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int v = i0 + i, u = back ? w.chunks - 1 - v : v;
+      if (v < w.chunks) state[u * CN + id] = h;
+      h = d[i] == d[i] ? fmaf(exp2_fast(A * d[i]), h, e[i]) : e[i];
     }
   }
 }
@@ -275,14 +282,14 @@ __device__ __forceinline__ int merged_value() {
 }
 
 // ---- main ----------------------------------------------------------------------------------------
-template <typename IO, int K, bool GATE>
+template <typename IO, int K>
 __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, SelGrads o,
                                                              const IO* dy, const float* dfinal,
                                                              int tiles) {
   constexpr int T = kQuarter, TC = kChunk, NP = NPL * K, CH = kSelThreads / K;
   constexpr int MV = 64 / K;  // values of a merge
   __shared__ __attribute__((aligned(16))) float s_dl[TC][CH], s_du[TC][CH], s_e[TC][CH];
-  __shared__ float s_y[GATE ? TC : 1][CH];
+  __shared__ float s_y[TC][CH];
   __shared__ __attribute__((aligned(16))) float s_b[TC][NP], s_c[TC][NP];
   __shared__ float s_bc[kSelThreads / 64][T][2][NP];
   const Tile b(q, CH, blockIdx.x % tiles);
@@ -305,108 +312,116 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
 #pragma unroll
   for (int j = 0; j < NPL; ++j) A[j] *= kLog2e;
   __syncthreads();
-  // forward to the start of the last quarter
-#pragma unroll
-  for (int s = 0; s < 3; ++s) {
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) h[s + 1][j] = h[s][j];
-#pragma unroll 4
-    for (int i = 0; i < T; ++i) {
-      const int t = s * T + i;
-      if ((starts >> t) & 1) seq_states(q, q.h0, r0 + t, c, k, live, h[s + 1]);
-      const float dl = s_dl[t][ch], du = s_du[t][ch];
-#pragma unroll
-      for (int j = 0; j < NPL; ++j)
-        h[s + 1][j] = fmaf(exp2_fast(dl * A[j]), h[s + 1][j], du * s_b[t][k * NPL + j]);
-    }
-  }
   const int mine = merged_value<K>();
+  // events: a sequence begins or ends in the chunk. Where none does (`quiet`), no branch separates
+  // the tokens and the loads and products of several overlap.
+  auto walk = [&](auto quiet) {
+    constexpr bool EV = !decltype(quiet)::value;
+    // forward to the start of the last quarter
 #pragma unroll
-  for (int s = 3; s >= 0; --s) {
-    float hn[T][NPL], a[T][NPL];  // h after each token, its decay
+    for (int s = 0; s < 3; ++s) {
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-      const int t = s * T + i;
-      float prev[NPL];
+      for (int j = 0; j < NPL; ++j) h[s + 1][j] = h[s][j];
+#pragma unroll 8
+      for (int i = 0; i < T; ++i) {
+        const int t = s * T + i;
+        if (EV && ((starts >> t) & 1)) seq_states(q, q.h0, r0 + t, c, k, live, h[s + 1]);
+        const float dl = s_dl[t][ch], du = s_du[t][ch];
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
-      if ((starts >> t) & 1) seq_states(q, q.h0, r0 + t, c, k, live, prev);
-      const float dl = s_dl[t][ch], du = s_du[t][ch];
-      float y = 0.f;
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) {
-        a[i][j] = exp2_fast(dl * A[j]);
-        hn[i][j] = fmaf(a[i][j], prev[j], du * s_b[t][k * NPL + j]);
-        if (GATE) y = fmaf(hn[i][j], s_c[t][k * NPL + j], y);
+        for (int j = 0; j < NPL; ++j)
+          h[s + 1][j] = fmaf(exp2_fast(dl * A[j]), h[s + 1][j], du * s_b[t][k * NPL + j]);
       }
-      if (GATE) {
-        y = sum_lanes<K>(y);
-        if (k == t % K) s_y[t][ch] = y;
-      }
-      __builtin_amdgcn_sched_barrier(0);  // loads of later tokens would cost registers here
     }
-    float vals[MV < 8 ? 8 : MV];  // dB of the four entries, then dC; K 4: of two tokens
 #pragma unroll
-    for (int i = T - 1; i >= 0; --i) {
-      const int t = s * T + i;
-      if ((ends >> t) & 1) seq_states(q, dfinal, r0 + t, c, k, live, g);
-      float prev[NPL];
+    for (int s = 3; s >= 0; --s) {
+      float hn[T][NPL], a[T][NPL];  // h after each token, its decay
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
-      const bool start = (starts >> t) & 1;
-      if (start) seq_states(q, q.h0, r0 + t, c, k, live, prev);
-      const float dl = s_dl[t][ch], du = s_du[t][ch], e = s_e[t][ch];
-      float qs = 0.f, sa = 0.f;
+      for (int i = 0; i < T; ++i) {
+        const int t = s * T + i;
+        float prev[NPL];
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) {
-        const float G = fmaf(s_c[t][k * NPL + j], e, g[j]);
-        const float aG = a[i][j] * G, wv = aG * prev[j];
-        qs = fmaf(G, s_b[t][k * NPL + j], qs);
-        sa = fmaf(wv, A[j], sa);
-        dA[j] = fmaf(wv, dl, dA[j]);
-        g[j] = aG;
-        const int slot = K == 4 ? (i & 1) * 8 + j : j;
-        vals[slot] = G * du;
-        vals[slot + 4] = hn[i][j] * e;
-      }
-      if constexpr (K == 4) {
-        if ((i & 1) == 0)
-          s_bc[wave][i + (mine >> 3)][(mine >> 2) & 1][k * NPL + (mine & 3)] = merge<K>(vals);
-      } else if constexpr (K == 8) {
-        s_bc[wave][i][mine >> 2][k * NPL + (mine & 3)] = merge<K>(vals);
-      } else {
-        const float vb[4] = {vals[0], vals[1], vals[2], vals[3]};
-        const float vc[4] = {vals[4], vals[5], vals[6], vals[7]};
-        s_bc[wave][i][0][k * NPL + mine] = merge<K>(vb);
-        s_bc[wave][i][1][k * NPL + mine] = merge<K>(vc);
-      }
-      qs = sum_lanes<K>(qs);
-      sa = sum_lanes<K>(sa);
-      // this token's delta x and e have no further reader: q and sum w A take their places
-      if (k < 2) (k ? s_e : s_du)[t][ch] = k ? sa : qs;
-      if (start) {
-        if (o.dh0 && live) {
-          const int sq = seq_of(q.rows, r0 + t);
-          store_states<NPL>(o.dh0 + ((int64_t)sq * q.C + c) * q.N, k, q.N, g);
+        for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
+        if (EV && ((starts >> t) & 1)) seq_states(q, q.h0, r0 + t, c, k, live, prev);
+        const float dl = s_dl[t][ch], du = s_du[t][ch];
+        float y = 0.f;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+          a[i][j] = exp2_fast(dl * A[j]);
+          hn[i][j] = fmaf(a[i][j], prev[j], du * s_b[t][k * NPL + j]);
+          y = fmaf(hn[i][j], s_c[t][k * NPL + j], y);
         }
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) g[j] = 0.f;
+        // (without a gate y has no use, but leaving it out took more registers; the K lanes write
+        // the same value)
+        s_y[t][ch] = sum_lanes<K>(y);
+        if (EV || i % 4 == 3)
+          __builtin_amdgcn_sched_barrier(0);  // loads of later tokens would cost registers here
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    __syncthreads();
-    for (int v = threadIdx.x; v < T * 2 * NP; v += kSelThreads) {
-      const int i = v / (2 * NP), rest = v % (2 * NP), which = rest / NP, n = rest % NP;
-      const int row = r0 + s * T + i;
-      if (row < r1 && n < q.N) {
-        float m = s_bc[0][i][which][n];
+      asm volatile("" ::: "memory");  // and so would what was loaded above, kept for its reuse below
+      float vals[MV < 8 ? 8 : MV];  // dB of the four entries, then dC; K 4: of two tokens
 #pragma unroll
-        for (int x = 1; x < kSelThreads / 64; ++x) m += s_bc[x][i][which][n];
-        w.bc[(((int64_t)b.ct * q.rows.R + row) * 2 + which) * q.N + n] = m;
+      for (int i = T - 1; i >= 0; --i) {
+        const int t = s * T + i;
+        if (EV && ((ends >> t) & 1)) seq_states(q, dfinal, r0 + t, c, k, live, g);
+        float prev[NPL];
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
+        const bool start = EV && ((starts >> t) & 1);
+        if (start) seq_states(q, q.h0, r0 + t, c, k, live, prev);
+        const float dl = s_dl[t][ch], du = s_du[t][ch], e = s_e[t][ch];
+        float qs = 0.f, sa = 0.f;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+          const float G = fmaf(s_c[t][k * NPL + j], e, g[j]);
+          const float aG = a[i][j] * G, wv = aG * prev[j];
+          qs = fmaf(G, s_b[t][k * NPL + j], qs);
+          sa = fmaf(wv, A[j], sa);
+          dA[j] = fmaf(wv, dl, dA[j]);
+          g[j] = aG;
+          const int slot = K == 4 ? (i & 1) * 8 + j : j;
+          vals[slot] = G * du;
+          vals[slot + 4] = hn[i][j] * e;
+        }
+        if constexpr (K == 4) {
+          if ((i & 1) == 0)
+            s_bc[wave][i + (mine >> 3)][(mine >> 2) & 1][k * NPL + (mine & 3)] = merge<K>(vals);
+        } else if constexpr (K == 8) {
+          s_bc[wave][i][mine >> 2][k * NPL + (mine & 3)] = merge<K>(vals);
+        } else {
+          const float vb[4] = {vals[0], vals[1], vals[2], vals[3]};
+          const float vc[4] = {vals[4], vals[5], vals[6], vals[7]};
+          s_bc[wave][i][0][k * NPL + mine] = merge<K>(vb);
+          s_bc[wave][i][1][k * NPL + mine] = merge<K>(vc);
+        }
+        qs = sum_lanes<K>(qs);
+        sa = sum_lanes<K>(sa);
+        // this token's delta x and e have no further reader: q and sum w A take their places
+        (k & 1 ? s_e : s_du)[t][ch] = k & 1 ? sa : qs;
+        if (start) {
+          if (o.dh0 && live) {
+            const int sq = seq_of(q.rows, r0 + t);
+            store_states<NPL>(o.dh0 + ((int64_t)sq * q.C + c) * q.N, k, q.N, g);
+          }
+#pragma unroll
+          for (int j = 0; j < NPL; ++j) g[j] = 0.f;
+        }
+        if (EV || (i & 1) == 0) __builtin_amdgcn_sched_barrier(0);
       }
+      __syncthreads();
+      for (int v = threadIdx.x; v < T * 2 * NP; v += kSelThreads) {
+        const int i = v / (2 * NP), rest = v % (2 * NP), which = rest / NP, n = rest % NP;
+        const int row = r0 + s * T + i;
+        if (row < r1 && n < q.N) {
+          float m = s_bc[0][i][which][n];
+#pragma unroll
+          for (int x = 1; x < kSelThreads / 64; ++x) m += s_bc[x][i][which][n];
+          w.bc[(((int64_t)b.ct * q.rows.R + row) * 2 + which) * q.N + n] = m;
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
+  };
+  if (starts | ends) walk(std::false_type{});
+  else walk(std::true_type{});
   float* part = w.part + (int64_t)u * q.C * (q.N + 2);
   if (live) store_states<NPL>(part + (int64_t)c * q.N, k, q.N, dA);
   // outputs of the chunk: a thread takes 8 channels of every 32nd row; e x and ddt are summed over
@@ -429,13 +444,13 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
       xr.load((const IO*)q.x + row * q.xs + cc);
       tr.load((const IO*)q.dt + row * q.dts + cc);
       dr.load(dy + row * q.C + cc);
-      if (GATE) zr.load((const IO*)q.z + row * q.zs + cc);
+      if (q.z) zr.load((const IO*)q.z + row * q.zs + cc);
       float ox[V], ot[V], oz[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float x = xr.get(j), qv = s_du[t][cl + j], sa = s_e[t][cl + j] * 0.6931471805599453f;
         float e = dr.get(j);
-        if (GATE) {
+        if (q.z) {
           const float zv = zr.get(j), sg = sigmoid(zv);
           oz[j] = e * fmaf(D[j], x, s_y[t][cl + j]) * (sg * fmaf(zv, 1.f - sg, 1.f));
           e *= zv * sg;
@@ -449,7 +464,7 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
       }
       store_vec<IO, V>((IO*)o.dx + row * q.C + cc, ox);
       store_vec<IO, V>((IO*)o.ddt + row * q.C + cc, ot);
-      if (GATE) store_vec<IO, V>((IO*)o.dz + row * q.C + cc, oz);
+      if (q.z) store_vec<IO, V>((IO*)o.dz + row * q.C + cc, oz);
     }
   }
   __syncthreads();
@@ -514,7 +529,7 @@ int tiles_of(const SelArgs& a) {  // channel tiles of a group
 int64_t lay_out(const SelArgs& a, float* ws, Work* w) {
   w->chunks = (a.rows.R + kChunk - 1) / kChunk;
   const int64_t tiles = (int64_t)tiles_of(a) * a.G, n = w->chunks;
-  const int64_t st = round64(n * a.C * a.N), sm = round64(n * a.C);
+  const int64_t st = round64(n * a.C * a.N), sm = round64(2 * n * a.C);
   const int64_t bc = round64(tiles * a.rows.R * 2 * a.N), pt = round64(n * a.C * (a.N + 2));
   w->state = ws;
   w->adj = w->state + st;
@@ -545,12 +560,8 @@ hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const flo
       hipLaunchKernelGGL((k_bwd_ends<IO, K>), dim3(blocks), dim3(kSelThreads), 0, s, a, w,
                          (const IO*)dy, dfinal, tiles);
       hipLaunchKernelGGL(k_bwd_chain, dim3((unsigned)((CN + 255) / 256), 2), dim3(256), 0, s, a, w);
-      if (a.z)
-        hipLaunchKernelGGL((k_bwd_main<IO, K, true>), dim3(blocks), dim3(kSelThreads), 0, s, a,
-                           w, g, (const IO*)dy, dfinal, tiles);
-      else
-        hipLaunchKernelGGL((k_bwd_main<IO, K, false>), dim3(blocks), dim3(kSelThreads), 0, s, a,
-                           w, g, (const IO*)dy, dfinal, tiles);
+      hipLaunchKernelGGL((k_bwd_main<IO, K>), dim3(blocks), dim3(kSelThreads), 0, s, a, w, g,
+                         (const IO*)dy, dfinal, tiles);
       const int64_t n = (int64_t)a.rows.R * 2 * a.N * a.G;
       hipLaunchKernelGGL((k_bwd_bc<IO>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, w,
                          g, per_group);
