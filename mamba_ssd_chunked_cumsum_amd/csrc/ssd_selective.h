@@ -27,6 +27,66 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
+// ---- a channel a lane, all its states in registers -------------------------------------------------
+// B or C of a token: N state entries at p, uniform over the wave. NT: N rounded up to a template's
+// size; entries past N read the last ones again (never past the row) and are set to zero.
+template <typename IO, int NT, bool EXACT>
+struct Row {
+  static constexpr int kW = 4 * sizeof(IO) / 4;  // words of four entries
+  uint32_t u[NT / 4][kW];
+  __device__ __forceinline__ void load(const IO* p, int N) {
+    typedef const __attribute__((address_space(4))) uint32_t* Words;  // read through scalar loads
+#pragma unroll
+    for (int i = 0; i < NT / 4; ++i) {
+      const Words w = (Words)(uintptr_t)(p + (EXACT ? 4 * i : min(4 * i, N - 4)));
+#pragma unroll
+      for (int j = 0; j < kW; ++j) u[i][j] = w[j];
+      if (!EXACT && 4 * i >= N) {
+#pragma unroll
+        for (int j = 0; j < kW; ++j) u[i][j] = 0;
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int n) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(u[n / 4][n % 4]);
+    else return __uint_as_float(n & 1 ? u[n / 4][n % 4 / 2] & 0xffff0000u : u[n / 4][n % 4 / 2] << 16);
+  }
+};
+
+template <typename IO>
+__device__ __forceinline__ const char* row_at(const IO* p, int64_t elements) {
+  return (const char*)(p + elements);
+}
+
+// One value as loaded, in a register of its own (two 16-bit values in one would make the second
+// load wait for the first), and as a float.
+template <typename IO>
+__device__ __forceinline__ uint32_t load_raw(const char* row, unsigned off) {
+  if constexpr (sizeof(IO) == 4) return *(const uint32_t*)(row + off);
+  else return *(const u16*)(row + off);
+}
+template <typename IO>
+__device__ __forceinline__ float raw_value(uint32_t v) {
+  return __uint_as_float(sizeof(IO) == 4 ? v : v << 16);
+}
+
+template <int NT>
+__device__ __forceinline__ void load_all(const float* p, int N, float (&h)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; i += 4) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < N) v = *reinterpret_cast<const float4*>(p + i);
+    h[i] = v.x; h[i + 1] = v.y; h[i + 2] = v.z; h[i + 3] = v.w;
+  }
+}
+template <int NT>
+__device__ __forceinline__ void store_all(float* p, int N, const float (&h)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; i += 4)
+    if (i < N) *reinterpret_cast<float4*>(p + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+}
+
+// ---- K lanes a channel -----------------------------------------------------------------------------
 // Starts and ends of sequences among the rows [r, r + 64) of a wave, as bit masks; rows at or past
 // `stop` count as neither.
 __device__ __forceinline__ void mark_rows(const Rows& q, int r, int stop, uint64_t& starts,
@@ -63,6 +123,17 @@ __device__ __forceinline__ void store_states(float* p, int k, int N, const float
     const int n = k * NPL + j;
     if (n < N) *reinterpret_cast<float4*>(p + n) = make_float4(h[j], h[j + 1], h[j + 2], h[j + 3]);
   }
+}
+
+// Template sizes of a lane that holds all N states: f(size, whether N is that size).
+template <typename F>
+hipError_t by_size(int N, F f) {
+  using std::integral_constant;
+  if (N == 16) return f(integral_constant<int, 16>{}, std::true_type{});
+  if (N <= 8) return f(integral_constant<int, 8>{}, std::false_type{});
+  if (N <= 16) return f(integral_constant<int, 16>{}, std::false_type{});
+  if (N <= 32) return f(integral_constant<int, 32>{}, std::false_type{});
+  return f(integral_constant<int, 64>{}, std::false_type{});
 }
 
 // Lanes a channel, four states each, for dstate N.

@@ -34,52 +34,6 @@ struct Plan {
   float* sums;   // [chunks, C]: sums of delta; NaN where a sequence begins in the chunk
 };
 
-// B or C of a token: N state entries at p, uniform over the wave. NT: N rounded up to a template's
-// size; entries past N read the last ones again (never past the row) and are set to zero.
-template <typename IO, int NT, bool EXACT>
-struct Row {
-  static constexpr int kW = 4 * sizeof(IO) / 4;  // words of four entries
-  uint32_t u[NT / 4][kW];
-  __device__ __forceinline__ void load(const IO* p, int N) {
-    typedef const __attribute__((address_space(4))) uint32_t* Words;  // read through scalar loads
-#pragma unroll
-    for (int i = 0; i < NT / 4; ++i) {
-      const Words w = (Words)(uintptr_t)(p + (EXACT ? 4 * i : min(4 * i, N - 4)));
-#pragma unroll
-      for (int j = 0; j < kW; ++j) u[i][j] = w[j];
-      if (!EXACT && 4 * i >= N) {
-#pragma unroll
-        for (int j = 0; j < kW; ++j) u[i][j] = 0;
-      }
-    }
-  }
-  __device__ __forceinline__ float get(int n) const {
-    if constexpr (sizeof(IO) == 4) return __uint_as_float(u[n / 4][n % 4]);
-    else return __uint_as_float(n & 1 ? u[n / 4][n % 4 / 2] & 0xffff0000u : u[n / 4][n % 4 / 2] << 16);
-  }
-};
-
-template <typename IO>
-__device__ __forceinline__ const char* row_at(const IO* p, int64_t elements) {
-  return (const char*)(p + elements);
-}
-
-template <int NT>
-__device__ __forceinline__ void load_all(const float* p, int N, float (&h)[NT]) {
-#pragma unroll
-  for (int i = 0; i < NT; i += 4) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < N) v = *reinterpret_cast<const float4*>(p + i);
-    h[i] = v.x; h[i + 1] = v.y; h[i + 2] = v.z; h[i + 3] = v.w;
-  }
-}
-template <int NT>
-__device__ __forceinline__ void store_all(float* p, int N, const float (&h)[NT]) {
-#pragma unroll
-  for (int i = 0; i < NT; i += 4)
-    if (i < N) *reinterpret_cast<float4*>(p + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
-}
-
 // STATES: only the end state and sum of delta of each chunk.
 template <typename IO, int NT, bool EXACT, bool STATES>
 __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int units,
@@ -134,9 +88,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
   const unsigned off = (unsigned)c * sizeof(IO);
   const IO *B = (const IO*)q.B + g * q.N, *C = (const IO*)q.Cm + g * q.N;
   bool began = false;
-  struct Token {
-    IO x, dt, z;
-  };
+  const void* zp = q.z ? q.z : q.x;  // (without a gate the values read are not used)
+  const int64_t zs = q.z ? q.zs : q.xs;
   for (int r = r0; r < r1;) {  // sequence by sequence
     const int s = seq_of(q.rows, r);
     if (s < 0) {
@@ -152,20 +105,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
     }
     // rows that are read next: a row's address is scalar, the channel the lane's offset
     const char *px = row_at((const IO*)q.x, r * q.xs), *pt = row_at((const IO*)q.dt, r * q.dts),
-               *pz = row_at((const IO*)q.z, r * q.zs), *pb = row_at(B, r * q.bs), *pc = row_at(C, r * q.cs);
-    int ahead = r, ahead_bc = r;  // their indices, held at the last row of the sequence
-    auto fetch = [&] {
-      Token k;
-      k.x = *(const IO*)(px + off);
-      k.dt = *(const IO*)(pt + off);
-      if (!STATES && q.z) k.z = *(const IO*)(pz + off);
-      if (++ahead < b) {
-        px += q.xs * sizeof(IO);
-        pt += q.dts * sizeof(IO);
-        if (!STATES) pz += q.zs * sizeof(IO);
-      }
-      return k;
-    };
+               *pz = row_at((const IO*)zp, r * zs), *pb = row_at(B, r * q.bs),
+               *pc = row_at(C, r * q.cs);
+    int ahead = r, ahead_bc = r;  // their indices, held at the last row of the run
     struct Rows2 {
       Row<IO, NT, EXACT> B, C;
     };
@@ -179,61 +121,83 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
       }
       return w;
     };
-    auto token = [&](int t, const Token& k, const Rows2& w) {
-      const float xv = Io<IO>::load(&k.x, 0);
-      float dl = Io<IO>::load(&k.dt, 0) + bias;
-      if (q.softplus) dl = softplus(dl);
-      const float du = dl * xv;
-      float acc[2] = {0.f, 0.f};
-      if (STATES) sum += dl;
-      // in groups of GR state entries, so that no instruction waits for the one before it
-#pragma unroll
-      for (int n = 0; n < NT; n += GR) {
-        float a[GR], v[GR];
-#pragma unroll
-        for (int j = 0; j < GR; ++j) a[j] = dl * A[n + j];
-#pragma unroll
-        for (int j = 0; j < GR; ++j) a[j] = exp2_fast(a[j]);
-#pragma unroll
-        for (int j = 0; j < GR; ++j) v[j] = du * w.B.get(n + j);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < GR; ++j) h[n + j] = fmaf(a[j], h[n + j], v[j]);
-        if (!STATES) {
-#pragma unroll
-          for (int j = 0; j < GR; ++j) acc[j & 1] = fmaf(h[n + j], w.C.get(n + j), acc[j & 1]);
-        }
-      }
-      if (!STATES) {
-        float o = fmaf(D, xv, acc[0] + acc[1]);
-        if (q.z) {
-          const float zv = Io<IO>::load(&k.z, 0);
-          o *= zv * sigmoid(zv);
-        }
-        // (idle lanes write the last channel's value once more)
-        store_io((IO*)((char*)(y + (int64_t)t * q.C) + off), 0, o);
-      }
-    };
-    Token cur[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) cur[i] = fetch();
-    Rows2 w = rows();
-    for (; r + U <= b; r += U) {
+    uint32_t rx[U], rt[U], rz[U];
+    auto fetch = [&] {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
+        rx[i] = load_raw<IO>(px, off);
+        rt[i] = load_raw<IO>(pt, off);
+        if (!STATES) rz[i] = load_raw<IO>(pz, off);
+        if (++ahead < b) {
+          px += q.xs * sizeof(IO);
+          pt += q.dts * sizeof(IO);
+          if (!STATES) pz += zs * sizeof(IO);
+        }
+      }
+    };
+    fetch();
+    Rows2 w = rows();
+#pragma unroll 1
+    for (; r < b; r += U) {
+      float x[U], dl[U], gate[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        x[i] = raw_value<IO>(rx[i]);
+        dl[i] = raw_value<IO>(rt[i]) + bias;
+        if (!STATES) gate[i] = raw_value<IO>(rz[i]);
+      }
+      fetch();
+      if (q.softplus) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) dl[i] = softplus(dl[i]);
+      }
+      if (!STATES) {
+        if (q.z) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) gate[i] *= sigmoid(gate[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < U; ++i) gate[i] = 1.f;
+        }
+      }
+      auto token = [&](int i) {
         const Rows2 wn = rows();  // a token ahead
-        const Token k = cur[i];
-        cur[i] = fetch();
-        token(r + i, k, w);
+        const float du = dl[i] * x[i];
+        float acc[2] = {0.f, 0.f};
+        if (STATES) sum += dl[i];
+        // in groups of GR state entries, so that no instruction waits for the one before it
+#pragma unroll
+        for (int n = 0; n < NT; n += GR) {
+          float a[GR], v[GR];
+#pragma unroll
+          for (int j = 0; j < GR; ++j) a[j] = dl[i] * A[n + j];
+#pragma unroll
+          for (int j = 0; j < GR; ++j) a[j] = exp2_fast(a[j]);
+#pragma unroll
+          for (int j = 0; j < GR; ++j) v[j] = du * w.B.get(n + j);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < GR; ++j) h[n + j] = fmaf(a[j], h[n + j], v[j]);
+          if (!STATES) {
+#pragma unroll
+            for (int j = 0; j < GR; ++j) acc[j & 1] = fmaf(h[n + j], w.C.get(n + j), acc[j & 1]);
+          }
+        }
         w = wn;
+        // (idle lanes write the last channel's value once more)
+        if (!STATES)
+          store_io((IO*)((char*)(y + (int64_t)(r + i) * q.C) + off), 0,
+                   fmaf(D, x[i], acc[0] + acc[1]) * gate[i]);
+      };
+      if (r + U <= b) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) token(i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < U - 1; ++i)
+          if (r + i < b) token(i);
       }
     }
-#pragma unroll
-    for (int i = 0; i < U - 1; ++i)
-      if (r + i < b) {
-        token(r + i, cur[i], w);
-        w = rows();
-      }
     r = b;
     if (!STATES && fin && b == end && live)
       store_all<NT>(fin + ((int64_t)s * q.C + c) * q.N, q.N, h);
@@ -380,12 +344,7 @@ hipError_t launch_selective(const SelArgs& a, void* y, float* fin, float* ws, in
     return hipGetLastError();
   };
   auto sizes = [&](auto io) {
-    using std::integral_constant;
-    if (a.N == 16) return run(io, integral_constant<int, 16>{}, std::true_type{});
-    if (a.N <= 8) return run(io, integral_constant<int, 8>{}, std::false_type{});
-    if (a.N <= 16) return run(io, integral_constant<int, 16>{}, std::false_type{});
-    if (a.N <= 32) return run(io, integral_constant<int, 32>{}, std::false_type{});
-    return run(io, integral_constant<int, 64>{}, std::false_type{});
+    return by_size(a.N, [&](auto size, auto exact) { return run(io, size, exact); });
   };
   return a.io == kIoBf16 ? sizes(u16{}) : sizes(float{});
 }

@@ -30,10 +30,13 @@ constexpr int NPL = 4, kQuarter = 16, kChunk = 4 * kQuarter;
 
 struct Work {
   int chunks;
-  float *state, *adj;  // [chunks, C, N]: end states, entering gradients; then the chained ones
-  float *sums;         // [2, chunks, C]: sums of delta, for either direction
-  float *bc;           // [tiles, R, 2, N]: dB and dC over a block's channels
-  float *part;         // [chunks, C N + 2 C]: dA, dD, ddt_bias of a chunk
+  float* state;  // [chunks, 4, C, N]: states after each quarter from a zero state at the chunk's
+                 // start; the last, chained, becomes the state entering the chunk
+  float* adj;    // [chunks, C, N]: gradients of the entering states; then those from later chunks
+  float* sums;   // [chunks, 4, C]: sums of delta up to there, NaN where the entering state has no part
+  float* back;   // [chunks, C]: the whole chunk's, NaN where no gradient passes
+  float* bc;     // [tiles, R, 2, N]: dB and dC over a block's channels
+  float* part;   // [chunks, C N + 2 C]: dA, dD, ddt_bias of a chunk
 };
 
 struct Tile {  // the channels of a block
@@ -116,73 +119,151 @@ __device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int
 }
 
 // ---- chunk ends ----------------------------------------------------------------------------------
-template <typename IO, int K>
-__global__ __launch_bounds__(kSelThreads) void k_bwd_ends(SelArgs q, Work w, const IO* dy,
-                                                          const float* dfinal, int tiles) {
-  constexpr int T = 32, NP = NPL * K, CH = kSelThreads / K;
-  __shared__ __attribute__((aligned(16))) float s_dl[T][CH], s_du[T][CH], s_e[T][CH];
-  __shared__ __attribute__((aligned(16))) float s_b[T][NP], s_c[T][NP];
-  const Tile b(q, CH, blockIdx.x % tiles);
-  const int u = blockIdx.x / tiles, k = threadIdx.x % K, ch = threadIdx.x / K, c = b.base + ch;
-  const bool live = c < b.stop;
+// As the forward's chunk states: a lane holds a channel, B and C come through scalar loads. NT: up to
+// 16 states; of more, other waves take the others.
+// EVENTS: the chunks in which a sequence begins after the first row or ends before the last; the
+// others take a launch of their own, whose waves need fewer registers (126 against 155: four of them
+// on a SIMD against three).
+template <typename IO, int NT, bool EXACT, bool EVENTS>
+__global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* dy,
+                                                  const float* dfinal) {
+  constexpr int U = 4;  // tokens whose loads are in flight
+  const int cg = q.C / q.G, tiles = (cg + 63) / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+  const int parts = (q.N + NT - 1) / NT, n0 = (int)(id % parts) * NT, N = min(NT, q.N - n0);
+  const int ct = (int)(id / parts % (tiles * q.G)), u = (int)(id / parts / (tiles * q.G));
+  if (u >= w.chunks) return;
+  const int g = ct / tiles, c0 = g * cg + ct % tiles * 64, c1 = (g + 1) * cg;
+  const bool live = c0 + (threadIdx.x & 63) < c1;
+  const int c = live ? c0 + (threadIdx.x & 63) : c1 - 1;  // idle lanes compute the last one again
+  const unsigned off = (unsigned)c * sizeof(IO);
   const int r0 = u * kChunk, r1 = min(r0 + kChunk, q.rows.R);
-  float A[NPL], h[NPL], p[NPL], gl[NPL], sum = 0.f;
+  const int s0 = seq_of(q.rows, r0);
+  const bool quiet = r1 - r0 == kChunk && s0 >= 0 && seq_end(q.rows, s0) >= r1;
+  if (quiet == EVENTS) return;
+  const int64_t CN = (int64_t)q.C * q.N, at = (int64_t)c * q.N + n0;
+  float A[NT], h[NT], p[NT], gl[NT], sum = 0.f;
+  load_all<NT>(q.A + at, N, A);
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    A[j] = h[j] = gl[j] = 0.f;
-    p[j] = 1.f;
+  for (int n = 0; n < NT; ++n) {
+    A[n] *= kLog2e;
+    h[n] = gl[n] = 0.f;
+    p[n] = 1.f;
   }
-  if (live) load_states<NPL>(q.A + (int64_t)c * q.N, k, q.N, A);
+  const float bias = q.dt_bias ? q.dt_bias[c] : 0.f, none = __builtin_nanf("");
+  const IO *B = (const IO*)q.B + g * q.N + n0, *C = (const IO*)q.Cm + g * q.N + n0;
+  const void* zp = q.z ? q.z : q.x;  // (without a gate the values read are not used)
+  const int64_t zs = q.z ? q.zs : q.xs;
+  uint32_t rx[U], rt[U], ry[U], rz[U];
+  auto fetch = [&](int t, int i) {
+    rx[i] = load_raw<IO>(row_at((const IO*)q.x, t * q.xs), off);
+    rt[i] = load_raw<IO>(row_at((const IO*)q.dt, t * q.dts), off);
+    ry[i] = load_raw<IO>(row_at(dy, (int64_t)t * q.C), off);
+    rz[i] = load_raw<IO>(row_at((const IO*)zp, t * zs), off);
+  };
+  float x[U], dl[U], e[U];
+  auto unpack = [&] {
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) A[j] *= kLog2e;
-  for (int r = r0; r < r1; r += T) {
-    uint64_t starts, ends, inside;
-    mark_rows(q.rows, r, min(r + T, r1), starts, ends, inside);
-    __syncthreads();
-    stage<IO, T, CH, NP>(q, dy, b, r, r1, inside, s_dl, s_du, s_e, s_b, s_c);
-    __syncthreads();
-#pragma unroll 4
-    for (int t = 0; t < T; ++t) {
-      if ((starts >> t) & 1) {  // what came before belongs to another sequence
-        seq_states(q, q.h0, r + t, c, k, live, h);
-        sum = 0.f;
+    for (int i = 0; i < U; ++i) {
+      x[i] = raw_value<IO>(rx[i]);
+      dl[i] = raw_value<IO>(rt[i]) + bias;
+      e[i] = raw_value<IO>(ry[i]);
+    }
+    if (q.softplus) {
 #pragma unroll
-        for (int j = 0; j < NPL; ++j) p[j] = 0.f;
-      }
-      const float dl = s_dl[t][ch], du = s_du[t][ch], e = s_e[t][ch];
-      sum += dl;
+      for (int i = 0; i < U; ++i) dl[i] = softplus(dl[i]);
+    }
+    if (q.z) {
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) {
-        const float a = exp2_fast(dl * A[j]);
-        h[j] = fmaf(a, h[j], du * s_b[t][k * NPL + j]);
-        p[j] *= a;
-        gl[j] = fmaf(p[j], e * s_c[t][k * NPL + j], gl[j]);
-      }
-      if ((ends >> t) & 1) {
-        if (dfinal) {
-          float d[NPL];
-          seq_states(q, dfinal, r + t, c, k, live, d);
-#pragma unroll
-          for (int j = 0; j < NPL; ++j) gl[j] = fmaf(p[j], d[j], gl[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) p[j] = 0.f;
+      for (int i = 0; i < U; ++i) {
+        const float zv = raw_value<IO>(rz[i]);
+        e[i] *= zv * sigmoid(zv);
       }
     }
+  };
+  auto token = [&](int t, int i) {
+    Row<IO, NT, EXACT> Bt, Ct;
+    Bt.load(B + t * q.bs, N);
+    Ct.load(C + t * q.cs, N);
+    const float du = dl[i] * x[i];
+    sum += dl[i];
+    constexpr int GR = 8;
+#pragma unroll
+    for (int n = 0; n < NT; n += GR) {
+      float a[GR], v[GR];
+#pragma unroll
+      for (int j = 0; j < GR; ++j) a[j] = dl[i] * A[n + j];
+#pragma unroll
+      for (int j = 0; j < GR; ++j) a[j] = exp2_fast(a[j]);
+#pragma unroll
+      for (int j = 0; j < GR; ++j) v[j] = du * Bt.get(n + j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < GR; ++j) {
+        h[n + j] = fmaf(a[j], h[n + j], v[j]);
+        p[n + j] *= a[j];
+        gl[n + j] = fmaf(p[n + j], e[i] * Ct.get(n + j), gl[n + j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // (registers)
+    }
+  };
+  bool began = false;
+  auto begin = [&](int s) {  // what came before belongs to another sequence
+    began = true;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) h[n] = p[n] = 0.f;
+    if (q.h0) load_all<NT>(q.h0 + (int64_t)s * CN + at, N, h);
+  };
+  auto finish = [&](int s) {
+    if (dfinal) {
+      float d[NT];
+      load_all<NT>(dfinal + (int64_t)s * CN + at, N, d);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) gl[n] = fmaf(p[n], d[n], gl[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) p[n] = 0.f;
+  };
+  auto write_quarter = [&](int i) {
+    if (!live) return;
+    const int64_t slot = (int64_t)u * 4 + i;
+    store_all<NT>(w.state + slot * CN + at, N, h);
+    if (n0 == 0) w.sums[slot * q.C + c] = began ? none : sum;
+  };
+  uint64_t starts = 0, ends = 0, inside = ~uint64_t(0);
+  if (EVENTS) mark_rows(q.rows, r0, r1, starts, ends, inside);
+  else if (seq_begin(q.rows, s0) == r0) begin(s0);
+#pragma unroll
+  for (int i = 0; i < U; ++i) fetch(min(r0 + i, r1 - 1), i);
+#pragma unroll 1
+  for (int t = 0; t < kChunk; t += U) {
+    if (t && t % kQuarter == 0) write_quarter(t / kQuarter - 1);
+    unpack();
+#pragma unroll
+    for (int i = 0; i < U; ++i) fetch(min(r0 + t + U + i, r1 - 1), i);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (EVENTS) {
+        if (!((inside >> (t + i)) & 1)) dl[i] = x[i] = e[i] = 0.f;  // decays nothing, adds nothing
+        if ((starts >> (t + i)) & 1) begin(seq_of(q.rows, r0 + t + i));
+      }
+      token(min(r0 + t + i, r1 - 1), i);
+      if (EVENTS && ((ends >> (t + i)) & 1)) finish(seq_of(q.rows, r0 + t + i));
+    }
   }
+  if (!EVENTS && seq_end(q.rows, s0) == r1) finish(s0);
   if (live) {
-    const int64_t at = ((int64_t)u * q.C + c) * q.N;
-    store_states<NPL>(w.state + at, k, q.N, h);
-    store_states<NPL>(w.adj + at, k, q.N, gl);
-    if (k == 0) {
-      // what passes: the state through rows of one sequence that began before the chunk, its
-      // gradient if that sequence also goes on behind it
-      const int s = seq_of(q.rows, r1 - 1);
-      const bool fwd = s >= 0 && seq_begin(q.rows, s) < r0;
-      const bool bwd = fwd && seq_end(q.rows, s) > r1;
-      const float none = __builtin_nanf("");
-      w.sums[(int64_t)u * q.C + c] = fwd ? sum : none;
-      w.sums[((int64_t)w.chunks + u) * q.C + c] = bwd ? sum : none;
+    store_all<NT>(w.state + ((int64_t)u * 4 + 3) * CN + at, N, h);
+    store_all<NT>(w.adj + (int64_t)u * CN + at, N, gl);
+    // what passes: the state through rows of one sequence that began before the chunk, its gradient
+    // if that sequence also goes on behind it
+    const int s = seq_of(q.rows, r1 - 1);
+    const bool fwd = s >= 0 && seq_begin(q.rows, s) < r0;
+    const bool bwd = fwd && seq_end(q.rows, s) > r1;
+    if (n0 == 0) {
+      w.sums[((int64_t)u * 4 + 3) * q.C + c] = fwd ? sum : none;
+      w.back[(int64_t)u * q.C + c] = bwd ? sum : none;
     }
   }
 }
@@ -197,21 +278,23 @@ __global__ __launch_bounds__(256) void k_bwd_chain(SelArgs q, Work w) {
   if (id >= CN) return;
   const int c = (int)(id / q.N), back = blockIdx.y;
   const float A = q.A[id] * kLog2e;
-  const float* sums = w.sums + (back ? (int64_t)w.chunks * q.C : 0);
-  float* state = back ? w.adj : w.state;
+  // (states and sums of a chunk's last quarter)
+  const int64_t step = back ? 1 : 4;
+  const float* sums = back ? w.back : w.sums + 3 * q.C;
+  float* state = back ? w.adj : w.state + 3 * CN;
   float h = 0.f;
   for (int i0 = 0; i0 < w.chunks; i0 += kAhead) {
     float e[kAhead], d[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int v = min(i0 + i, w.chunks - 1), u = back ? w.chunks - 1 - v : v;
-      e[i] = state[u * CN + id];
-      d[i] = sums[(int64_t)u * q.C + c];
+      e[i] = state[u * step * CN + id];
+      d[i] = sums[u * step * q.C + c];
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int v = i0 + i, u = back ? w.chunks - 1 - v : v;
-      if (v < w.chunks) state[u * CN + id] = h;
+      if (v < w.chunks) state[u * step * CN + id] = h;
       h = d[i] == d[i] ? fmaf(exp2_fast(A * d[i]), h, e[i]) : e[i];
     }
   }
@@ -289,7 +372,7 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
   constexpr int T = kQuarter, TC = kChunk, NP = NPL * K, CH = kSelThreads / K;
   constexpr int MV = 64 / K;  // values of a merge
   __shared__ __attribute__((aligned(16))) float s_dl[TC][CH], s_du[TC][CH], s_e[TC][CH];
-  __shared__ float s_y[TC][CH];
+  __shared__ __attribute__((aligned(16))) float s_y[TC][CH];
   __shared__ __attribute__((aligned(16))) float s_b[TC][NP], s_c[TC][NP];
   __shared__ float s_bc[kSelThreads / 64][T][2][NP];
   const Tile b(q, CH, blockIdx.x % tiles);
@@ -302,36 +385,31 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
   stage<IO, TC, CH, NP>(q, dy, b, r0, r1, inside, s_dl, s_du, s_e, s_b, s_c);
   float A[NPL], h[4][NPL], g[NPL], dA[NPL];
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) A[j] = h[0][j] = g[j] = dA[j] = 0.f;
-  const int64_t at = ((int64_t)u * q.C + c) * q.N;
+  for (int j = 0; j < NPL; ++j) A[j] = h[0][j] = h[1][j] = h[2][j] = h[3][j] = g[j] = dA[j] = 0.f;
+  const int64_t CN = (int64_t)q.C * q.N, at = (int64_t)c * q.N;
   if (live) {
-    load_states<NPL>(q.A + (int64_t)c * q.N, k, q.N, A);
-    load_states<NPL>(w.state + at, k, q.N, h[0]);
-    load_states<NPL>(w.adj + at, k, q.N, g);
+    load_states<NPL>(q.A + at, k, q.N, A);
+    load_states<NPL>(w.state + ((int64_t)u * 4 + 3) * CN + at, k, q.N, h[0]);
+    load_states<NPL>(w.adj + (int64_t)u * CN + at, k, q.N, g);
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+      load_states<NPL>(w.state + ((int64_t)u * 4 + s) * CN + at, k, q.N, h[s + 1]);
   }
 #pragma unroll
   for (int j = 0; j < NPL; ++j) A[j] *= kLog2e;
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {  // the entering state's part in the quarters'
+    const float d = live ? w.sums[((int64_t)u * 4 + s) * q.C + c] : 0.f;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j)
+      h[s + 1][j] = d == d ? fmaf(exp2_fast(d * A[j]), h[0][j], h[s + 1][j]) : h[s + 1][j];
+  }
   __syncthreads();
   const int mine = merged_value<K>();
   // events: a sequence begins or ends in the chunk. Where none does (`quiet`), no branch separates
   // the tokens and the loads and products of several overlap.
   auto walk = [&](auto quiet) {
     constexpr bool EV = !decltype(quiet)::value;
-    // forward to the start of the last quarter
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-#pragma unroll
-      for (int j = 0; j < NPL; ++j) h[s + 1][j] = h[s][j];
-#pragma unroll 8
-      for (int i = 0; i < T; ++i) {
-        const int t = s * T + i;
-        if (EV && ((starts >> t) & 1)) seq_states(q, q.h0, r0 + t, c, k, live, h[s + 1]);
-        const float dl = s_dl[t][ch], du = s_du[t][ch];
-#pragma unroll
-        for (int j = 0; j < NPL; ++j)
-          h[s + 1][j] = fmaf(exp2_fast(dl * A[j]), h[s + 1][j], du * s_b[t][k * NPL + j]);
-      }
-    }
 #pragma unroll
     for (int s = 3; s >= 0; --s) {
       float hn[T][NPL], a[T][NPL];  // h after each token, its decay
@@ -445,17 +523,21 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
       tr.load((const IO*)q.dt + row * q.dts + cc);
       dr.load(dy + row * q.C + cc);
       if (q.z) zr.load((const IO*)q.z + row * q.zs + cc);
-      float ox[V], ot[V], oz[V];
+      float ox[V], ot[V], oz[V], vq[V], va[V], vy[V], vd[V];
+      load_f32<V>(&s_du[t][cl], vq);
+      load_f32<V>(&s_e[t][cl], va);
+      load_f32<V>(&s_y[t][cl], vy);
+      load_f32<V>(&s_dl[t][cl], vd);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float x = xr.get(j), qv = s_du[t][cl + j], sa = s_e[t][cl + j] * 0.6931471805599453f;
+        const float x = xr.get(j), qv = vq[j], sa = va[j] * 0.6931471805599453f;
         float e = dr.get(j);
         if (q.z) {
           const float zv = zr.get(j), sg = sigmoid(zv);
-          oz[j] = e * fmaf(D[j], x, s_y[t][cl + j]) * (sg * fmaf(zv, 1.f - sg, 1.f));
+          oz[j] = e * fmaf(D[j], x, vy[j]) * (sg * fmaf(zv, 1.f - sg, 1.f));
           e *= zv * sg;
         }
-        ox[j] = fmaf(s_dl[t][cl + j], qv, D[j] * e);
+        ox[j] = fmaf(vd[j], qv, D[j] * e);
         float dd = fmaf(x, qv, sa);
         if (q.softplus) dd *= sigmoid(tr.get(j) + bias[j]);
         ot[j] = dd;
@@ -529,14 +611,15 @@ int tiles_of(const SelArgs& a) {  // channel tiles of a group
 int64_t lay_out(const SelArgs& a, float* ws, Work* w) {
   w->chunks = (a.rows.R + kChunk - 1) / kChunk;
   const int64_t tiles = (int64_t)tiles_of(a) * a.G, n = w->chunks;
-  const int64_t st = round64(n * a.C * a.N), sm = round64(2 * n * a.C);
+  const int64_t st = round64(n * a.C * a.N), sm = round64(n * a.C);
   const int64_t bc = round64(tiles * a.rows.R * 2 * a.N), pt = round64(n * a.C * (a.N + 2));
   w->state = ws;
-  w->adj = w->state + st;
+  w->adj = w->state + 4 * st;
   w->sums = w->adj + st;
-  w->bc = w->sums + sm;
+  w->back = w->sums + 4 * sm;
+  w->bc = w->back + sm;
   w->part = w->bc + bc;
-  return 2 * st + sm + bc + pt;
+  return 5 * (st + sm) + bc + pt;
 }
 
 }  // namespace
@@ -550,25 +633,42 @@ hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const flo
                                      const SelGrads& g, float* ws, hipStream_t s) {
   Work w;
   lay_out(a, ws, &w);
-  const int per_group = tiles_of(a), tiles = per_group * a.G;
+  const int cg = a.C / a.G, per_group = tiles_of(a), tiles = per_group * a.G;
   const unsigned blocks = (unsigned)((int64_t)tiles * w.chunks);
   const int64_t CN = (int64_t)a.C * a.N;
-  const hipError_t e = by_states(a.N, [&](auto lanes) {
-    constexpr int K = decltype(lanes)::value;
-    auto run = [&](auto io) {
-      using IO = decltype(io);
-      hipLaunchKernelGGL((k_bwd_ends<IO, K>), dim3(blocks), dim3(kSelThreads), 0, s, a, w,
-                         (const IO*)dy, dfinal, tiles);
-      hipLaunchKernelGGL(k_bwd_chain, dim3((unsigned)((CN + 255) / 256), 2), dim3(256), 0, s, a, w);
-      hipLaunchKernelGGL((k_bwd_main<IO, K>), dim3(blocks), dim3(kSelThreads), 0, s, a, w, g,
-                         (const IO*)dy, dfinal, tiles);
-      const int64_t n = (int64_t)a.rows.R * 2 * a.N * a.G;
-      hipLaunchKernelGGL((k_bwd_bc<IO>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, w,
-                         g, per_group);
+  auto run = [&](auto io) {
+    using IO = decltype(io);
+    auto ends = [&](auto size, auto exact) {
+      constexpr int NT = decltype(size)::value;
+      const int64_t waves = (int64_t)((cg + 63) / 64) * a.G * w.chunks * ((a.N + NT - 1) / NT);
+      constexpr bool EX = decltype(exact)::value;
+      const dim3 grid((unsigned)((waves + 3) / 4));
+      if (a.rows.starts || a.rows.L >= kChunk)
+        hipLaunchKernelGGL((k_bwd_ends<IO, NT, EX, false>), grid, dim3(256), 0, s, a, w,
+                           (const IO*)dy, dfinal);
+      if (a.rows.starts || a.rows.L % kChunk)
+        hipLaunchKernelGGL((k_bwd_ends<IO, NT, EX, true>), grid, dim3(256), 0, s, a, w,
+                           (const IO*)dy, dfinal);
       return hipGetLastError();
     };
-    return a.io == kIoBf16 ? run(u16{}) : run(float{});
-  });
+    using std::integral_constant;
+    hipError_t e = a.N % 16 == 0 ? ends(integral_constant<int, 16>{}, std::true_type{})
+                   : a.N <= 8    ? ends(integral_constant<int, 8>{}, std::false_type{})
+                                 : ends(integral_constant<int, 16>{}, std::false_type{});
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_bwd_chain, dim3((unsigned)((CN + 255) / 256), 2), dim3(256), 0, s, a, w);
+    e = by_states(a.N, [&](auto lanes) {
+      hipLaunchKernelGGL((k_bwd_main<IO, decltype(lanes)::value>), dim3(blocks), dim3(kSelThreads),
+                         0, s, a, w, g, (const IO*)dy, dfinal, tiles);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    const int64_t n = (int64_t)a.rows.R * 2 * a.N * a.G;
+    hipLaunchKernelGGL((k_bwd_bc<IO>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, w, g,
+                       per_group);
+    return hipGetLastError();
+  };
+  const hipError_t e = a.io == kIoBf16 ? run(u16{}) : run(float{});
   if (e != hipSuccess) return e;
   if (g.dh0 && a.rows.starts) {
     hipLaunchKernelGGL(k_bwd_empty, dim3((unsigned)((CN * a.rows.S + 255) / 256)), dim3(256), 0, s,
