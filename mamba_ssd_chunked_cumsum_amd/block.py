@@ -157,15 +157,22 @@ def _tokens(x, cu_seqlens=None):
     return SSDTokens(1, L, C, S, p, _io(x), 0), S
 
 
+def _stream(dev):
+    """The current stream's handle (torch.cuda.current_stream builds an object for it, which costs
+    more than the rest of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _run(name, dev, *args):
     """Calls an entry point on the current stream of `dev`, as that device's own call."""
-    f = _function(name)
+    f = _functions.get(name) or _function(name)
     if torch.cuda.current_device() == dev.index:
-        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        status = f(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(status, name)
+            status = f(*args, _stream(dev))
+    if status:
+        _check(status, name)
 
 
 def _workspace(name, dev, *args):
@@ -181,8 +188,9 @@ def _workspace(name, dev, *args):
     return ws, (None if ws is None else ws.data_ptr()), n.value
 
 
-def _or(t, shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+def _or(t, like, shape, dtype=None):
+    """The given output, or a new one of `like`'s device (and type, unless given)."""
+    return like.new_empty(shape, dtype=dtype) if t is None else t
 
 
 # ---- short causal convolution ------------------------------------------------------------------
@@ -200,9 +208,9 @@ def _parts(ts, name, sizes, lead, dtype, dev):
     return _Ptr3(*ptrs), _Split3(*sizes)
 
 
-def _outputs(out, split, sizes, lead, dtype, dev):
+def _outputs(out, split, sizes, lead, x):
     if out is None:
-        return tuple(torch.empty((*lead, n), dtype=dtype, device=dev) for n in sizes)
+        return tuple([x.new_empty((*lead, n)) for n in sizes])
     out = (out,) if split is None else tuple(out)
     if len(out) != len(sizes):
         raise ValueError(f"out must hold {len(sizes)} tensors")
@@ -238,9 +246,9 @@ def conv(x, weight, bias=None, initial_state=None, *, activation="silu", split=N
     W, w, b = _conv_params(weight, bias, C, dev)
     h0 = _tensor(initial_state, "initial_state", (S, W - 1, C), x.dtype, dev)
     sizes = _split_sizes(split, C)
-    ys = _outputs(out, split, sizes, (Bt, L), x.dtype, dev)
+    ys = _outputs(out, split, sizes, (Bt, L), x)
     yp, sp = _parts(ys, "out", sizes, (Bt, L), x.dtype, dev)
-    fin = _or(final_out, (S, W - 1, C), x.dtype, dev) if want_final else None
+    fin = _or(final_out, x, (S, W - 1, C)) if want_final else None
     fp = _tensor(fin, "final_out", (S, W - 1, C), x.dtype, dev)
     _run("ssd_conv", dev, ctypes.byref(tok), xp, xs, w, b, W, _silu(activation), h0, yp, sp, fp)
     return (ys[0] if split is None else ys), fin
@@ -257,9 +265,9 @@ def conv_step(state, x, weight, bias=None, *, activation="silu", split=None, out
     W, w, b = _conv_params(weight, bias, C, dev)
     sp_in = _tensor(state, "state", (Bt, W - 1, C), x.dtype, dev)
     sizes = _split_sizes(split, C)
-    ys = _outputs(out, split, sizes, (Bt,), x.dtype, dev)
+    ys = _outputs(out, split, sizes, (Bt,), x)
     yp, sp = _parts(ys, "out", sizes, (Bt,), x.dtype, dev)
-    so = _or(out_state, (Bt, W - 1, C), x.dtype, dev)
+    so = torch.empty_like(state) if out_state is None else out_state
     sop = _tensor(so, "out_state", (Bt, W - 1, C), x.dtype, dev)
     _run("ssd_conv_step", dev, ctypes.byref(tok), xp, xs, w, b, W, _silu(activation), sp_in, sop,
          yp, sp)
@@ -331,9 +339,9 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, initial_state=None, *, dt_bia
     dev = x.device
     tok, S = _tokens(x, cu_seqlens)
     q = _selective(x, dt, A, B, C, D, z, initial_state, dt_bias, dt_softplus, S, x.shape[:2], dev)
-    y = _or(out, x.shape, x.dtype, dev)
+    y = _or(out, x, x.shape)
     yp = _tensor(y, "out", x.shape, x.dtype, dev)
-    fin = _or(final_out, (S, x.shape[2], q.dstate), torch.float32, dev) if want_final else None
+    fin = _or(final_out, A, (S, x.shape[2], q.dstate)) if want_final else None
     fp = _tensor(fin, "final_out", (S, x.shape[2], q.dstate), torch.float32, dev)
     t, qr = ctypes.byref(tok), ctypes.byref(q)
     ws, wp, n = _workspace("ssd_selective_scan_workspace", dev, t, qr)
@@ -351,8 +359,8 @@ def selective_step(state, x, dt, A, B, C, D=None, z=None, *, dt_bias=None, dt_so
         raise ValueError("state must be [batch, channels, dstate]")
     tok = SSDTokens(Bt, 1, Dm, Bt, None, io, 0)
     q = _selective(x, dt, A, B, C, D, z, state, dt_bias, dt_softplus, Bt, (Bt,), dev)
-    y = _or(out, (Bt, Dm), x.dtype, dev)
-    so = _or(out_state, state.shape, torch.float32, dev)
+    y = _or(out, x, (Bt, Dm))
+    so = torch.empty_like(state) if out_state is None else out_state
     yp = _tensor(y, "out", (Bt, Dm), x.dtype, dev)
     sop = _tensor(so, "out_state", state.shape, torch.float32, dev)
     _run("ssd_selective_step", dev, ctypes.byref(tok), ctypes.byref(q), sop, yp)
@@ -400,7 +408,7 @@ def gated_norm(x, z, weight, *, eps=1e-5, ngroups=1, norm_before_gate=False, out
     xp, xs = _rows(x, "x", x.shape, x.dtype, dev)
     zp, zs = _rows(z, "z", x.shape, x.dtype, dev)
     w = _tensor(weight, "weight", x.shape[2:], torch.float32, dev)
-    y = _or(out, x.shape, x.dtype, dev)
+    y = _or(out, x, x.shape)
     yp = _tensor(y, "out", x.shape, x.dtype, dev)
     _run("ssd_gated_norm", dev, ctypes.byref(tok), xp, xs, zp, zs, w, ngroups, eps,
          1 if norm_before_gate else 0, yp)
@@ -455,7 +463,7 @@ def residual_norm(x, residual, weight, *, scale=None, eps=1e-5, residual_dtype=N
     rp = _tensor(residual, "residual", x.shape, rt, dev)
     w = _tensor(weight, "weight", x.shape[2:], torch.float32, dev)
     sc = _tensor(scale, "scale", x.shape[2:], torch.float32, dev)
-    y, r = _or(out, x.shape, x.dtype, dev), _or(residual_out, x.shape, rt, dev)
+    y, r = _or(out, x, x.shape), _or(residual_out, x, x.shape, rt)
     yp = _tensor(y, "out", x.shape, x.dtype, dev)
     op = _tensor(r, "residual_out", x.shape, rt, dev)
     _run("ssd_residual_norm", dev, ctypes.byref(tok), xp, xs, rp, DTYPES[rt], sc, w, eps, yp, op)

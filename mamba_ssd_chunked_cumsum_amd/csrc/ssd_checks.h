@@ -2,6 +2,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/ssd.h"
@@ -24,8 +25,11 @@ inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline ssd_status device_ready() {
+  static std::atomic<bool> seen{false};  // devices do not go away once a call has found one
+  if (seen.load(std::memory_order_relaxed)) return SSD_OK;
   int n = 0;
   if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) return SSD_ERR_NO_DEVICE;
+  seen.store(true, std::memory_order_relaxed);
   return SSD_OK;
 }
 

@@ -155,12 +155,39 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
   const IO *B = (const IO*)q.B + g * q.N + n0, *C = (const IO*)q.Cm + g * q.N + n0;
   const void* zp = q.z ? q.z : q.x;  // (without a gate the values read are not used)
   const int64_t zs = q.z ? q.zs : q.xs;
+  // rows that are read next: a row's address is scalar, the channel the lane's offset
+  const char *px = row_at((const IO*)q.x, r0 * q.xs), *pt = row_at((const IO*)q.dt, r0 * q.dts),
+             *py = row_at(dy, (int64_t)r0 * q.C), *pz = row_at((const IO*)zp, r0 * zs),
+             *pb = row_at(B, r0 * q.bs), *pc = row_at(C, r0 * q.cs);
+  int ahead = r0, ahead_bc = r0;  // their indices, held at the last row
   uint32_t rx[U], rt[U], ry[U], rz[U];
-  auto fetch = [&](int t, int i) {
-    rx[i] = load_raw<IO>(row_at((const IO*)q.x, t * q.xs), off);
-    rt[i] = load_raw<IO>(row_at((const IO*)q.dt, t * q.dts), off);
-    ry[i] = load_raw<IO>(row_at(dy, (int64_t)t * q.C), off);
-    rz[i] = load_raw<IO>(row_at((const IO*)zp, t * zs), off);
+  auto fetch = [&] {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      rx[i] = load_raw<IO>(px, off);
+      rt[i] = load_raw<IO>(pt, off);
+      ry[i] = load_raw<IO>(py, off);
+      rz[i] = load_raw<IO>(pz, off);
+      if (++ahead < r1) {
+        px += q.xs * sizeof(IO);
+        pt += q.dts * sizeof(IO);
+        py += (int64_t)q.C * sizeof(IO);
+        pz += zs * sizeof(IO);
+      }
+    }
+  };
+  struct Rows2 {
+    Row<IO, NT, EXACT> B, C;
+  };
+  auto rows = [&] {
+    Rows2 m;
+    m.B.load((const IO*)pb, N);
+    m.C.load((const IO*)pc, N);
+    if (++ahead_bc < r1) {
+      pb += q.bs * sizeof(IO);
+      pc += q.cs * sizeof(IO);
+    }
+    return m;
   };
   float x[U], dl[U], e[U];
   auto unpack = [&] {
@@ -182,10 +209,9 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
       }
     }
   };
-  auto token = [&](int t, int i) {
-    Row<IO, NT, EXACT> Bt, Ct;
-    Bt.load(B + t * q.bs, N);
-    Ct.load(C + t * q.cs, N);
+  Rows2 bc = rows();
+  auto token = [&](int i) {
+    const Rows2 next = rows();  // a token ahead
     const float du = dl[i] * x[i];
     sum += dl[i];
     constexpr int GR = 8;
@@ -197,16 +223,17 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
 #pragma unroll
       for (int j = 0; j < GR; ++j) a[j] = exp2_fast(a[j]);
 #pragma unroll
-      for (int j = 0; j < GR; ++j) v[j] = du * Bt.get(n + j);
+      for (int j = 0; j < GR; ++j) v[j] = du * bc.B.get(n + j);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < GR; ++j) {
         h[n + j] = fmaf(a[j], h[n + j], v[j]);
         p[n + j] *= a[j];
-        gl[n + j] = fmaf(p[n + j], e[i] * Ct.get(n + j), gl[n + j]);
+        gl[n + j] = fmaf(p[n + j], e[i] * bc.C.get(n + j), gl[n + j]);
       }
       __builtin_amdgcn_sched_barrier(0);  // (registers)
     }
+    bc = next;
   };
   bool began = false;
   auto begin = [&](int s) {  // what came before belongs to another sequence
@@ -234,21 +261,19 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
   uint64_t starts = 0, ends = 0, inside = ~uint64_t(0);
   if (EVENTS) mark_rows(q.rows, r0, r1, starts, ends, inside);
   else if (seq_begin(q.rows, s0) == r0) begin(s0);
-#pragma unroll
-  for (int i = 0; i < U; ++i) fetch(min(r0 + i, r1 - 1), i);
+  fetch();
 #pragma unroll 1
   for (int t = 0; t < kChunk; t += U) {
     if (t && t % kQuarter == 0) write_quarter(t / kQuarter - 1);
     unpack();
-#pragma unroll
-    for (int i = 0; i < U; ++i) fetch(min(r0 + t + U + i, r1 - 1), i);
+    fetch();
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (EVENTS) {
         if (!((inside >> (t + i)) & 1)) dl[i] = x[i] = e[i] = 0.f;  // decays nothing, adds nothing
         if ((starts >> (t + i)) & 1) begin(seq_of(q.rows, r0 + t + i));
       }
-      token(min(r0 + t + i, r1 - 1), i);
+      token(i);
       if (EVENTS && ((ends >> (t + i)) & 1)) finish(seq_of(q.rows, r0 + t + i));
     }
   }
