@@ -28,6 +28,7 @@ struct ConvArgs {
   const float *w, *bias;
   const void* init;
   Split y;  // forward: outputs; backward: their gradients
+  int stream = 0;  // forward: outputs are written past the caches
 };
 
 hipError_t launch_conv(const ConvArgs& a, void* fin, hipStream_t s);

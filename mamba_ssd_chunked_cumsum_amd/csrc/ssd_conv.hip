@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kBlock) void k_conv(ConvArgs q, IO* fin, int strip)
         v = fmaf(w[W - 1][i], xv[i], v);
         o[i] = q.silu ? v * sigmoid(v) : v;
       }
-      store_vec<IO, V>(y + (int64_t)(r + u) * width + col, o);
+      store_vec<IO, V>(y + (int64_t)(r + u) * width + col, o, q.stream);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -165,7 +165,8 @@ __global__ __launch_bounds__(kBlock) void k_conv_step(ConvArgs q, IO* state_out)
 // still incomplete: dv[t] adds w[W - 1 - i] dv[t] to the gradient of x[t - i]. Sums over rows (dw,
 // db) are kept in registers for the strip's own rows, added over the block's four strips in LDS and
 // written as one partial per block, which a second kernel sums in a fixed order.
-constexpr int kBwdV = 4, kBwdWaves = 4, kBwdStrip = 64;
+constexpr int kBwdV = 4, kBwdWaves = 4, kBwdStrip = 128;
+static_assert(64 * kBwdWaves == kBlock, "the trailing blocks count threads in kBlock");
 
 template <typename IO, typename DY, int W>
 __device__ __forceinline__ void conv_dv(const ConvArgs& q, const float (&w)[W][kBwdV],
@@ -187,12 +188,67 @@ __device__ __forceinline__ void conv_dv(const ConvArgs& q, const float (&w)[W][k
   }
 }
 
+// Gradient of the initial state: position p < 0 of sequence s takes w[k] dv[t] for its taps
+// t = p + W - 1 - k >= 0, and the final state's gradient where the sequence is shorter than it.
+template <typename IO, typename DY, int W>
+__device__ __forceinline__ void conv_dinit(const ConvArgs& q, const float* dfinal, float* dinit,
+                                           int64_t id) {
+  constexpr int V = kBwdV;
+  const int nvec = q.C / V;
+  const int s = (int)(id / nvec), c = (int)(id % nvec) * V;
+  if (s >= q.rows.S) return;
+  const int a = seq_begin(q.rows, s), len = max(seq_end(q.rows, s) - a, 0);
+  int width, col;
+  const int pi = split_of(q.y, c, &width, &col);
+  const DY* dyp = (const DY*)(pi == 0 ? q.y.p[0] : pi == 1 ? q.y.p[1] : q.y.p[2]) + col;
+  float w[W][V], bias[V], win[W - 1][V], g[W - 1][V];
+  load_weights<V, W>(q.w, q.bias, c, w, bias);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    input_at<IO, V>(q, s, a, j - (W - 1), W, c, win[j]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[j][i] = 0.f;
+    if (dfinal && j >= len) load_f32<V>(dfinal + ((int64_t)s * (W - 1) + j - len) * q.C + c, g[j]);
+  }
+#pragma unroll
+  for (int t = 0; t < W - 1; ++t) {
+    if (t >= len) break;
+    float xv[V], dy[V], dv[V];
+    input_at<IO, V>(q, s, a, t, W, c, xv);
+    Vec<DY, V> d;
+    d.load(dyp + (int64_t)(a + t) * width);
+    d.get(dy);
+    conv_dv<IO, DY, W>(q, w, bias, win, xv, dy, dv);
+    // state entry j is at position j - (W - 1): tap k = j - t of token t
+#pragma unroll
+    for (int j = t; j < W - 1; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[j][i] = fmaf(w[j - t][i], dv[i], g[j][i]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
+      win[W - 2][i] = xv[i];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+    store_vec<float, V>(dinit + ((int64_t)s * (W - 1) + j) * q.C + c, g[j]);
+}
+
 template <typename IO, typename DY, int W>
 __global__ __launch_bounds__(64 * kBwdWaves) void k_conv_bwd(ConvArgs q, const float* dfinal,
-                                                             IO* dx, float* part, int nvb) {
+                                                             IO* dx, float* part, float* dinit,
+                                                             int nvb, int nsb) {
   constexpr int V = kBwdV, U = 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int vb = blockIdx.x % nvb, sb = blockIdx.x / nvb;
+  const unsigned block = blockIdx.x;
+  const int vb = block % nvb, sb = block / nvb;
+  if (sb >= nsb) {  // the blocks behind the strips take the initial states' gradients
+    const int64_t id = (int64_t)(block - (unsigned)nvb * nsb) * kBlock + threadIdx.x;
+    conv_dinit<IO, DY, W>(q, dfinal, dinit, id);
+    return;
+  }
   const int c = (vb * 64 + lane) * V;
   const bool live = c < q.C;
   float dw[W + 1][V];
@@ -239,15 +295,26 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_conv_bwd(ConvArgs q, const f
         }
         store_vec<IO, V>(dx + (int64_t)t * q.C + c, o);
       };
+      Vec<IO, V> nx[U];  // the next U rows, loaded while the current ones are worked on
+      Vec<DY, V> ny[U];
+      auto fetch = [&](int from) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t t = min(from + u, last - 1);
+          nx[u].load(x + t * q.xs);
+          ny[u].load(dyp + t * width);
+        }
+      };
+      fetch(r);
       while (r < last) {
         Vec<IO, V> in[U];
         Vec<DY, V> din[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int64_t t = min(r + u, last - 1);
-          in[u].load(x + t * q.xs);
-          din[u].load(dyp + t * width);
+          in[u] = nx[u];
+          din[u] = ny[u];
         }
+        fetch(r + U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int t = r + u;
@@ -308,55 +375,6 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_conv_bwd(ConvArgs q, const f
   }
 }
 
-// Gradient of the initial state: position p < 0 of sequence s takes w[k] dv[t] for its taps
-// t = p + W - 1 - k >= 0, and the final state's gradient where the sequence is shorter than it.
-template <typename IO, typename DY, int W>
-__global__ __launch_bounds__(kBlock) void k_conv_dinit(ConvArgs q, const float* dfinal,
-                                                       float* dinit) {
-  constexpr int V = kBwdV;
-  const int nvec = q.C / V;
-  const int64_t id = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  const int s = (int)(id / nvec), c = (int)(id % nvec) * V;
-  if (s >= q.rows.S) return;
-  const int a = seq_begin(q.rows, s), len = max(seq_end(q.rows, s) - a, 0);
-  int width, col;
-  const int pi = split_of(q.y, c, &width, &col);
-  const DY* dyp = (const DY*)(pi == 0 ? q.y.p[0] : pi == 1 ? q.y.p[1] : q.y.p[2]) + col;
-  float w[W][V], bias[V], win[W - 1][V], g[W - 1][V];
-  load_weights<V, W>(q.w, q.bias, c, w, bias);
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) {
-    input_at<IO, V>(q, s, a, j - (W - 1), W, c, win[j]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) g[j][i] = 0.f;
-    if (dfinal && j >= len) load_f32<V>(dfinal + ((int64_t)s * (W - 1) + j - len) * q.C + c, g[j]);
-  }
-#pragma unroll
-  for (int t = 0; t < W - 1; ++t) {
-    if (t >= len) break;
-    float xv[V], dy[V], dv[V];
-    input_at<IO, V>(q, s, a, t, W, c, xv);
-    Vec<DY, V> d;
-    d.load(dyp + (int64_t)(a + t) * width);
-    d.get(dy);
-    conv_dv<IO, DY, W>(q, w, bias, win, xv, dy, dv);
-    // state entry j is at position j - (W - 1): tap k = j - t of token t
-#pragma unroll
-    for (int j = t; j < W - 1; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) g[j][i] = fmaf(w[j - t][i], dv[i], g[j][i]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-      for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
-      win[W - 2][i] = xv[i];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-    store_vec<float, V>(dinit + ((int64_t)s * (W - 1) + j) * q.C + c, g[j]);
-}
-
 unsigned blocks_of(int64_t threads) { return (unsigned)((threads + kBlock - 1) / kBlock); }
 
 int conv_bwd_blocks(int R) {
@@ -374,7 +392,11 @@ hipError_t by_width(int W, F f) {
 
 }  // namespace
 
-hipError_t launch_conv(const ConvArgs& a, void* fin, hipStream_t s) {
+hipError_t launch_conv(const ConvArgs& given, void* fin, hipStream_t s) {
+  ConvArgs a = given;
+  // outputs beyond 64 MiB would not be found in a cache by what reads them next anyway (2 x 8192 x
+  // 5376 bf16: 78 us with ordinary stores, 74 us past the caches)
+  a.stream = (int64_t)a.rows.R * a.C * (a.io == kIoBf16 ? 2 : 4) > (int64_t(64) << 20);
   const int nvec = a.C / 8;
   const int strip = 16;
   const int64_t nstrip = (a.rows.R + strip - 1) / strip;
@@ -410,18 +432,12 @@ template <typename IO, typename DY, int W>
 static hipError_t conv_backward(const ConvArgs& a, const float* dfinal, void* dx, float* dw,
                                 float* db, float* dinit, float* ws, hipStream_t s) {
   const int nvb = (a.C / kBwdV + 63) / 64, nsb = conv_bwd_blocks(a.rows.R);
-  hipLaunchKernelGGL((k_conv_bwd<IO, DY, W>), dim3((unsigned)((int64_t)nvb * nsb)),
-                     dim3(64 * kBwdWaves), 0, s, a, dfinal, (IO*)dx, ws, nvb);
-  hipError_t e = hipGetLastError();
-  if (e == hipSuccess)
-    e = launch_column_sums(ws, nsb, (int64_t)W * a.C, dw, a.C, 1, W, a.C, db, 0, nullptr, s);
-  if (e == hipSuccess && dinit) {
-    hipLaunchKernelGGL((k_conv_dinit<IO, DY, W>),
-                       dim3(blocks_of((int64_t)a.rows.S * (a.C / kBwdV))), dim3(kBlock), 0, s, a,
-                       dfinal, dinit);
-    e = hipGetLastError();
-  }
-  return e;
+  const int64_t tail = dinit ? ((int64_t)a.rows.S * (a.C / kBwdV) + kBlock - 1) / kBlock : 0;
+  hipLaunchKernelGGL((k_conv_bwd<IO, DY, W>), dim3((unsigned)((int64_t)nvb * nsb + tail)),
+                     dim3(64 * kBwdWaves), 0, s, a, dfinal, (IO*)dx, ws, dinit, nvb, nsb);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_column_sums(ws, nsb, (int64_t)W * a.C, dw, a.C, 1, W, a.C, db, 0, nullptr, s);
 }
 
 hipError_t launch_conv_backward(const ConvArgs& a, int dy_io, const float* dfinal, void* dx,

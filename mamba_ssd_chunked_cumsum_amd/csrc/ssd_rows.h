@@ -71,8 +71,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ void store_io(float* p, int i, float v) { p[i] = v; }
 __device__ __forceinline__ void store_io(u16* p, int i, float v) { p[i] = (u16)pack_bf16(v, v); }
 
+// stream: past the caches, for outputs far larger than they are.
 template <typename IO, int V>
-__device__ __forceinline__ void store_vec(IO* p, const float (&v)[V]) {
+__device__ __forceinline__ void store_vec(IO* p, const float (&v)[V], bool stream = false) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   uint32_t u[Vec<IO, V>::kWords];
   if constexpr (sizeof(IO) == 4) {
 #pragma unroll
@@ -83,8 +85,11 @@ __device__ __forceinline__ void store_vec(IO* p, const float (&v)[V]) {
   }
   if constexpr (Vec<IO, V>::kWords % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < Vec<IO, V>::kWords / 4; ++i)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+    for (int i = 0; i < Vec<IO, V>::kWords / 4; ++i) {
+      const u32x4 w = {u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]};
+      if (stream) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p) + i);
+      else reinterpret_cast<u32x4*>(p)[i] = w;
+    }
   } else {
     *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
   }
