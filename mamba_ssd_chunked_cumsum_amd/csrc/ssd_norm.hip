@@ -45,6 +45,39 @@ struct Shape {
   static constexpr int kThreads = NT < 256 ? 256 : NT, kRows = kThreads / NT;
 };
 
+// A block's sums for n columns: of its one row walker, or of the four that its waves are, added in
+// LDS.
+template <int NT, int NV>
+__device__ __forceinline__ void store_sums(float* part, int n, float (&v)[NV][V]) {
+  const int t = threadIdx.x % NT;
+  if constexpr (NT == 64) {
+    __shared__ __attribute__((aligned(16))) float red[4][64 * V];
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      __syncthreads();
+      store_vec<float, V>(&red[wave][t * V], v[i]);
+      __syncthreads();
+      const int c = (t + i * NT) * V + 2 * wave;  // two columns a thread
+      if (c < n) {
+        float o[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int at = t * V + 2 * wave + j;
+          o[j] = ((red[0][at] + red[1][at]) + red[2][at]) + red[3][at];
+        }
+        *reinterpret_cast<float2*>(part + c) = make_float2(o[0], o[1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (t + i * NT) * V;
+      if (c < n) store_vec<float, V>(part + c, v[i]);
+    }
+  }
+}
+
 // ---- gated norm --------------------------------------------------------------------------------
 // BEFORE: norm before gate. z null: no gate.
 template <typename IO, int NT, int NV, bool BEFORE, bool GATE>
@@ -108,9 +141,8 @@ __global__ __launch_bounds__(Shape<NT>::kThreads) void k_gated_bwd(
   __shared__ float red[2][16];
   int turn = 0;
   const int n = q.C / q.G, t = threadIdx.x % NT;
-  const int64_t id = (int64_t)blockIdx.x * Shape<NT>::kRows + threadIdx.x / NT;
-  if (id >= (int64_t)walkers * q.G) return;
-  const int c0 = (int)(id % q.G) * n, walker = (int)(id / q.G);
+  const int c0 = (int)(blockIdx.x % q.G) * n;
+  const int walker = (int)(blockIdx.x / q.G) * Shape<NT>::kRows + threadIdx.x / NT;
   float w[NV][V], dw[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -191,11 +223,7 @@ __global__ __launch_bounds__(Shape<NT>::kThreads) void k_gated_bwd(
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * NT) * V;
-    if (c < n) store_vec<float, V>(part + (int64_t)walker * q.C + c0 + c, dw[i]);
-  }
+  store_sums<NT, NV>(part + (int64_t)(blockIdx.x / q.G) * q.C + c0, n, dw);
 }
 
 // ---- residual norm -----------------------------------------------------------------------------
@@ -258,7 +286,6 @@ __global__ __launch_bounds__(Shape<NT>::kThreads) void k_residual_bwd(
   int turn = 0;
   const int n = q.C, t = threadIdx.x % NT;
   const int walker = (int)(blockIdx.x * Shape<NT>::kRows + threadIdx.x / NT);
-  if (walker >= walkers) return;
   float w[NV][V], dw[NV][V], ds[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -267,23 +294,36 @@ __global__ __launch_bounds__(Shape<NT>::kThreads) void k_residual_bwd(
     for (int j = 0; j < V; ++j) w[i][j] = dw[i][j] = ds[i][j] = 0.f;
     if (c < n) load_f32<V>(q.w + c, w[i]);
   }
+  Vec<RES, V> nr[NV], ng[NV];  // the next row, loaded while the current one is worked on
+  Vec<IO, V> nd[NV], nx[NV];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (t + i * NT) * V;
+      nr[i].zero();
+      ng[i].zero();
+      nd[i].zero();
+      nx[i].zero();
+      if (c < n) {
+        nr[i].load(rsum + row * n + c);
+        nd[i].load(dy + row * n + c);
+        if (dres) ng[i].load(dres + row * n + c);
+        if (SCALE) nx[i].load(x + row * xs + c);
+      }
+    }
+  };
+  if (walker < q.R) fetch(walker);
   for (int64_t row = walker; row < q.R; row += walkers) {
     Vec<RES, V> rr[NV], gr[NV];
     Vec<IO, V> dr[NV], xr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * NT) * V;
-      rr[i].zero();
-      gr[i].zero();
-      dr[i].zero();
-      xr[i].zero();
-      if (c < n) {
-        rr[i].load(rsum + row * n + c);
-        dr[i].load(dy + row * n + c);
-        if (dres) gr[i].load(dres + row * n + c);
-        if (SCALE) xr[i].load(x + row * xs + c);
-      }
+      rr[i] = nr[i];
+      gr[i] = ng[i];
+      dr[i] = nd[i];
+      xr[i] = nx[i];
     }
+    if (row + walkers < q.R) fetch(row + walkers);
     float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -317,15 +357,9 @@ __global__ __launch_bounds__(Shape<NT>::kThreads) void k_residual_bwd(
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * NT) * V;
-    if (c < n) {
-      float* p = part + (int64_t)walker * n * (SCALE ? 2 : 1) + c;
-      store_vec<float, V>(p, dw[i]);
-      if (SCALE) store_vec<float, V>(p + n, ds[i]);
-    }
-  }
+  float* p = part + (int64_t)blockIdx.x * n * (SCALE ? 2 : 1);
+  store_sums<NT, NV>(p, n, dw);
+  if (SCALE) store_sums<NT, NV>(p + n, n, ds);
 }
 
 // The smallest shape that holds n channels: a wave up to 1024, a block of 256 up to 6144, of 512 up
@@ -343,12 +377,18 @@ hipError_t by_length(int n, F f) {
   return go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
 }
 
-// Walkers of a backward pass: rows of partial sums. At least 8 rows each keeps their traffic
-// (4 bytes a column) under an eighth of the rows'; up to 2048 waves' worth of blocks.
-int walkers_of(int R, int G, int n) {
-  const int most = n <= 1024 ? 4096 / G : n <= 8192 ? 1024 / G : 512 / G;
-  const int want = (R + 7) / 8;
-  return want < 1 ? 1 : want < most ? want : most < 1 ? 1 : most;
+// How a backward pass is divided: row walkers, each of a wave (up to 1024 channels) or a block, and
+// the partial sums they leave, one a block. At least 4 rows a walker (8 of a block), so that the
+// partials are small beside the rows, and at most 8192 waves or 1024 blocks, a few for every SIMD.
+struct Walk {
+  int walkers, parts;  // of a group
+};
+Walk walk_of(int R, int G, int n) {
+  const int per = n <= 1024 ? 4 : 1;  // walkers a block
+  const int most = (n <= 1024 ? 8192 : 1024) / G, want = n <= 1024 ? (R + 3) / 4 : (R + 7) / 8;
+  const int w = want < most ? want : most < 1 ? 1 : most;
+  const int parts = (w + per - 1) / per;
+  return Walk{parts * per, parts};
 }
 
 }  // namespace
@@ -375,22 +415,22 @@ hipError_t launch_gated_norm(const NormArgs& a, const void* x, int64_t xs, const
 }
 
 int64_t norm_backward_bytes(const NormArgs& a, int sums) {
-  return (int64_t)walkers_of(a.R, a.G, a.C / a.G) * a.C * sums * 4;
+  return (int64_t)walk_of(a.R, a.G, a.C / a.G).parts * a.C * sums * 4;
 }
 
 hipError_t launch_gated_norm_backward(const NormArgs& a, const void* x, int64_t xs, const void* z,
                                       int64_t zs, int before, const void* dy, void* dx, void* dz,
                                       float* dw, float* ws, hipStream_t s) {
-  const int walkers = walkers_of(a.R, a.G, a.C / a.G);
+  const Walk walk = walk_of(a.R, a.G, a.C / a.G);
   const hipError_t e = by_length(a.C / a.G, [&](auto nt, auto nv) {
     constexpr int NT = decltype(nt)::value, NV = decltype(nv)::value;
-    const unsigned nb =
-        (unsigned)(((int64_t)walkers * a.G + Shape<NT>::kRows - 1) / Shape<NT>::kRows);
+    const unsigned nb = (unsigned)((int64_t)walk.parts * a.G);
     auto run = [&](auto io, auto bf, auto gt) {
       using IO = decltype(io);
       hipLaunchKernelGGL((k_gated_bwd<IO, NT, NV, decltype(bf)::value, decltype(gt)::value>),
                          dim3(nb), dim3(Shape<NT>::kThreads), 0, s, a, (const IO*)x, xs,
-                         (const IO*)z, zs, (const IO*)dy, (IO*)dx, (IO*)dz, ws, walkers);
+                         (const IO*)z, zs, (const IO*)dy, (IO*)dx, (IO*)dz, ws,
+                         walk.walkers);
       return hipGetLastError();
     };
     auto gates = [&](auto io) {
@@ -401,7 +441,7 @@ hipError_t launch_gated_norm_backward(const NormArgs& a, const void* x, int64_t 
     return a.io == kIoBf16 ? gates(u16{}) : gates(float{});
   });
   if (e != hipSuccess) return e;
-  return launch_column_sums(ws, walkers, a.C, dw, a.C, 0, 1, 0, nullptr, 0, nullptr, s);
+  return launch_column_sums(ws, walk.parts, a.C, dw, a.C, 0, 1, 0, nullptr, 0, nullptr, s);
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, const void* x, int64_t xs, const void* res,
@@ -426,16 +466,17 @@ hipError_t launch_residual_norm_backward(const NormArgs& a, const void* r, int r
                                          const void* x, int64_t xs, const float* scale,
                                          const void* dy, const void* dres, void* dx, void* dresid,
                                          float* dw, float* dscale, float* ws, hipStream_t s) {
-  const int walkers = walkers_of(a.R, 1, a.C);
+  const Walk walk = walk_of(a.R, 1, a.C);
   const hipError_t e = by_length(a.C, [&](auto nt, auto nv) {
     constexpr int NT = decltype(nt)::value, NV = decltype(nv)::value;
-    const unsigned nb = (unsigned)((walkers + Shape<NT>::kRows - 1) / Shape<NT>::kRows);
+    const unsigned nb = (unsigned)walk.parts;
     auto run = [&](auto io, auto re, auto sc) {
       using IO = decltype(io);
       using RES = decltype(re);
       hipLaunchKernelGGL((k_residual_bwd<IO, RES, NT, NV, decltype(sc)::value>), dim3(nb),
                          dim3(Shape<NT>::kThreads), 0, s, a, (const RES*)r, (const IO*)x, xs, scale,
-                         (const IO*)dy, (const RES*)dres, (IO*)dx, (RES*)dresid, ws, walkers);
+                         (const IO*)dy, (const RES*)dres, (IO*)dx, (RES*)dresid, ws,
+                         walk.walkers);
       return hipGetLastError();
     };
     auto scales = [&](auto io, auto re) {
@@ -445,7 +486,7 @@ hipError_t launch_residual_norm_backward(const NormArgs& a, const void* r, int r
     return res_io == kIoF32 ? scales(u16{}, float{}) : scales(u16{}, u16{});
   });
   if (e != hipSuccess) return e;
-  return launch_column_sums(ws, walkers, a.C, dw, a.C, 0, 1, scale ? a.C : 0, dscale, 0,
+  return launch_column_sums(ws, walk.parts, a.C, dw, a.C, 0, 1, scale ? a.C : 0, dscale, 0,
                             nullptr, s);
 }
 
