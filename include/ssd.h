@@ -282,7 +282,8 @@ ssd_status ssd_backward(const ssd_problem* prob, const void* x, const float* dt,
  * (seq_starts NULL): `batch` sequences of `seqlen` tokens, nseq must equal batch. Packed: batch
  * must be 1, and sequence s of the nseq holds the rows [seq_starts[s], seq_starts[s + 1]);
  * seq_starts is nseq + 1 non-decreasing int32 offsets in device memory. A sequence may be empty.
- * Rows outside every sequence are neither read nor written. Offsets outside [0, seqlen] or out of
+ * Rows outside every sequence (behind the last) are not read, forward outputs there are left as
+ * they were, and their gradients are zero. Offsets outside [0, seqlen] or out of
  * order are not reported (the host does not read them): which rows are computed is then
  * undefined, but no access leaves the tensors.
  *

@@ -8,8 +8,8 @@ float32. An activation may be a slice of wider rows (one projection's output) as
 channels are adjacent, its rows evenly spaced, the offset 16-byte aligned and the row stride a
 multiple of 8 elements (the selective scan's B and C: of 4 elements each). Packed prompts: batch 1 and cu_seqlens, int32 offsets [nseq + 1] on the
 device, sequence s being the tokens [cu_seqlens[s], cu_seqlens[s + 1]) (it may be empty); states
-then have nseq entries. Tokens outside every sequence are left as they are in given outputs and
-undefined in fresh ones. cu_seqlens is not read on the host: offsets that decrease or leave
+then have nseq entries. Tokens behind the last sequence are not read; forward outputs there are
+left as they are (undefined in fresh tensors) and their gradients are zero. cu_seqlens is not read on the host: offsets that decrease or leave
 [0, seqlen] give undefined results.
 
 The calls run on the current stream of the inputs' device and allocate their outputs and workspace

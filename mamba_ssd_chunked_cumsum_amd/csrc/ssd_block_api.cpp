@@ -2,6 +2,7 @@
 // host before the first HIP call.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -190,17 +191,21 @@ int64_t sel_state_bytes(const ssd_tokens* t, const ssd_selective* in) {
 bool grid_fits(double blocks, int threads) { return blocks * threads < 4294967296.0; }
 
 bool selective_grid_fits(const ssd::SelArgs& a) {
-  const double tiles = double(a.C) / 16 + a.G;  // the narrowest tile is 16 channels
+  const int width = a.N <= 16 ? 64 : a.N <= 32 ? 32 : 16;  // channels of the backward's tiles
+  const double tiles = double(a.C) / width + a.G;
   const double units = double(a.rows.R) / 64 + a.rows.S + 1;
   return grid_fits(tiles * units, 256) && grid_fits(double(a.C) * a.N * a.rows.S / 256 + 1, 256) &&
          grid_fits(double(a.rows.R) * 2 * a.N * a.G / 256 + 1, 256);
 }
 
-int compute_units() {
+int compute_units() {  // of the current device, asked for once
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
     n = 256;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

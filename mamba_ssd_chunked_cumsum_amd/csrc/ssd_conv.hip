@@ -87,9 +87,8 @@ __global__ __launch_bounds__(kBlock) void k_conv(ConvArgs q, IO* fin, int strip)
   for (int r = r0; r < r1;) {
     if (r >= end) {  // the next sequence (the first one: where the strip stands in it)
       s = seq_of(q.rows, r);
-      if (s < 0) {  // a row of no sequence
-        ++r;
-        end = r;
+      if (s < 0) {  // rows of no sequence
+        r = end = after_gap(q.rows, r);
         continue;
       }
       const int a = seq_begin(q.rows, s);
@@ -267,8 +266,10 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_conv_bwd(ConvArgs q, const f
     float win[W - 1][V], acc[W][V];  // acc[i]: gradient of x[r - i], incomplete but for i = W - 1
     for (int r = r0; r < r1;) {  // sequence by sequence
       const int s = seq_of(q.rows, r);
-      if (s < 0) {
-        ++r;
+      if (s < 0) {  // rows of no sequence: no gradient
+        const float zero[V] = {};
+        const int to = min(after_gap(q.rows, r), r1);
+        for (; r < to; ++r) store_vec<IO, V>(dx + (int64_t)r * q.C + c, zero);
         continue;
       }
       const int a = seq_begin(q.rows, s), b = seq_end(q.rows, s);

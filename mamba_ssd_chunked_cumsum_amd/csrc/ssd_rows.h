@@ -27,6 +27,12 @@ __device__ __forceinline__ int seq_of(const Rows& q, int r) {
   return r < seq_end(q, lo) ? lo : -1;
 }
 
+// Where to go on from row r of no sequence: only rows before the first sequence and behind the last
+// are in none.
+__device__ __forceinline__ int after_gap(const Rows& q, int r) {
+  return r < seq_begin(q, 0) ? seq_begin(q, 0) : q.R;
+}
+
 // ---- vectors of V consecutive channels (16-byte aligned for V = 8, 8-byte for bf16 V = 4) -------
 template <typename IO, int V>
 struct Vec {

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
   for (int r = r0; r < r1;) {  // sequence by sequence
     const int s = seq_of(q.rows, r);
     if (s < 0) {
-      ++r;
+      r = after_gap(q.rows, r);
       continue;
     }
     const int end = seq_end(q.rows, s), b = min(end, r1);

@@ -209,6 +209,9 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
       }
     }
   };
+  // open: no boundary so far, so the rows still reach the state that entered the chunk. (A flag, not
+  // p = 0: a NaN of the next sequence would pass through that.)
+  bool began = false, open = true;
   Rows2 bc = rows();
   auto token = [&](int i) {
     const Rows2 next = rows();  // a token ahead
@@ -226,31 +229,33 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
       for (int j = 0; j < GR; ++j) v[j] = du * bc.B.get(n + j);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < GR; ++j) {
-        h[n + j] = fmaf(a[j], h[n + j], v[j]);
-        p[n + j] *= a[j];
-        gl[n + j] = fmaf(p[n + j], e[i] * bc.C.get(n + j), gl[n + j]);
+      for (int j = 0; j < GR; ++j) h[n + j] = fmaf(a[j], h[n + j], v[j]);
+      if (!EVENTS || open) {
+#pragma unroll
+        for (int j = 0; j < GR; ++j) {
+          p[n + j] *= a[j];
+          gl[n + j] = fmaf(p[n + j], e[i] * bc.C.get(n + j), gl[n + j]);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);  // (registers)
     }
     bc = next;
   };
-  bool began = false;
   auto begin = [&](int s) {  // what came before belongs to another sequence
     began = true;
+    open = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) h[n] = p[n] = 0.f;
+    for (int n = 0; n < NT; ++n) h[n] = 0.f;
     if (q.h0) load_all<NT>(q.h0 + (int64_t)s * CN + at, N, h);
   };
   auto finish = [&](int s) {
-    if (dfinal) {
+    if (open && dfinal) {
       float d[NT];
       load_all<NT>(dfinal + (int64_t)s * CN + at, N, d);
 #pragma unroll
       for (int n = 0; n < NT; ++n) gl[n] = fmaf(p[n], d[n], gl[n]);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) p[n] = 0.f;
+    open = false;
   };
   auto write_quarter = [&](int i) {
     if (!live) return;
@@ -263,7 +268,7 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
   else if (seq_begin(q.rows, s0) == r0) begin(s0);
   fetch();
 #pragma unroll 1
-  for (int t = 0; t < kChunk; t += U) {
+  for (int t = 0; t < (inside ? kChunk : 0); t += U) {
     if (t && t % kQuarter == 0) write_quarter(t / kQuarter - 1);
     unpack();
     fetch();
@@ -278,6 +283,10 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
     }
   }
   if (!EVENTS && seq_end(q.rows, s0) == r1) finish(s0);
+  if (!EVENTS && began) {  // nothing entered
+#pragma unroll
+    for (int n = 0; n < NT; ++n) gl[n] = 0.f;
+  }
   if (live) {
     store_all<NT>(w.state + ((int64_t)u * 4 + 3) * CN + at, N, h);
     store_all<NT>(w.adj + (int64_t)u * CN + at, N, gl);
@@ -389,6 +398,29 @@ __device__ __forceinline__ int merged_value() {
   else return r;
 }
 
+// Gradients of a row of no sequence, 8 channels.
+template <typename IO>
+__device__ __forceinline__ void zero_row(const SelArgs& q, const SelGrads& o, int64_t row, int c) {
+  const float zero[8] = {};
+  store_vec<IO, 8>((IO*)o.dx + row * q.C + c, zero);
+  store_vec<IO, 8>((IO*)o.ddt + row * q.C + c, zero);
+  if (q.z) store_vec<IO, 8>((IO*)o.dz + row * q.C + c, zero);
+}
+
+// A chunk that holds no row of a sequence: zero gradients, nothing to the sums.
+template <typename IO, int K>
+__device__ __forceinline__ void leave_empty(const SelArgs& q, const SelGrads& o, const Tile& b,
+                                            int r0, int r1, float* part) {
+  constexpr int CH = kSelThreads / K, PER = CH / 8;
+  const int c = b.base + threadIdx.x % PER * 8;
+  for (int row = r0 + threadIdx.x / PER; row < r1; row += kSelThreads / PER)
+    if (c < b.stop) zero_row<IO>(q, o, row, c);
+  const int ch = min(CH, b.stop - b.base);
+  for (int i = threadIdx.x; i < ch * q.N; i += kSelThreads) part[(int64_t)b.base * q.N + i] = 0.f;
+  for (int i = threadIdx.x; i < 2 * ch; i += kSelThreads)
+    part[(int64_t)q.C * q.N + (int64_t)(i / ch) * q.C + b.base + i % ch] = 0.f;
+}
+
 // ---- main ----------------------------------------------------------------------------------------
 template <typename IO, int K>
 __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, SelGrads o,
@@ -407,6 +439,11 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
   const int r0 = u * TC, r1 = min(r0 + TC, q.rows.R);
   uint64_t starts, ends, inside;
   mark_rows(q.rows, r0, r1, starts, ends, inside);
+  float* part = w.part + (int64_t)u * q.C * (q.N + 2);
+  if (!inside) {  // rows of no sequence
+    leave_empty<IO, K>(q, o, b, r0, r1, part);
+    return;
+  }
   stage<IO, TC, CH, NP>(q, dy, b, r0, r1, inside, s_dl, s_du, s_e, s_b, s_c);
   float A[NPL], h[4][NPL], g[NPL], dA[NPL];
 #pragma unroll
@@ -525,7 +562,6 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
   };
   if (starts | ends) walk(std::false_type{});
   else walk(std::true_type{});
-  float* part = w.part + (int64_t)u * q.C * (q.N + 2);
   if (live) store_states<NPL>(part + (int64_t)c * q.N, k, q.N, dA);
   // outputs of the chunk: a thread takes 8 channels of every 32nd row; e x and ddt are summed over
   // its rows, then over the threads of the same channels
@@ -541,8 +577,11 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
     if (q.D) load_f32<V>(q.D + cc, D);
     if (q.dt_bias) load_f32<V>(q.dt_bias + cc, bias);
     for (int t = threadIdx.x / (CH / V); t < TC; t += TR) {
-      if (!((inside >> t) & 1)) continue;
       const int64_t row = r0 + t;
+      if (!((inside >> t) & 1)) {
+        if (row < r1) zero_row<IO>(q, o, row, cc);
+        continue;
+      }
       Vec<IO, V> xr, tr, dr, zr;
       xr.load((const IO*)q.x + row * q.xs + cc);
       tr.load((const IO*)q.dt + row * q.dts + cc);
@@ -608,12 +647,13 @@ __global__ __launch_bounds__(256) void k_bwd_bc(SelArgs q, Work w, SelGrads o, i
   if (id >= RN * q.G) return;
   const int g = (int)(id / RN);
   const int64_t at = id % RN, row = at / (2 * q.N);
-  if (seq_of(q.rows, (int)row) < 0) return;
   const int which = (int)(at / q.N) & 1, n = (int)(at % q.N);
   const float* p = w.bc + (int64_t)g * per_group * RN + at;
   float m = 0.f;
+  if (seq_of(q.rows, (int)row) >= 0) {
 #pragma unroll 4
-  for (int i = 0; i < per_group; ++i) m += p[i * RN];
+    for (int i = 0; i < per_group; ++i) m += p[i * RN];
+  }
   Io<IO>::store((IO*)(which ? o.dC : o.dB), (row * q.G + g) * q.N + n, m);
 }
 

@@ -139,6 +139,7 @@ def test_conv(lay, io, W, C, split, pad, act, bias, init):
         ag = block.conv_backward(xv, wv, bv, dyv, seqs, hv, dfv, act is not None, absolute=True)
         mt = torch.from_numpy(m).to(DEV)
         check(g["dx"].reshape(rows, C)[mt], wg["dx"][m], ag["dx"][m], 64, "dx")
+        assert torch.all(g["dx"].reshape(rows, C)[~mt] == 0)
         check(g["dweight"], wg["dw"], ag["dw"], 512, "dweight")
         if bias:
             check(g["dbias"], wg["db"], ag["db"], 512, "dbias")
@@ -245,6 +246,7 @@ def test_selective(lay, io, Dm, N, G, pad, gate, init, skip, soft):
         ag = block.selective_backward(*args, *more, absolute=True)
         for n in ("dx", "ddt", "dB", "dC") + (("dz",) if gate else ()):
             check(g[n].flatten(0, 1)[mt], wg[n][m], ag[n][m], k, (n, final))
+            assert torch.all(g[n].flatten(0, 1)[~mt] == 0)
         check(g["dA"], wg["dA"], ag["dA"], k + 16 * rows, "dA")
         if skip:
             check(g["dD"], wg["dD"], ag["dD"], k + 16 * rows, "dD")
@@ -320,6 +322,49 @@ def test_selective_extremes():
     assert torch.equal(y2[0][keep], y[0][keep])
     keep = torch.arange(Dm, device=DEV) != 9
     assert torch.equal(f2[0][keep], f[0][keep])
+
+
+@pytest.mark.parametrize("lens", [(70, 90, 60), (64, 128, 64), (3, 1, 2), (130, 640, 700)])
+def test_a_sequence_of_nan_stays_alone(lens):
+    """NaN in every input of the middle sequence: the others' outputs, states and gradients are those
+    of a call without it, bit for bit."""
+    rng = np.random.default_rng(19)
+    L, Dm, N = sum(lens), 72, 16
+    note(f"a sequence of NaN, {lens}")
+    t, _ = selective_inputs(rng, (1, L), 3, Dm, N, 1, "f32", 0, True, True, True, True)
+    dy, _ = value(rng, (1, L, Dm))
+    df, _ = value(rng, (3, Dm, N))
+    w, _ = value(rng, (Dm, 4))
+    cs, _ = value(rng, (3, 3, Dm))
+    _, cu = ranges(lens=lens)
+    mid = slice(lens[0], lens[0] + lens[1])
+    kw = dict(dt_bias=t["dt_bias"], dt_softplus=True, cu_seqlens=cu)
+    x = t["x"].contiguous()
+
+    def calls():
+        y, f = ssd.selective_scan(*(t[k] for k in NAMES), t["h0"], **kw)
+        g = ssd.selective_backward(*(t[k] for k in NAMES), dy, t["h0"], df, **kw)
+        cy, cf = ssd.conv(x, w, None, cs, cu_seqlens=cu)
+        cg = ssd.conv_backward(x, w, None, dy, cs, cs.float(), cu_seqlens=cu)
+        rows = [y, cy, cg["dx"]] + [g[k].flatten(2) for k in ("dx", "ddt", "dz", "dB", "dC")]
+        return [v.clone() for v in rows], [v.clone() for v in (
+            f, g["dinitial_state"], cf, cg["dinitial_state"])]
+
+    rows, states = calls()
+    for k in ("x", "dt", "B", "C", "z"):
+        t[k] = t[k].clone()
+        t[k][:, mid] = float("nan")
+    x[:, mid] = float("nan")
+    for v in (dy[0], ):
+        v[mid] = float("nan")
+    for v in (t["h0"], df, cs):
+        v[1] = float("nan")
+    rows2, states2 = calls()
+    for a, b in zip(rows, rows2):
+        assert torch.equal(a[:, :mid.start], b[:, :mid.start])
+        assert torch.equal(a[:, mid.stop:], b[:, mid.stop:])
+    for a, b in zip(states, states2):
+        assert torch.equal(a[::2], b[::2])
 
 
 # ---- norms -----------------------------------------------------------------------------------------
