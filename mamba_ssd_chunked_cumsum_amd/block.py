@@ -97,15 +97,16 @@ def _place(t, name, dtype, dev):
 
 
 def _tensor(t, name, shape, dtype, dev):
-    """A dense input or output: shape, dtype, device."""
+    """Address of a dense input or output (None for None) after checks of shape, dtype, device."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype == dtype and t.is_cuda and t.device == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     _place(t, name, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, name, shape, dtype, dev, lead=2):
@@ -196,7 +197,9 @@ def _or(t, like, shape, dtype=None):
 # ---- short causal convolution ------------------------------------------------------------------
 
 def _split_sizes(split, C):
-    sizes = (C,) if split is None else tuple(int(n) for n in split)
+    if split is None:
+        return (C,)
+    sizes = tuple(map(int, split))
     if not 1 <= len(sizes) <= 3 or sum(sizes) != C or min(sizes) <= 0:
         raise ValueError(f"split must be up to three positive sizes that sum to {C}")
     return sizes
@@ -204,8 +207,8 @@ def _split_sizes(split, C):
 
 def _parts(ts, name, sizes, lead, dtype, dev):
     """(void*[3], int64[3]) of the tensors the channels are split over."""
-    ptrs = [_tensor(t, name, (*lead, n), dtype, dev) for t, n in zip(ts, sizes)]
-    return _Ptr3(*ptrs), _Split3(*sizes)
+    return _Ptr3(*[_tensor(t, name, (*lead, n), dtype, dev) for t, n in zip(ts, sizes)]), \
+        _Split3(*sizes)
 
 
 def _outputs(out, split, sizes, lead, x):
@@ -218,9 +221,11 @@ def _outputs(out, split, sizes, lead, x):
 
 
 def _silu(activation):
-    if activation not in (None, "silu"):
+    if activation == "silu":
+        return 1
+    if activation is not None:
         raise ValueError(f"unknown activation {activation!r}")
-    return 1 if activation == "silu" else 0
+    return 0
 
 
 def _conv_params(weight, bias, C, dev):
