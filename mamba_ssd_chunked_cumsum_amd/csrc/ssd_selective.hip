@@ -212,7 +212,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
 // a sequence begins in a chunk (its sum is NaN, as is the end state where delta was NaN) nothing
 // passes through it. The loads of kAhead chunks are issued together.
 __global__ __launch_bounds__(256) void k_scan_chain(SelArgs q, Plan pl) {
-  constexpr int kAhead = 16;
+  constexpr int kAhead = 32;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, CN = (int64_t)q.C * q.N;
   if (id >= CN) return;
   const int c = (int)(id / q.N);
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(256) void k_sel_step(SelArgs q, float* state_out, I
   }
 }
 
-constexpr int kMinLen = 16;  // rows of a chunk
+constexpr int kMinLen = 32;  // rows of a chunk
 
 int64_t tiles_of(const SelArgs& a) { return (int64_t)((a.C / a.G + 63) / 64) * a.G; }
 
