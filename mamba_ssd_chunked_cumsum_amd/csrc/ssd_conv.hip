@@ -82,6 +82,18 @@ __global__ __launch_bounds__(kBlock) void k_conv(ConvArgs q, IO* fin, int strip)
   const IO* x = (const IO*)q.x;
   float w[W][V], bias[V];
   load_weights<V, W>(q.w, q.bias, c, w, bias);
+  // rows are loaded before it is known which sequence they are of; a sequence's start replaces the
+  // window's rows in front of it
+  Vec<IO, V> before[W - 1], nx[U];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) before[j].load(x + (int64_t)max(r0 - (W - 1) + j, 0) * q.xs + c);
+  int at = r0;  // the first row of nx
+  auto fetch = [&](int r) {
+    at = r;
+#pragma unroll
+    for (int u = 0; u < U; ++u) nx[u].load(x + (int64_t)min(r + u, r1 - 1) * q.xs + c);
+  };
+  fetch(r0);
   float win[W - 1][V];  // the last W - 1 inputs, oldest first
   int s = -1, end = r0;
   for (int r = r0; r < r1;) {
@@ -94,11 +106,17 @@ __global__ __launch_bounds__(kBlock) void k_conv(ConvArgs q, IO* fin, int strip)
       const int a = seq_begin(q.rows, s);
       end = min(seq_end(q.rows, s), r1);
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) input_at<IO, V>(q, s, a, r - a - (W - 1) + j, W, c, win[j]);
+      for (int j = 0; j < W - 1; ++j) {
+        const int p = r - a - (W - 1) + j;
+        if (r == r0 && p >= 0) before[j].get(win[j]);
+        else input_at<IO, V>(q, s, a, p, W, c, win[j]);
+      }
     }
+    if (at != r) fetch(r);
     Vec<IO, V> in[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) in[u].load(x + (int64_t)min(r + u, end - 1) * q.xs + c);
+    for (int u = 0; u < U; ++u) in[u] = nx[u];
+    if (r + U < r1) fetch(r + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (r + u >= end) break;
@@ -399,7 +417,8 @@ hipError_t launch_conv(const ConvArgs& given, void* fin, hipStream_t s) {
   // 5376 bf16: 78 us with ordinary stores, 74 us past the caches)
   a.stream = (int64_t)a.rows.R * a.C * (a.io == kIoBf16 ? 2 : 4) > (int64_t(64) << 20);
   const int nvec = a.C / 8;
-  const int strip = 16;
+  // 16 rows a thread; 8 where that would leave fewer than four waves a SIMD
+  const int strip = (int64_t)a.rows.R * nvec >= 16 * 262144 ? 16 : 8;
   const int64_t nstrip = (a.rows.R + strip - 1) / strip;
   const unsigned nb = blocks_of((nstrip + (fin ? a.rows.S : 0)) * nvec);
   return by_width(a.W, [&](auto w) {

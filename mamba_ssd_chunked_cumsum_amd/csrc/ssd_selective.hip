@@ -236,46 +236,58 @@ __global__ __launch_bounds__(256) void k_scan_chain(SelArgs q, Plan pl) {
 
 // ---- single token ----------------------------------------------------------------------------------
 // L lanes a channel with four states each, as the SSD step: bound by the state, read and written
-// once past the caches.
-template <typename IO, int L>
+// once past the caches. A thread takes NB sequences of its channel, whose states it loads together
+// and which share A, D and the bias.
+template <typename IO, int L, int NB>
 __global__ __launch_bounds__(256) void k_sel_step(SelArgs q, float* state_out, IO* y) {
   const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
-  const int n = (threadIdx.x % L) * 4;
-  if (id >= (int64_t)q.rows.R * q.C) return;
-  const int b = (int)(id / q.C), c = (int)(id % q.C), g = c / (q.C / q.G);
+  const int n = (threadIdx.x % L) * 4, groups = (q.rows.R + NB - 1) / NB;
+  if (id >= (int64_t)groups * q.C) return;
+  const int b0 = (int)(id / q.C) * NB, c = (int)(id % q.C), g = c / (q.C / q.G);
   const bool on = n < q.N;
   const int nc = on ? n : 0;
-  const f32x4 h = __builtin_nontemporal_load(
-      reinterpret_cast<const f32x4*>(q.h0 + id * q.N + nc));
-  const float4 A = *reinterpret_cast<const float4*>(q.A + (int64_t)c * q.N + nc);
-  Vec<IO, 4> B, Cv;
-  B.load((const IO*)q.B + b * q.bs + g * q.N + nc);
-  Cv.load((const IO*)q.Cm + b * q.cs + g * q.N + nc);
-  const float x = Io<IO>::load((const IO*)q.x, b * q.xs + c);
-  float dl = Io<IO>::load((const IO*)q.dt, b * q.dts + c) + (q.dt_bias ? q.dt_bias[c] : 0.f);
-  if (q.softplus) dl = softplus(dl);
-  const float du = dl * x, dl2 = dl * kLog2e;
-  const float a[4] = {A.x, A.y, A.z, A.w};
-  f32x4 o;
-  float acc = 0.f;
+  f32x4 h[NB];
+  Vec<IO, 4> B[NB], Cv[NB];
+  float x[NB], dl[NB], z[NB];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    o[j] = fmaf(exp2_fast(dl2 * a[j]), h[j], du * B.get(j));
-    acc = fmaf(o[j], Cv.get(j), acc);
+  for (int i = 0; i < NB; ++i) {
+    const int64_t b = min(b0 + i, q.rows.R - 1);
+    h[i] = __builtin_nontemporal_load(
+        reinterpret_cast<const f32x4*>(q.h0 + (b * q.C + c) * q.N + nc));
+    B[i].load((const IO*)q.B + b * q.bs + g * q.N + nc);
+    Cv[i].load((const IO*)q.Cm + b * q.cs + g * q.N + nc);
+    x[i] = Io<IO>::load((const IO*)q.x, b * q.xs + c);
+    dl[i] = Io<IO>::load((const IO*)q.dt, b * q.dts + c);
+    if (q.z) z[i] = Io<IO>::load((const IO*)q.z, b * q.zs + c);
   }
-  if (on)
-    __builtin_nontemporal_store(o, reinterpret_cast<f32x4*>(state_out + id * q.N + n));
-  else
-    acc = 0.f;
+  const float4 Av = *reinterpret_cast<const float4*>(q.A + (int64_t)c * q.N + nc);
+  const float a[4] = {Av.x, Av.y, Av.z, Av.w};
+  const float bias = q.dt_bias ? q.dt_bias[c] : 0.f, D = q.D ? q.D[c] : 0.f;
 #pragma unroll
-  for (int m = L / 2; m >= 1; m >>= 1) acc += __shfl_xor(acc, m, kWave);
-  if (n == 0) {
-    if (q.D) acc = fmaf(q.D[c], x, acc);
-    if (q.z) {
-      const float zv = Io<IO>::load((const IO*)q.z, b * q.zs + c);
-      acc *= zv * sigmoid(zv);
+  for (int i = 0; i < NB; ++i) {
+    if (b0 + i >= q.rows.R) break;
+    const int64_t at = (int64_t)(b0 + i) * q.C + c;
+    float d = dl[i] + bias;
+    if (q.softplus) d = softplus(d);
+    const float du = d * x[i], d2 = d * kLog2e;
+    f32x4 o;
+    float acc = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[j] = fmaf(exp2_fast(d2 * a[j]), h[i][j], du * B[i].get(j));
+      acc = fmaf(o[j], Cv[i].get(j), acc);
     }
-    Io<IO>::store(y, id, acc);
+    if (on)
+      __builtin_nontemporal_store(o, reinterpret_cast<f32x4*>(state_out + at * q.N + n));
+    else
+      acc = 0.f;
+#pragma unroll
+    for (int m = L / 2; m >= 1; m >>= 1) acc += __shfl_xor(acc, m, kWave);
+    if (n == 0) {
+      acc = fmaf(D, x[i], acc);
+      if (q.z) acc *= z[i] * sigmoid(z[i]);
+      Io<IO>::store(y, at, acc);
+    }
   }
 }
 
@@ -350,22 +362,30 @@ hipError_t launch_selective(const SelArgs& a, void* y, float* fin, float* ws, in
 }
 
 hipError_t launch_selective_step(const SelArgs& a, float* state_out, void* y, hipStream_t s) {
-  const int64_t ch = (int64_t)a.rows.R * a.C;
-  auto run = [&](auto lanes) {
-    constexpr int L = decltype(lanes)::value;
-    const unsigned nb = (unsigned)((ch * L + 255) / 256);
-    if (a.io == kIoBf16)
-      hipLaunchKernelGGL((k_sel_step<u16, L>), dim3(nb), dim3(256), 0, s, a, state_out, (u16*)y);
-    else
-      hipLaunchKernelGGL((k_sel_step<float, L>), dim3(nb), dim3(256), 0, s, a, state_out,
-                         (float*)y);
+  auto run = [&](auto io, auto lanes, auto seqs) {
+    using IO = decltype(io);
+    constexpr int L = decltype(lanes)::value, NB = decltype(seqs)::value;
+    const int64_t threads = (int64_t)((a.rows.R + NB - 1) / NB) * a.C * L;
+    hipLaunchKernelGGL((k_sel_step<IO, L, NB>), dim3((unsigned)((threads + 255) / 256)), dim3(256),
+                       0, s, a, state_out, (IO*)y);
     return hipGetLastError();
   };
-  if (a.N <= 4) return run(std::integral_constant<int, 1>{});
-  if (a.N <= 8) return run(std::integral_constant<int, 2>{});
-  if (a.N <= 16) return run(std::integral_constant<int, 4>{});
-  if (a.N <= 32) return run(std::integral_constant<int, 8>{});
-  return run(std::integral_constant<int, 16>{});
+  auto seqs = [&](auto io, auto lanes) {
+    // four sequences a thread once that leaves four waves a SIMD
+    using std::integral_constant;
+    if ((int64_t)a.rows.R * a.C * decltype(lanes)::value >= 4 * 262144)
+      return run(io, lanes, integral_constant<int, 4>{});
+    return run(io, lanes, integral_constant<int, 1>{});
+  };
+  auto lanes = [&](auto io) {
+    using std::integral_constant;
+    if (a.N <= 4) return seqs(io, integral_constant<int, 1>{});
+    if (a.N <= 8) return seqs(io, integral_constant<int, 2>{});
+    if (a.N <= 16) return seqs(io, integral_constant<int, 4>{});
+    if (a.N <= 32) return seqs(io, integral_constant<int, 8>{});
+    return seqs(io, integral_constant<int, 16>{});
+  };
+  return a.io == kIoBf16 ? lanes(u16{}) : lanes(float{});
 }
 
 }  // namespace ssd

@@ -16,11 +16,14 @@ bound) and k counts the fp32 roundings a term passes:
   additions a lane and a few waves: k = n / 32 + 64; sums over rows one a row.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import mamba_ssd_chunked_cumsum_amd as ssd
+from mamba_ssd_chunked_cumsum_amd import block as block_binding
 from oracle import block
 
 from gpu_util import DEV, note
@@ -682,3 +685,47 @@ def test_refusals_write_nothing():
             bad()
     torch.cuda.synchronize()
     assert torch.all(out == FILL)
+
+
+# ---- the variants that only large sizes take -------------------------------------------------------
+
+def test_large_batches_equal_their_parts():
+    """Many rows or sequences take longer strips, stores past the caches and several sequences a
+    thread: bit for bit what the sequences give one batch at a time."""
+    note("large batches against their parts")
+    rng = np.random.default_rng(27)
+    w, _ = value(rng, (1024, 4))
+    x = torch.randn(3, 11003, 1024, device=DEV).to(torch.bfloat16)
+    state = torch.randn(3, 3, 1024, device=DEV).to(torch.bfloat16)
+    y, f = ssd.conv(x, w, None, state)
+    for i in range(3):
+        part = x[i:i + 1, :4000].contiguous()
+        yi, fi = ssd.conv(part, w, None, state[i:i + 1].contiguous())
+        assert torch.equal(y[i:i + 1, :4000], yi) and torch.equal(fi, part[:, -3:])
+    assert torch.equal(f, x[:, -3:])
+    for Bt, Dm, N, G in ((67, 4104, 16, 1), (19, 2048, 40, 2)):
+        t, _ = selective_inputs(rng, (Bt, 1), Bt, Dm, N, G, "bf16", 8, True, True, True, True)
+        one = [t[k] if k in "AD" else t[k][:, 0] for k in NAMES]
+        kw = dict(dt_bias=t["dt_bias"], dt_softplus=True)
+        y, s = ssd.selective_step(t["h0"], *one, **kw)
+        for i in (0, 3, Bt - 1):
+            few = [v if k in "AD" else v[i:i + 1] for k, v in zip(NAMES, one)]
+            yi, si = ssd.selective_step(t["h0"][i:i + 1].contiguous(), *few, **kw)
+            assert torch.equal(y[i:i + 1], yi) and torch.equal(s[i:i + 1], si)
+
+
+def test_which_scans_are_cut_into_chunks():
+    """A long sequence of few channels needs a workspace (its rows are cut into chunks), many short
+    sequences of many channels none."""
+    note("scan plans")
+    rng = np.random.default_rng(28)
+    sizes = []
+    for Bt, L, Dm in ((1, 4096, 64), (64, 32, 4096)):
+        t, _ = selective_inputs(rng, (Bt, L), Bt, Dm, 16, 1, "bf16", 0, False, False, False, False)
+        q = block_binding._selective(t["x"], t["dt"], t["A"], t["B"], t["C"], None, None, None, None,
+                                     False, Bt, (Bt, L), t["x"].device)
+        tok, _ = block_binding._tokens(t["x"])
+        ws, _, n = block_binding._workspace("ssd_selective_scan_workspace", t["x"].device,
+                                            ctypes.byref(tok), ctypes.byref(q))
+        sizes.append(n)
+    assert sizes[0] > 0 and sizes[1] == 0
