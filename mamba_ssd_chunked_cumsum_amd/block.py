@@ -189,9 +189,12 @@ def _workspace(name, dev, *args):
     return ws, (None if ws is None else ws.data_ptr()), n.value
 
 
-def _or(t, like, shape, dtype=None):
-    """The given output, or a new one of `like`'s device (and type, unless given)."""
-    return like.new_empty(shape, dtype=dtype) if t is None else t
+def _output(given, name, like, shape, dtype):
+    """(tensor, address) of the given output, checked, or of a new one on `like`'s device."""
+    if given is None:
+        given = like.new_empty(shape, dtype=dtype)
+        return given, given.data_ptr()
+    return given, _tensor(given, name, shape, dtype, like.device)
 
 
 # ---- short causal convolution ------------------------------------------------------------------
@@ -212,12 +215,14 @@ def _parts(ts, name, sizes, lead, dtype, dev):
 
 
 def _outputs(out, split, sizes, lead, x):
+    """The tensors that the channels come in, given or new, and as _parts."""
     if out is None:
-        return tuple([x.new_empty((*lead, n)) for n in sizes])
+        out = tuple([x.new_empty((*lead, n)) for n in sizes])
+        return out, _Ptr3(*[t.data_ptr() for t in out]), _Split3(*sizes)
     out = (out,) if split is None else tuple(out)
     if len(out) != len(sizes):
         raise ValueError(f"out must hold {len(sizes)} tensors")
-    return out
+    return out, *_parts(out, "out", sizes, lead, x.dtype, x.device)
 
 
 def _silu(activation):
@@ -251,10 +256,10 @@ def conv(x, weight, bias=None, initial_state=None, *, activation="silu", split=N
     W, w, b = _conv_params(weight, bias, C, dev)
     h0 = _tensor(initial_state, "initial_state", (S, W - 1, C), x.dtype, dev)
     sizes = _split_sizes(split, C)
-    ys = _outputs(out, split, sizes, (Bt, L), x)
-    yp, sp = _parts(ys, "out", sizes, (Bt, L), x.dtype, dev)
-    fin = _or(final_out, x, (S, W - 1, C)) if want_final else None
-    fp = _tensor(fin, "final_out", (S, W - 1, C), x.dtype, dev)
+    ys, yp, sp = _outputs(out, split, sizes, (Bt, L), x)
+    fin = fp = None
+    if want_final:
+        fin, fp = _output(final_out, "final_out", x, (S, W - 1, C), x.dtype)
     _run("ssd_conv", dev, ctypes.byref(tok), xp, xs, w, b, W, _silu(activation), h0, yp, sp, fp)
     return (ys[0] if split is None else ys), fin
 
@@ -270,10 +275,8 @@ def conv_step(state, x, weight, bias=None, *, activation="silu", split=None, out
     W, w, b = _conv_params(weight, bias, C, dev)
     sp_in = _tensor(state, "state", (Bt, W - 1, C), x.dtype, dev)
     sizes = _split_sizes(split, C)
-    ys = _outputs(out, split, sizes, (Bt,), x)
-    yp, sp = _parts(ys, "out", sizes, (Bt,), x.dtype, dev)
-    so = torch.empty_like(state) if out_state is None else out_state
-    sop = _tensor(so, "out_state", (Bt, W - 1, C), x.dtype, dev)
+    ys, yp, sp = _outputs(out, split, sizes, (Bt,), x)
+    so, sop = _output(out_state, "out_state", x, (Bt, W - 1, C), x.dtype)
     _run("ssd_conv_step", dev, ctypes.byref(tok), xp, xs, w, b, W, _silu(activation), sp_in, sop,
          yp, sp)
     return (ys[0] if split is None else ys), so
@@ -344,10 +347,10 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, initial_state=None, *, dt_bia
     dev = x.device
     tok, S = _tokens(x, cu_seqlens)
     q = _selective(x, dt, A, B, C, D, z, initial_state, dt_bias, dt_softplus, S, x.shape[:2], dev)
-    y = _or(out, x, x.shape)
-    yp = _tensor(y, "out", x.shape, x.dtype, dev)
-    fin = _or(final_out, A, (S, x.shape[2], q.dstate)) if want_final else None
-    fp = _tensor(fin, "final_out", (S, x.shape[2], q.dstate), torch.float32, dev)
+    y, yp = _output(out, "out", x, x.shape, x.dtype)
+    fin = fp = None
+    if want_final:
+        fin, fp = _output(final_out, "final_out", x, (S, x.shape[2], q.dstate), torch.float32)
     t, qr = ctypes.byref(tok), ctypes.byref(q)
     ws, wp, n = _workspace("ssd_selective_scan_workspace", dev, t, qr)
     _run("ssd_selective_scan", dev, t, qr, yp, fp, wp, n)
@@ -364,10 +367,8 @@ def selective_step(state, x, dt, A, B, C, D=None, z=None, *, dt_bias=None, dt_so
         raise ValueError("state must be [batch, channels, dstate]")
     tok = SSDTokens(Bt, 1, Dm, Bt, None, io, 0)
     q = _selective(x, dt, A, B, C, D, z, state, dt_bias, dt_softplus, Bt, (Bt,), dev)
-    y = _or(out, x, (Bt, Dm))
-    so = torch.empty_like(state) if out_state is None else out_state
-    yp = _tensor(y, "out", (Bt, Dm), x.dtype, dev)
-    sop = _tensor(so, "out_state", state.shape, torch.float32, dev)
+    y, yp = _output(out, "out", x, (Bt, Dm), x.dtype)
+    so, sop = _output(out_state, "out_state", x, (Bt, Dm, q.dstate), torch.float32)
     _run("ssd_selective_step", dev, ctypes.byref(tok), ctypes.byref(q), sop, yp)
     return y, so
 
@@ -413,8 +414,7 @@ def gated_norm(x, z, weight, *, eps=1e-5, ngroups=1, norm_before_gate=False, out
     xp, xs = _rows(x, "x", x.shape, x.dtype, dev)
     zp, zs = _rows(z, "z", x.shape, x.dtype, dev)
     w = _tensor(weight, "weight", x.shape[2:], torch.float32, dev)
-    y = _or(out, x, x.shape)
-    yp = _tensor(y, "out", x.shape, x.dtype, dev)
+    y, yp = _output(out, "out", x, x.shape, x.dtype)
     _run("ssd_gated_norm", dev, ctypes.byref(tok), xp, xs, zp, zs, w, ngroups, eps,
          1 if norm_before_gate else 0, yp)
     return y
@@ -468,9 +468,8 @@ def residual_norm(x, residual, weight, *, scale=None, eps=1e-5, residual_dtype=N
     rp = _tensor(residual, "residual", x.shape, rt, dev)
     w = _tensor(weight, "weight", x.shape[2:], torch.float32, dev)
     sc = _tensor(scale, "scale", x.shape[2:], torch.float32, dev)
-    y, r = _or(out, x, x.shape), _or(residual_out, x, x.shape, rt)
-    yp = _tensor(y, "out", x.shape, x.dtype, dev)
-    op = _tensor(r, "residual_out", x.shape, rt, dev)
+    y, yp = _output(out, "out", x, x.shape, x.dtype)
+    r, op = _output(residual_out, "residual_out", x, x.shape, rt)
     _run("ssd_residual_norm", dev, ctypes.byref(tok), xp, xs, rp, DTYPES[rt], sc, w, eps, yp, op)
     return y, r
 

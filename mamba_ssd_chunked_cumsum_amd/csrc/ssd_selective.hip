@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan(SelArgs q, Plan pl, int un
   int r0, r1;
   if (pl.len && u < pl.chunks) {
     r0 = u * pl.len;
-    r1 = min(r0 + pl.len, q.rows.R);
+    r1 = q.rows.R - r0 > pl.len ? r0 + pl.len : q.rows.R;  // (r0 + len may pass 31 bits)
   } else {
     const int s = pl.len ? u - pl.chunks : u;
     r0 = seq_begin(q.rows, s);
@@ -315,7 +315,7 @@ Plan plan(const SelArgs& a, int n_cu) {
     const int64_t len = ((a.rows.R + chunks - 1) / chunks + 3) / 4 * 4;
     if (len < kMinLen && w > 1) continue;
     pl.len = (int)(len < kMinLen ? kMinLen : len);
-    pl.chunks = (a.rows.R + pl.len - 1) / pl.len;
+    pl.chunks = (int)(((int64_t)a.rows.R + pl.len - 1) / pl.len);
     break;
   }
   if (pl.chunks < 2) pl.len = pl.chunks = 0;

@@ -729,3 +729,49 @@ def test_which_scans_are_cut_into_chunks():
                                             ctypes.byref(tok), ctypes.byref(q))
         sizes.append(n)
     assert sizes[0] > 0 and sizes[1] == 0
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 elements: the last sequence is what it is alone. The selective scan
+    may be cut differently there, so its outputs are held to two roundings of bf16 of the largest
+    value; the others are equal bit for bit."""
+    note("offsets beyond 32 bits")
+    S, L, C, N = 2701, 100, 8192, 4
+    assert S * L * C > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(29)
+
+    def act():
+        t = torch.empty(S, L, C, dtype=torch.bfloat16, device=DEV)
+        return t.normal_(generator=g)
+
+    def last(t):
+        return t[-1:].contiguous()
+
+    x, z, dy = act(), act(), act()
+    w = torch.randn(C, 4, device=DEV, generator=g)
+    nw = torch.randn(C, device=DEV, generator=g)
+    A = -torch.rand(C, N, device=DEV, generator=g)
+    B = torch.empty(S, L, 1, N, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    pairs = [
+        (lambda x, z, dy: ssd.conv(x, w, nw)[0], True),
+        (lambda x, z, dy: ssd.conv_backward(x, w, nw, dy)["dx"], True),
+        (lambda x, z, dy: ssd.gated_norm(x, z, nw), True),
+        (lambda x, z, dy: ssd.gated_norm_backward(x, z, nw, dy)["dz"], True),
+        (lambda x, z, dy: ssd.residual_norm(x, z, nw)[1], True),
+        (lambda x, z, dy: ssd.residual_norm_backward(x, z, nw, dy)["dx"], True),
+        (lambda x, z, dy: ssd.selective_scan(x, z, A, B[-x.shape[0]:], B[-x.shape[0]:], nw, z,
+                                             dt_softplus=True, want_final=False)[0], False),
+        (lambda x, z, dy: ssd.selective_backward(x, z, A, B[-x.shape[0]:], B[-x.shape[0]:], nw, z,
+                                                 dy, dt_softplus=True)["ddt"], False),
+    ]
+    for i, (call, same) in enumerate(pairs):
+        got = last(call(x, z, dy))
+        want = call(last(x), last(z), last(dy))
+        if same:
+            assert torch.equal(got, want), i
+        else:
+            err = (got.float() - want.float()).abs().max()
+            assert err <= 2 * torch.finfo(got.dtype).eps * want.float().abs().max(), (i, err)
+        del got, want
+    del x, z, dy, B, pairs
+    torch.cuda.empty_cache()
