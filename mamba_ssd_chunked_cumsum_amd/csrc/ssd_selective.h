@@ -4,28 +4,8 @@
 
 namespace ssd {
 
-// ---- work split ----------------------------------------------------------------------------------
-// A block of 256 threads takes kCh channels of one group and a range of rows. K lanes share a
-// channel, each with NPL of its states (lane = K * channel + k, states k NPL .. k NPL + NPL - 1;
-// past dstate they are zero: A = 0, B = 0).
-constexpr int kSelThreads = 256;
-
+// The hardware's exponential, one unit in the last place; arguments are products with log2(e).
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
-
-// Sum over the K (4, 8 or 16) lanes that share a channel, in every one of them.
-template <int CTRL>
-__device__ __forceinline__ float add_dpp(float v) {
-  return v + __int_as_float(
-                 __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-template <int K>
-__device__ __forceinline__ float sum_lanes(float v) {
-  v = add_dpp<0xB1>(v);                      // quad_perm [1,0,3,2]
-  v = add_dpp<0x4E>(v);                      // quad_perm [2,3,0,1]
-  if constexpr (K >= 8) v = add_dpp<0x141>(v);   // row_half_mirror
-  if constexpr (K >= 16) v = add_dpp<0x140>(v);  // row_mirror
-  return v;
-}
 
 // ---- a channel a lane, all its states in registers -------------------------------------------------
 // B or C of a token: N state entries at p, uniform over the wave. NT: N rounded up to a template's
@@ -87,6 +67,26 @@ __device__ __forceinline__ void store_all(float* p, int N, const float (&h)[NT])
 }
 
 // ---- K lanes a channel -----------------------------------------------------------------------------
+// A block of 256 threads takes 256 / K channels of one group and a range of rows; K lanes share a
+// channel, each with NPL of its states (lane = K * channel + k, states k NPL .. k NPL + NPL - 1; past
+// dstate they are zero: A = 0, B = 0).
+constexpr int kSelThreads = 256;
+
+// Sum over the K (4, 8 or 16) lanes that share a channel, in every one of them.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(
+                 __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int K>
+__device__ __forceinline__ float sum_lanes(float v) {
+  v = add_dpp<0xB1>(v);                      // quad_perm [1,0,3,2]
+  v = add_dpp<0x4E>(v);                      // quad_perm [2,3,0,1]
+  if constexpr (K >= 8) v = add_dpp<0x141>(v);   // row_half_mirror
+  if constexpr (K >= 16) v = add_dpp<0x140>(v);  // row_mirror
+  return v;
+}
+
 // Starts and ends of sequences among the rows [r, r + 64) of a wave, as bit masks; rows at or past
 // `stop` count as neither.
 __device__ __forceinline__ void mark_rows(const Rows& q, int r, int stop, uint64_t& starts,

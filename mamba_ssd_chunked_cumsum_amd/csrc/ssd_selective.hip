@@ -5,9 +5,9 @@
 //
 // For each (token, channel, state entry) one exponential, two products and two fused
 // multiply-adds. With a different decay for every state entry no matrix product covers several
-// tokens, so the vector units and their transcendental rate bound it (measured at four waves a
-// SIMD: an exponential of 64 lanes takes 10.6 cycles, another operation 3.1: 23 cycles for 64
-// entries of one token).
+// tokens, so the vector units bound it: 8 cycles of a SIMD for the exponential and 4 for each of the
+// others (from counters), 24 for 64 entries of a token, 214 us at 2 x 8192 tokens x 5120 channels x
+// 16 entries if nothing else were done.
 //
 // A lane holds one channel with all its states in registers and a wave 64 neighbouring channels, so
 // the sum over n needs no exchange between lanes, and B and C of a token are the same for the whole
@@ -16,7 +16,10 @@
 // channels and sequences, and where those do not fill the card the rows are cut into chunks (split
 // variant): one kernel computes each chunk's end state from a zero state and the sum of its delta,
 // one chains the chunks (the decay of a whole chunk is exp(A sum delta)), and the scan starts every
-// chunk from the state entering it. That evaluates the exponentials twice.
+// chunk from the state entering it. That evaluates the exponentials twice. At the size above (bf16,
+// gated): 250 us the end states, 10 the chain, 330 the scan, with the vector units busy 90 to 95% of
+// the time; 565 us a call. 64 x 5120 x 16 single tokens: 11 us, 4.1 TB/s. (Four lanes a channel with
+// tiles in LDS and one wave on most SIMDs, the first version, took 2031 us.)
 #include <cmath>
 
 #include "ssd_selective.h"
