@@ -14,8 +14,8 @@
 // quarters from the last to the first, forward from the quarter's entering state, keeping h and a
 // of its 16 tokens in registers, and back. So each exponential is evaluated twice and nothing of size
 // tokens x channels x dstate goes to memory; the vector units bound it. At 2 x 4096 tokens x 5120
-// channels x 16 entries (bf16, gated): 190 us the first kernel, 38 the chain, 650 the main kernel
-// (vector units busy 76%: h and a leave room for two waves a SIMD), 18 + 11 the sums; 872 us a call.
+// channels x 16 entries (bf16, gated): 190 us the first kernel, 38 the chain, 635 the main kernel
+// (vector units busy 76%: h and a leave room for two waves a SIMD), 18 + 11 the sums; 857 us a call.
 //
 // dB and dC sum over channels, i.e. over lanes: sums over the 16 channels of a wave are formed 16
 // values at a time, each step adding two lanes' values and merging two registers into one, so
@@ -472,6 +472,21 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
   const int mine = merged_value<K>();
   // events: a sequence begins or ends in the chunk. Where none does (`quiet`), no branch separates
   // the tokens and the loads and products of several overlap.
+  struct Token {
+    float dl, du, e, b[NPL], c[NPL];
+  };
+  auto staged = [&](int t) {
+    Token m;
+    m.dl = s_dl[t][ch];
+    m.du = s_du[t][ch];
+    m.e = s_e[t][ch];
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+      m.b[j] = s_b[t][k * NPL + j];
+      m.c[j] = s_c[t][k * NPL + j];
+    }
+    return m;
+  };
   auto walk = [&](auto quiet) {
     constexpr bool EV = !decltype(quiet)::value;
 #pragma unroll
@@ -499,6 +514,7 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
           __builtin_amdgcn_sched_barrier(0);  // loads of later tokens would cost registers here
       }
       asm volatile("" ::: "memory");  // and so would what was loaded above, kept for its reuse below
+      Token next = staged(s * T + T - 1);
       float vals[MV < 8 ? 8 : MV];  // dB of the four entries, then dC; K 4: of two tokens
 #pragma unroll
       for (int i = T - 1; i >= 0; --i) {
@@ -509,13 +525,15 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
         for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
         const bool start = EV && ((starts >> t) & 1);
         if (start) seq_states(q, q.h0, r0 + t, c, k, live, prev);
-        const float dl = s_dl[t][ch], du = s_du[t][ch], e = s_e[t][ch];
+        const Token m = next;
+        if (i) next = staged(t - 1);  // a token ahead
+        const float dl = m.dl, du = m.du, e = m.e;
         float qs = 0.f, sa = 0.f;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-          const float G = fmaf(s_c[t][k * NPL + j], e, g[j]);
+          const float G = fmaf(m.c[j], e, g[j]);
           const float aG = a[i][j] * G, wv = aG * prev[j];
-          qs = fmaf(G, s_b[t][k * NPL + j], qs);
+          qs = fmaf(G, m.b[j], qs);
           sa = fmaf(wv, A[j], sa);
           dA[j] = fmaf(wv, dl, dA[j]);
           g[j] = aG;
@@ -546,7 +564,7 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
 #pragma unroll
           for (int j = 0; j < NPL; ++j) g[j] = 0.f;
         }
-        if (EV || (i & 1) == 0) __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();
       for (int v = threadIdx.x; v < T * 2 * NP; v += kSelThreads) {
