@@ -317,7 +317,7 @@ ssd_status ssd_conv_backward(const ssd_tokens* t, const void* x, int64_t x_strid
   st = with_workspace(workspace, workspace_bytes, need);
   if (st != SSD_OK) return st;
   if (!b.fine()) return SSD_ERR_INVALID_ARGUMENT;
-  if (!grid_fits((double(a.C) / 256 + 1) * (double(a.rows.R) / 256 + 1) +
+  if (!grid_fits((double(a.C) / 256 + 1) * (double(a.rows.R) / 512 + 1) + 1024 +
                      double(a.rows.S) * (a.C / 4) / 256 + 1, 256))
     return SSD_ERR_UNSUPPORTED;
   st = device_ready();

@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kBlock) void k_conv_step(ConvArgs q, IO* state_out)
 // still incomplete: dv[t] adds w[W - 1 - i] dv[t] to the gradient of x[t - i]. Sums over rows (dw,
 // db) are kept in registers for the strip's own rows, added over the block's four strips in LDS and
 // written as one partial per block, which a second kernel sums in a fixed order.
-constexpr int kBwdV = 4, kBwdWaves = 4, kBwdStrip = 128;
+constexpr int kBwdV = 4, kBwdWaves = 4;
 static_assert(64 * kBwdWaves == kBlock, "the trailing blocks count threads in kBlock");
 
 template <typename IO, typename DY, int W>
@@ -258,7 +258,7 @@ __device__ __forceinline__ void conv_dinit(const ConvArgs& q, const float* dfina
 template <typename IO, typename DY, int W>
 __global__ __launch_bounds__(64 * kBwdWaves) void k_conv_bwd(ConvArgs q, const float* dfinal,
                                                              IO* dx, float* part, float* dinit,
-                                                             int nvb, int nsb) {
+                                                             int nvb, int nsb, int strip) {
   constexpr int V = kBwdV, U = 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const unsigned block = blockIdx.x;
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_conv_bwd(ConvArgs q, const f
   for (int k = 0; k <= W; ++k)
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[k][i] = 0.f;
-  const int r0 = (sb * kBwdWaves + wave) * kBwdStrip, r1 = min(r0 + kBwdStrip, q.rows.R);
+  const int r0 = (sb * kBwdWaves + wave) * strip, r1 = min(r0 + strip, q.rows.R);
   if (live && r0 < r1) {
     int width, col;
     const int pi = split_of(q.y, c, &width, &col);
@@ -398,8 +398,17 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_conv_bwd(ConvArgs q, const f
 
 unsigned blocks_of(int64_t threads) { return (unsigned)((threads + kBlock - 1) / kBlock); }
 
-int conv_bwd_blocks(int R) {
-  return (R + kBwdStrip * kBwdWaves - 1) / (kBwdStrip * kBwdWaves);
+// Rows a backward strip: 128, or as many fewer (8 at least) as it takes for 512 blocks, two a compute
+// unit (5882 rows x 784 channels: 147 us with 48 blocks of 128-row strips).
+int conv_bwd_strip(const ConvArgs& a) {
+  const int64_t nvb = (a.C / kBwdV + 63) / 64;
+  int strip = 128;
+  while (strip > 8 && nvb * (a.rows.R / (strip * kBwdWaves)) < 512) strip /= 2;
+  return strip;
+}
+int conv_bwd_blocks(const ConvArgs& a) {
+  const int rows = conv_bwd_strip(a) * kBwdWaves;
+  return (a.rows.R + rows - 1) / rows;
 }
 
 template <typename F>
@@ -447,16 +456,17 @@ hipError_t launch_conv_step(const ConvArgs& a, void* state_out, hipStream_t s) {
 }
 
 int64_t conv_backward_bytes(const ConvArgs& a) {
-  return (int64_t)conv_bwd_blocks(a.rows.R) * (a.W + 1) * a.C * 4;
+  return (int64_t)conv_bwd_blocks(a) * (a.W + 1) * a.C * 4;
 }
 
 template <typename IO, typename DY, int W>
 static hipError_t conv_backward(const ConvArgs& a, const float* dfinal, void* dx, float* dw,
                                 float* db, float* dinit, float* ws, hipStream_t s) {
-  const int nvb = (a.C / kBwdV + 63) / 64, nsb = conv_bwd_blocks(a.rows.R);
+  const int nvb = (a.C / kBwdV + 63) / 64, nsb = conv_bwd_blocks(a);
   const int64_t tail = dinit ? ((int64_t)a.rows.S * (a.C / kBwdV) + kBlock - 1) / kBlock : 0;
   hipLaunchKernelGGL((k_conv_bwd<IO, DY, W>), dim3((unsigned)((int64_t)nvb * nsb + tail)),
-                     dim3(64 * kBwdWaves), 0, s, a, dfinal, (IO*)dx, ws, dinit, nvb, nsb);
+                     dim3(64 * kBwdWaves), 0, s, a, dfinal, (IO*)dx, ws, dinit, nvb, nsb,
+                     conv_bwd_strip(a));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_column_sums(ws, nsb, (int64_t)W * a.C, dw, a.C, 1, W, a.C, db, 0, nullptr, s);

@@ -124,11 +124,12 @@ __device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int
 // As the forward's chunk states: a lane holds a channel, B and C come through scalar loads. NT: up to
 // 16 states; of more, other waves take the others.
 // EVENTS: the chunks in which a sequence begins after the first row or ends before the last; the
-// others take a launch of their own, whose waves need fewer registers (126 against 155: four of them
-// on a SIMD against three).
+// others take a launch of their own, whose waves need fewer registers (122 against 145: four of them
+// on a SIMD against three). `all`: every chunk, where the launch has no more waves than fit the card
+// at once and two launches would only follow one another (4 x 71 tokens x 2432: 27 and 29 us).
 template <typename IO, int NT, bool EXACT, bool EVENTS>
 __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* dy,
-                                                  const float* dfinal) {
+                                                  const float* dfinal, int all) {
   constexpr int U = 4;  // tokens whose loads are in flight
   const int cg = q.C / q.G, tiles = (cg + 63) / 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
   const int r0 = u * kChunk, r1 = min(r0 + kChunk, q.rows.R);
   const int s0 = seq_of(q.rows, r0);
   const bool quiet = r1 - r0 == kChunk && s0 >= 0 && seq_end(q.rows, s0) >= r1;
-  if (quiet == EVENTS) return;
+  if (quiet == EVENTS && !(EVENTS && all)) return;
   const int64_t CN = (int64_t)q.C * q.N, at = (int64_t)c * q.N + n0;
   float A[NT], h[NT], p[NT], gl[NT], sum = 0.f;
   load_all<NT>(q.A + at, N, A);
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
   else if (seq_begin(q.rows, s0) == r0) begin(s0);
   fetch();
 #pragma unroll 1
-  for (int t = 0; t < (inside ? kChunk : 0); t += U) {
+  for (int t = 0; t < (inside ? r1 - r0 : 0); t += U) {
     if (t && t % kQuarter == 0) write_quarter(t / kQuarter - 1);
     unpack();
     fetch();
@@ -491,6 +492,7 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
     constexpr bool EV = !decltype(quiet)::value;
 #pragma unroll
     for (int s = 3; s >= 0; --s) {
+      if (EV && s * T >= r1 - r0) continue;  // of a short last chunk
       float hn[T][NPL], a[T][NPL];  // h after each token, its decay
 #pragma unroll
       for (int i = 0; i < T; ++i) {
@@ -728,12 +730,13 @@ hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const flo
       const int64_t waves = (int64_t)((cg + 63) / 64) * a.G * w.chunks * ((a.N + NT - 1) / NT);
       constexpr bool EX = decltype(exact)::value;
       const dim3 grid((unsigned)((waves + 3) / 4));
-      if (a.rows.starts || a.rows.L >= kChunk)
+      const bool events = a.rows.starts || a.rows.L % kChunk, all = events && waves <= 3072;
+      if (!all && (a.rows.starts || a.rows.L >= kChunk))
         hipLaunchKernelGGL((k_bwd_ends<IO, NT, EX, false>), grid, dim3(256), 0, s, a, w,
-                           (const IO*)dy, dfinal);
-      if (a.rows.starts || a.rows.L % kChunk)
+                           (const IO*)dy, dfinal, 0);
+      if (events)
         hipLaunchKernelGGL((k_bwd_ends<IO, NT, EX, true>), grid, dim3(256), 0, s, a, w,
-                           (const IO*)dy, dfinal);
+                           (const IO*)dy, dfinal, all ? 1 : 0);
       return hipGetLastError();
     };
     using std::integral_constant;

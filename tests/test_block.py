@@ -775,3 +775,32 @@ def test_offsets_beyond_32_bits():
         del got, want
     del x, z, dy, B, pairs
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("lens", [None, (96, 1, 700, 64, 0, 2000, 979)])
+def test_selective_backward_of_many_channels_equals_its_parts(lens):
+    """Many channels (chunks with and without sequence boundaries in launches of their own) against a
+    call with a few of them, which are independent but for dB and dC: to 2^-17 of the largest
+    value, some tens of fp32 roundings."""
+    note("selective backward, many channels")
+    rng = np.random.default_rng(30)
+    C, N, few = 4096, 16, slice(1984, 2112)
+    Bt, L = (40, 96) if lens is None else (1, sum(lens))
+    seqs, cu = ranges(batch=Bt, L=L) if lens is None else ranges(lens=lens)
+    S = len(seqs)
+    t, _ = selective_inputs(rng, (Bt, L), S, C, N, 1, "f32", 0, True, True, True, True)
+    dy, _ = value(rng, (Bt, L, C))
+    df, _ = value(rng, (S, C, N))
+    kw = dict(dt_softplus=True, cu_seqlens=cu)
+    g = ssd.selective_backward(*(t[k] for k in NAMES), dy, t["h0"], df, dt_bias=t["dt_bias"], **kw)
+
+    def cut(v):
+        return v[..., few].contiguous()
+
+    p = ssd.selective_backward(cut(t["x"]), cut(t["dt"]), t["A"][few].contiguous(), t["B"], t["C"],
+                               cut(t["D"]), cut(t["z"]), cut(dy), t["h0"][:, few].contiguous(),
+                               df[:, few].contiguous(), dt_bias=cut(t["dt_bias"]), **kw)
+    for k in ("dx", "ddt", "dz", "dD", "ddt_bias", "dA", "dinitial_state"):
+        whole = g[k][few] if k == "dA" else g[k][:, few] if k == "dinitial_state" else cut(g[k])
+        err = (whole - p[k]).abs().max()
+        assert err <= 2.0 ** -17 * p[k].abs().max(), (k, err)
