@@ -294,7 +294,7 @@ __global__ __launch_bounds__(256) void k_sel_step(SelArgs q, float* state_out, I
   }
 }
 
-constexpr int kMinLen = 32;  // rows of a chunk
+constexpr int kMinLen = 32;  // rows of a chunk with several waves a SIMD
 
 int64_t tiles_of(const SelArgs& a) { return (int64_t)((a.C / a.G + 63) / 64) * a.G; }
 
@@ -302,7 +302,8 @@ int64_t tiles_of(const SelArgs& a) { return (int64_t)((a.C / a.G + 63) / 64) * a
 // together do; a row costs about 28 cycles a state entry with the SIMD full, as much again for the
 // split's first pass, whose chain and extra launches cost about 15 us more. The chunks make the
 // largest number of waves up to four a SIMD that leaves them 32 rows or more: just over a whole
-// number of waves a SIMD would leave most of the card idle for the last of them.
+// number of waves a SIMD would leave most of the card idle for the last of them. Where even one wave a
+// SIMD leaves fewer, time goes by the rows of a wave, and chunks go down to 8.
 Plan plan(const SelArgs& a, int n_cu) {
   Plan pl{0, 0, nullptr, nullptr};
   const double simds = 4.0 * n_cu, row = 28.0 * (a.N < 8 ? 8 : a.N);
@@ -317,7 +318,7 @@ Plan plan(const SelArgs& a, int n_cu) {
     if (chunks < 2) break;
     const int64_t len = ((a.rows.R + chunks - 1) / chunks + 3) / 4 * 4;
     if (len < kMinLen && w > 1) continue;
-    pl.len = (int)(len < kMinLen ? kMinLen : len);
+    pl.len = (int)(len < 8 ? 8 : len);
     pl.chunks = (int)(((int64_t)a.rows.R + pl.len - 1) / pl.len);
     break;
   }

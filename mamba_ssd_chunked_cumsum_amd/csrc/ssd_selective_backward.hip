@@ -122,7 +122,7 @@ __device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int
 
 // ---- chunk ends ----------------------------------------------------------------------------------
 // As the forward's chunk states: a lane holds a channel, B and C come through scalar loads. NT: up to
-// 16 states; of more, other waves take the others.
+// 16 states; of more (4 where the launch is small) other waves take the others.
 // EVENTS: the chunks in which a sequence begins after the first row or ends before the last; the
 // others take a launch of their own, whose waves need fewer registers (122 against 145: four of them
 // on a SIMD against three). `all`: every chunk, where the launch has no more waves than fit the card
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
     const Rows2 next = rows();  // a token ahead
     const float du = dl[i] * x[i];
     sum += dl[i];
-    constexpr int GR = 8;
+    constexpr int GR = NT < 8 ? NT : 8;
 #pragma unroll
     for (int n = 0; n < NT; n += GR) {
       float a[GR], v[GR];
@@ -740,9 +740,12 @@ hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const flo
       return hipGetLastError();
     };
     using std::integral_constant;
-    hipError_t e = a.N % 16 == 0 ? ends(integral_constant<int, 16>{}, std::true_type{})
-                   : a.N <= 8    ? ends(integral_constant<int, 8>{}, std::false_type{})
-                                 : ends(integral_constant<int, 16>{}, std::false_type{});
+    // four entries a lane where that still fits the card at once: shorter for each token
+    const int64_t fours = (int64_t)((cg + 63) / 64) * a.G * w.chunks * (a.N / 4);
+    hipError_t e = fours <= 2048   ? ends(integral_constant<int, 4>{}, std::true_type{})
+                   : a.N % 16 == 0 ? ends(integral_constant<int, 16>{}, std::true_type{})
+                   : a.N <= 8      ? ends(integral_constant<int, 8>{}, std::false_type{})
+                                   : ends(integral_constant<int, 16>{}, std::false_type{});
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_bwd_chain, dim3((unsigned)((CN + 255) / 256), 2), dim3(256), 0, s, a, w);
     e = by_states(a.N, [&](auto lanes) {
