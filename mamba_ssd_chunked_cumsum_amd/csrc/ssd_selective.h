@@ -87,24 +87,17 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
-// Starts and ends of sequences among the rows [r, r + 64) of a wave, as bit masks; rows at or past
-// `stop` count as neither.
+// Starts and ends of sequences among the rows [r, r + 64), as bit masks of the wave, which rows are
+// in a sequence, and in which (a row a lane: seq_at); rows at or past `stop` are in none.
 __device__ __forceinline__ void mark_rows(const Rows& q, int r, int stop, uint64_t& starts,
-                                          uint64_t& ends, uint64_t& inside) {
+                                          uint64_t& ends, uint64_t& inside, int& seq) {
   const int row = r + (threadIdx.x & 63);
-  bool st = false, en = false, in = false;
-  if (row < stop) {
-    const int s = seq_of(q, row);
-    if (s >= 0) {
-      in = true;
-      st = row == seq_begin(q, s);
-      en = row == seq_end(q, s) - 1;
-    }
-  }
-  starts = __ballot(st);
-  ends = __ballot(en);
-  inside = __ballot(in);
+  seq = row < stop ? seq_of(q, row) : -1;
+  starts = __ballot(seq >= 0 && row == seq_begin(q, max(seq, 0)));
+  ends = __ballot(seq >= 0 && row == seq_end(q, max(seq, 0)) - 1);
+  inside = __ballot(seq >= 0);
 }
+__device__ __forceinline__ int seq_at(int seq, int t) { return __builtin_amdgcn_readlane(seq, t); }
 
 template <int NPL>
 __device__ __forceinline__ void load_states(const float* p, int k, int N, float (&h)[NPL]) {

@@ -110,12 +110,11 @@ __device__ __forceinline__ void stage(const SelArgs& q, const IO* dy, const Tile
   }
 }
 
-__device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int row, int c, int k,
+__device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int s, int c, int k,
                                            bool live, float (&h)[NPL]) {
 #pragma unroll
   for (int j = 0; j < NPL; ++j) h[j] = 0.f;
   if (p && live) {
-    const int s = seq_of(q.rows, row);
     load_states<NPL>(p + ((int64_t)s * q.C + c) * q.N, k, q.N, h);
   }
 }
@@ -267,7 +266,8 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
     if (n0 == 0) w.sums[slot * q.C + c] = began ? none : sum;
   };
   uint64_t starts = 0, ends = 0, inside = ~uint64_t(0);
-  if (EVENTS) mark_rows(q.rows, r0, r1, starts, ends, inside);
+  int seq = -1;
+  if (EVENTS) mark_rows(q.rows, r0, r1, starts, ends, inside, seq);
   else if (seq_begin(q.rows, s0) == r0) begin(s0);
   fetch();
 #pragma unroll 1
@@ -279,10 +279,10 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
     for (int i = 0; i < U; ++i) {
       if (EVENTS) {
         if (!((inside >> (t + i)) & 1)) dl[i] = x[i] = e[i] = 0.f;  // decays nothing, adds nothing
-        if ((starts >> (t + i)) & 1) begin(seq_of(q.rows, r0 + t + i));
+        if ((starts >> (t + i)) & 1) begin(seq_at(seq, t + i));
       }
       token(i);
-      if (EVENTS && ((ends >> (t + i)) & 1)) finish(seq_of(q.rows, r0 + t + i));
+      if (EVENTS && ((ends >> (t + i)) & 1)) finish(seq_at(seq, t + i));
     }
   }
   if (!EVENTS && seq_end(q.rows, s0) == r1) finish(s0);
@@ -441,7 +441,8 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
   const bool live = c < b.stop;
   const int r0 = u * TC, r1 = min(r0 + TC, q.rows.R);
   uint64_t starts, ends, inside;
-  mark_rows(q.rows, r0, r1, starts, ends, inside);
+  int seq;
+  mark_rows(q.rows, r0, r1, starts, ends, inside, seq);
   float* part = w.part + (int64_t)u * q.C * (q.N + 2);
   if (!inside) {  // rows of no sequence
     leave_empty<IO, K>(q, o, b, r0, r1, part);
@@ -500,7 +501,7 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
         float prev[NPL];
 #pragma unroll
         for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
-        if (EV && ((starts >> t) & 1)) seq_states(q, q.h0, r0 + t, c, k, live, prev);
+        if (EV && ((starts >> t) & 1)) seq_states(q, q.h0, seq_at(seq, t), c, k, live, prev);
         const float dl = s_dl[t][ch], du = s_du[t][ch];
         float y = 0.f;
 #pragma unroll
@@ -521,12 +522,12 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
 #pragma unroll
       for (int i = T - 1; i >= 0; --i) {
         const int t = s * T + i;
-        if (EV && ((ends >> t) & 1)) seq_states(q, dfinal, r0 + t, c, k, live, g);
+        if (EV && ((ends >> t) & 1)) seq_states(q, dfinal, seq_at(seq, t), c, k, live, g);
         float prev[NPL];
 #pragma unroll
         for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
         const bool start = EV && ((starts >> t) & 1);
-        if (start) seq_states(q, q.h0, r0 + t, c, k, live, prev);
+        if (start) seq_states(q, q.h0, seq_at(seq, t), c, k, live, prev);
         const Token m = next;
         if (i) next = staged(t - 1);  // a token ahead
         const float dl = m.dl, du = m.du, e = m.e;
@@ -560,8 +561,7 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
         (k & 1 ? s_e : s_du)[t][ch] = k & 1 ? sa : qs;
         if (start) {
           if (o.dh0 && live) {
-            const int sq = seq_of(q.rows, r0 + t);
-            store_states<NPL>(o.dh0 + ((int64_t)sq * q.C + c) * q.N, k, q.N, g);
+            store_states<NPL>(o.dh0 + ((int64_t)seq_at(seq, t) * q.C + c) * q.N, k, q.N, g);
           }
 #pragma unroll
           for (int j = 0; j < NPL; ++j) g[j] = 0.f;
