@@ -29,6 +29,7 @@ namespace {
 
 // States a lane; rows a chunk and a quarter of it, so that a quarter's h and a take 128 registers.
 constexpr int NPL = 4, kQuarter = 16, kChunk = 4 * kQuarter;
+constexpr int64_t kOneLaunch = 12 * 1024;  // waves of k_bwd_ends: twelve a SIMD of the card's 1024
 
 struct Work {
   int chunks;
@@ -124,8 +125,10 @@ __device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int
 // 16 states; of more (4 where the launch is small) other waves take the others.
 // EVENTS: the chunks in which a sequence begins after the first row or ends before the last; the
 // others take a launch of their own, whose waves need fewer registers (122 against 145: four of them
-// on a SIMD against three). `all`: every chunk, where the launch has no more waves than fit the card
-// at once and two launches would only follow one another (4 x 71 tokens x 2432: 27 and 29 us).
+// on a SIMD against three). `all`: every chunk in the one launch. Two follow one another, and the
+// second is a chunk's latency however few chunks it has; the fewer registers pay only over many
+// rounds of waves (the whole backward, two launches and one: 1536 channels x 2041 tokens 161 and 130
+// us, x 5497 255 and 225, x 24569, 9200 waves, 830 and 822; 5120 x 16377, 20500 waves, 1695 and 1724).
 template <typename IO, int NT, bool EXACT, bool EVENTS>
 __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* dy,
                                                   const float* dfinal, int all) {
@@ -730,7 +733,7 @@ hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const flo
       const int64_t waves = (int64_t)((cg + 63) / 64) * a.G * w.chunks * ((a.N + NT - 1) / NT);
       constexpr bool EX = decltype(exact)::value;
       const dim3 grid((unsigned)((waves + 3) / 4));
-      const bool events = a.rows.starts || a.rows.L % kChunk, all = events && waves <= 3072;
+      const bool events = a.rows.starts || a.rows.L % kChunk, all = events && waves <= kOneLaunch;
       if (!all && (a.rows.starts || a.rows.L >= kChunk))
         hipLaunchKernelGGL((k_bwd_ends<IO, NT, EX, false>), grid, dim3(256), 0, s, a, w,
                            (const IO*)dy, dfinal, 0);

@@ -804,3 +804,36 @@ def test_selective_backward_of_many_channels_equals_its_parts(lens):
         whole = g[k][few] if k == "dA" else g[k][:, few] if k == "dinitial_state" else cut(g[k])
         err = (whole - p[k]).abs().max()
         assert err <= 2.0 ** -17 * p[k].abs().max(), (k, err)
+
+
+@pytest.mark.parametrize("lens", [None, (96, 1, 700, 64, 0, 300, 579)])
+def test_selective_backward_of_many_groups_equals_its_parts(lens):
+    """Many waves (chunks with and without sequence boundaries in launches of their own) against calls
+    with one group, which shares nothing with the others: to 2^-17 of the largest value, some tens
+    of fp32 roundings."""
+    note("selective backward, many groups")
+    rng = np.random.default_rng(31)
+    G, cg, N = 128, 8, 64
+    Bt, L = (5, 350) if lens is None else (1, sum(lens))
+    seqs, cu = ranges(batch=Bt, L=L) if lens is None else ranges(lens=lens)
+    S, C = len(seqs), G * cg
+    t, _ = selective_inputs(rng, (Bt, L), S, C, N, G, "f32", 0, True, True, True, True)
+    dy, _ = value(rng, (Bt, L, C))
+    df, _ = value(rng, (S, C, N))
+    kw = dict(dt_softplus=True, cu_seqlens=cu)
+    g = ssd.selective_backward(*(t[k] for k in NAMES), dy, t["h0"], df, dt_bias=t["dt_bias"], **kw)
+    for i in (0, 77, G - 1):
+        few = slice(i * cg, (i + 1) * cg)
+
+        def cut(k, v):
+            if k in ("B", "C", "dB", "dC"):
+                return v[:, :, i:i + 1].contiguous()
+            if k in ("A", "dA"):
+                return v[few].contiguous()
+            return v[:, few].contiguous() if k in ("h0", "dinitial_state") else v[..., few].contiguous()
+
+        p = ssd.selective_backward(*(cut(k, t[k]) for k in NAMES), cut("dy", dy), cut("h0", t["h0"]),
+                                   cut("h0", df), dt_bias=cut("dt_bias", t["dt_bias"]), **kw)
+        for k in p:
+            err = (cut(k, g[k]) - p[k]).abs().max()
+            assert err <= 2.0 ** -17 * p[k].abs().max(), (i, k, err)
