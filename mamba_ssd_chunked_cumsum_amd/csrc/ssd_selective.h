@@ -27,6 +27,12 @@ struct Row {
       }
     }
   }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < NT / 4; ++i)
+#pragma unroll
+      for (int j = 0; j < kW; ++j) u[i][j] = 0;
+  }
   __device__ __forceinline__ float get(int n) const {
     if constexpr (sizeof(IO) == 4) return __uint_as_float(u[n / 4][n % 4]);
     else return __uint_as_float(n & 1 ? u[n / 4][n % 4 / 2] & 0xffff0000u : u[n / 4][n % 4 / 2] << 16);

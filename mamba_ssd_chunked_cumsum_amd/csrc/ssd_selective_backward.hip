@@ -281,7 +281,11 @@ __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* d
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (EVENTS) {
-        if (!((inside >> (t + i)) & 1)) dl[i] = x[i] = e[i] = 0.f;  // decays nothing, adds nothing
+        if (!((inside >> (t + i)) & 1)) {  // decays nothing, adds nothing, whatever lies there
+          dl[i] = x[i] = e[i] = 0.f;
+          bc.B.zero();
+          bc.C.zero();
+        }
         if ((starts >> (t + i)) & 1) begin(seq_at(seq, t + i));
       }
       token(i);
@@ -525,7 +529,14 @@ __global__ __launch_bounds__(kSelThreads, 2) void k_bwd_main(SelArgs q, Work w, 
 #pragma unroll
       for (int i = T - 1; i >= 0; --i) {
         const int t = s * T + i;
-        if (EV && ((ends >> t) & 1)) seq_states(q, dfinal, seq_at(seq, t), c, k, live, g);
+        if (EV && ((ends >> t) & 1)) {
+          seq_states(q, dfinal, seq_at(seq, t), c, k, live, g);
+          if (inside >> t == 1) {  // what lies behind is of no sequence: its `prev` was this one's
+                                   // last state, which infinite or NaN does not vanish with delta = 0
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) dA[j] = 0.f;
+          }
+        }
         float prev[NPL];
 #pragma unroll
         for (int j = 0; j < NPL; ++j) prev[j] = i ? hn[i - 1][j] : h[s][j];
