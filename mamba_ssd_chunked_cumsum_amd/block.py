@@ -5,8 +5,9 @@ time. Argument marshalling only, as in libssd.py.
 
 Activations are [batch, seqlen, channels] of float32 or bfloat16, weights and scan states
 float32. An activation may be a slice of wider rows (one projection's output) as long as its
-channels are adjacent, its rows evenly spaced, the offset 16-byte aligned and the row stride a
-multiple of 8 elements (the selective scan's B and C: of 4 elements each). Packed prompts: batch 1 and cu_seqlens, int32 offsets [nseq + 1] on the
+channels are adjacent, its rows evenly spaced and apart (a broadcast tensor is refused), the offset
+16-byte aligned and the row stride a multiple of 8 elements (the selective scan's B and C: of 4
+elements each). Packed prompts: batch 1 and cu_seqlens, int32 offsets [nseq + 1] on the
 device, sequence s being the tokens [cu_seqlens[s], cu_seqlens[s + 1]) (it may be empty); states
 then have nseq entries. Tokens behind the last sequence are not read; forward outputs there are
 left as they are (undefined in fresh tensors) and their gradients are zero. cu_seqlens is not read on the host: offsets that decrease or leave
@@ -132,6 +133,9 @@ def _rows(t, name, shape, dtype, dev, lead=2):
                 raise ValueError(f"{name}: the rows of tokens must be evenly spaced")
             row = stride[i] // step if row is None else row
         step *= size[i]
+    if row is not None and row < width:  # 0, a broadcast, would mean dense to the library
+        raise ValueError(f"{name}: the rows of tokens must be at least {width} elements apart, they "
+                         f"are {row} (a broadcast tensor needs contiguous())")
     _place(t, name, dtype, dev)
     return t.data_ptr(), 0 if row is None else row
 
