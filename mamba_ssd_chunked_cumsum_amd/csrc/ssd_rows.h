@@ -21,7 +21,7 @@ __device__ __forceinline__ int seq_of(const Rows& q, int r) {
   int lo = 0, hi = q.S;  // starts[lo] <= r < starts[hi], taking starts[S] as beyond
   if (q.starts[0] > r) return -1;
   while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
+    const int m = lo + ((hi - lo) >> 1);  // (the sum may pass 31 bits)
     if (q.starts[m] <= r) lo = m; else hi = m;
   }
   return r < seq_end(q, lo) ? lo : -1;
