@@ -63,11 +63,12 @@ __global__ __launch_bounds__(kBlock) void k_conv(ConvArgs q, IO* fin, int strip)
   constexpr int V = 8, U = 8;  // U rows are loaded before the first of them is used
   const int nvec = q.C / V;
   const int64_t id = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  const int unit = (int)(id / nvec), c = (int)(id % nvec) * V;
+  const int64_t unit = id / nvec;  // strips and sequences together may pass 31 bits
+  const int c = (int)(id % nvec) * V;
   const int nstrip = (q.rows.R + strip - 1) / strip;
   if (unit >= nstrip) {  // the final state of sequence `unit - nstrip`
-    const int s = unit - nstrip;
-    if (!fin || s >= q.rows.S) return;
+    if (!fin || unit - nstrip >= q.rows.S) return;
+    const int s = (int)(unit - nstrip);
     const int a = seq_begin(q.rows, s), len = max(seq_end(q.rows, s) - a, 0);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(kBlock) void k_conv(ConvArgs q, IO* fin, int strip)
     }
     return;
   }
-  const int r0 = unit * strip, r1 = min(r0 + strip, q.rows.R);
+  const int r0 = (int)unit * strip, r1 = min(r0 + strip, q.rows.R);
   int width, col;
   const int part = split_of(q.y, c, &width, &col);
   IO* y = (IO*)(part == 0 ? q.y.p[0] : part == 1 ? q.y.p[1] : q.y.p[2]);

@@ -35,3 +35,21 @@ def test_search_among_many_sequences():
     g2 = ssd.conv_backward(x, w, None, dy, cu_seqlens=few, want_initial_grad=False)
     assert torch.equal(y, y2)
     assert torch.equal(g["dx"], g2["dx"]) and torch.equal(g["dweight"], g2["dweight"])
+
+
+def test_rows_and_final_states_of_many_sequences():
+    """Strips of rows and the sequences' final states in one launch: together more than 2^31."""
+    S, rows = (1 << 31) - 4097, 40000
+    note(f"conv over {S} sequences with final states")
+    cu, few = offsets(S, [3, 5, rows])
+    x, w, _ = inputs(rows, 8, 2)
+    x = x.to(torch.bfloat16)
+    y, f = ssd.conv(x, w, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    y2, f2 = ssd.conv(x, w, cu_seqlens=few)
+    assert torch.equal(y, y2) and torch.equal(f[-3:], f2)
+    step = 1 << 28
+    for i in range(0, S - 3, step):  # the others begin and stay at zero
+        assert not f[i:min(i + step, S - 3)].flatten().view(torch.int32).any()
+    del f, cu
+    torch.cuda.empty_cache()
