@@ -481,14 +481,14 @@ def residual_norm(x, residual, weight, *, scale=None, eps=1e-5, residual_dtype=N
 def residual_norm_backward(x, residual_sum, weight, dy, dres=None, *, scale=None, eps=1e-5,
                            want_residual_grad=True):
     """Gradients of residual_norm from what it returned: residual_sum is its r, dy the gradient of
-    y, dres that of r (r's dtype, None: zero). x is read only with a scale. Returns a dict: dx
-    (x's dtype), dresidual (r's dtype; the same tensor as dx where there is no scale and the two
-    dtypes agree; None unless want_residual_grad), dweight and dscale (float32; dscale None
-    without a scale)."""
+    y, dres that of r (r's dtype, None: zero). Without a scale x gives only its shape, dtype and
+    device. Returns a dict: dx (x's dtype), dresidual (r's dtype; the same tensor as dx where there
+    is no scale and the two dtypes agree; None unless want_residual_grad), dweight and dscale
+    (float32; dscale None without a scale)."""
     _io(x)
     dev = x.device
     tok, _ = _tokens(x)
-    xp, xs = _rows(x, "x", x.shape, x.dtype, dev)
+    xp, xs = (None, 0) if scale is None else _rows(x, "x", x.shape, x.dtype, dev)
     rt = _res_dtype(residual_sum, "residual_sum", x)
     rp = _tensor(residual_sum, "residual_sum", x.shape, rt, dev)
     w = _tensor(weight, "weight", x.shape[2:], torch.float32, dev)

@@ -547,6 +547,10 @@ ssd_status ssd_residual_norm_backward(const ssd_tokens* t, const void* residual_
       (res_dtype != SSD_DTYPE_F32 && res_dtype != t->io_dtype) || (scale && !x) ||
       (scale != nullptr) != (dscale != nullptr))
     return SSD_ERR_INVALID_ARGUMENT;
+  if (!scale) {  // x is not read, so nothing about it matters
+    x = nullptr;
+    x_stride = 0;
+  }
   const int64_t R = rows_of(t), C = t->channels, e = bytes_of(t->io_dtype), re = bytes_of(res_dtype);
   const int64_t xs = stride_of(x_stride, C), need = ssd::norm_backward_bytes(a, scale ? 2 : 1);
   if (xs < 0) return SSD_ERR_INVALID_ARGUMENT;
