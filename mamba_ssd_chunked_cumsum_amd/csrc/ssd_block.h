@@ -55,7 +55,7 @@ hipError_t launch_selective(const SelArgs& a, void* y, float* fin, float* ws, in
 hipError_t launch_selective_step(const SelArgs& a, float* state_out, void* y, hipStream_t s);
 int64_t selective_backward_bytes(const SelArgs& a);
 hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const float* dfinal,
-                                     const SelGrads& g, float* ws, hipStream_t s);
+                                     const SelGrads& g, float* ws, int n_cu, hipStream_t s);
 
 struct NormArgs {
   int R, C, G, io;  // rows, channels, groups (each normalised by itself)

@@ -430,6 +430,7 @@ ssd_status ssd_selective_backward(const ssd_tokens* t, const ssd_selective* in, 
   const ssd::SelGrads g{out->dx, out->ddt, out->dz, out->dB, out->dC,
                         out->dA, out->dD, out->ddt_bias, out->dinitial_state};
   return from_hip(ssd::launch_selective_backward(a, dy, dfinal, g, static_cast<float*>(workspace),
+                                                 compute_units(),
                                                  static_cast<hipStream_t>(stream)));
 }
 

@@ -29,7 +29,8 @@ namespace {
 
 // States a lane; rows a chunk and a quarter of it, so that a quarter's h and a take 128 registers.
 constexpr int NPL = 4, kQuarter = 16, kChunk = 4 * kQuarter;
-constexpr int64_t kOneLaunch = 12 * 1024;  // waves of k_bwd_ends: twelve a SIMD of the card's 1024
+constexpr int kOneLaunch = 12;  // waves of k_bwd_ends a SIMD, up to which it is launched once
+constexpr int kFours = 2;       // the same, up to which its lanes hold four state entries
 
 struct Work {
   int chunks;
@@ -128,7 +129,9 @@ __device__ __forceinline__ void seq_states(const SelArgs& q, const float* p, int
 // on a SIMD against three). `all`: every chunk in the one launch. Two follow one another, and the
 // second is a chunk's latency however few chunks it has; the fewer registers pay only over many
 // rounds of waves (the whole backward, two launches and one: 1536 channels x 2041 tokens 161 and 130
-// us, x 5497 255 and 225, x 24569, 9200 waves, 830 and 822; 5120 x 16377, 20500 waves, 1695 and 1724).
+// us, x 5497 255 and 225, x 24569, 9200 waves, 830 and 822; 5120 x 16377, 20500 waves, 1695 and 1724;
+// the limit of kOneLaunch waves a SIMD, 12288 on 256 compute units, lies between the last two, where
+// the two ways are level).
 template <typename IO, int NT, bool EXACT, bool EVENTS>
 __global__ __launch_bounds__(256) void k_bwd_ends(SelArgs q, Work w, const IO* dy,
                                                   const float* dfinal, int all) {
@@ -731,12 +734,12 @@ int64_t selective_backward_bytes(const SelArgs& a) {
 }
 
 hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const float* dfinal,
-                                     const SelGrads& g, float* ws, hipStream_t s) {
+                                     const SelGrads& g, float* ws, int n_cu, hipStream_t s) {
   Work w;
   lay_out(a, ws, &w);
   const int cg = a.C / a.G, per_group = tiles_of(a), tiles = per_group * a.G;
   const unsigned blocks = (unsigned)((int64_t)tiles * w.chunks);
-  const int64_t CN = (int64_t)a.C * a.N;
+  const int64_t CN = (int64_t)a.C * a.N, simds = 4 * (int64_t)n_cu;
   auto run = [&](auto io) {
     using IO = decltype(io);
     auto ends = [&](auto size, auto exact) {
@@ -744,7 +747,7 @@ hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const flo
       const int64_t waves = (int64_t)((cg + 63) / 64) * a.G * w.chunks * ((a.N + NT - 1) / NT);
       constexpr bool EX = decltype(exact)::value;
       const dim3 grid((unsigned)((waves + 3) / 4));
-      const bool events = a.rows.starts || a.rows.L % kChunk, all = events && waves <= kOneLaunch;
+      const bool events = a.rows.starts || a.rows.L % kChunk, all = events && waves <= kOneLaunch * simds;
       if (!all && (a.rows.starts || a.rows.L >= kChunk))
         hipLaunchKernelGGL((k_bwd_ends<IO, NT, EX, false>), grid, dim3(256), 0, s, a, w,
                            (const IO*)dy, dfinal, 0);
@@ -756,7 +759,7 @@ hipError_t launch_selective_backward(const SelArgs& a, const void* dy, const flo
     using std::integral_constant;
     // four entries a lane where that still fits the card at once: shorter for each token
     const int64_t fours = (int64_t)((cg + 63) / 64) * a.G * w.chunks * (a.N / 4);
-    hipError_t e = fours <= 2048   ? ends(integral_constant<int, 4>{}, std::true_type{})
+    hipError_t e = fours <= kFours * simds ? ends(integral_constant<int, 4>{}, std::true_type{})
                    : a.N % 16 == 0 ? ends(integral_constant<int, 16>{}, std::true_type{})
                    : a.N <= 8      ? ends(integral_constant<int, 8>{}, std::false_type{})
                                    : ends(integral_constant<int, 16>{}, std::false_type{});
