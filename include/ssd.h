@@ -282,10 +282,10 @@ ssd_status ssd_backward(const ssd_problem* prob, const void* x, const float* dt,
  * (seq_starts NULL): `batch` sequences of `seqlen` tokens, nseq must equal batch. Packed: batch
  * must be 1, and sequence s of the nseq holds the rows [seq_starts[s], seq_starts[s + 1]);
  * seq_starts is nseq + 1 non-decreasing int32 offsets in device memory. A sequence may be empty.
- * Rows outside every sequence (behind the last) are not read, forward outputs there are left as
- * they were, and their gradients are zero. Offsets outside [0, seqlen] or out of
- * order are not reported (the host does not read them): which rows are computed is then
- * undefined, but no access leaves the tensors.
+ * Rows outside every sequence (in front of the first, behind the last) have no part in any result,
+ * whatever lies there, NaN too (they may be loaded); forward outputs there are left as they were, and
+ * their gradients are zero. Offsets outside [0, seqlen] or out of order are not reported (the host
+ * does not read them): which rows are computed is then undefined, but no access leaves the tensors.
  *
  * Strides: an input with a `stride` argument has rows that many elements apart (at least its own
  * width, a multiple of 8), so a slice of a wider projection is taken as it is; 0 means dense.
@@ -301,8 +301,13 @@ ssd_status ssd_backward(const ssd_problem* prob, const void* x, const float* dt,
  * each; so every entry point can be captured into a graph, which then holds that workspace.
  * The current device must be the one that holds the tensors.
  *
- * Limits (beyond them SSD_ERR_UNSUPPORTED): channels a multiple of 8 up to 2^20, rows below
- * 2^31. Errors as for ssd_forward: every check on the host before any HIP call. */
+ * Limits (beyond them SSD_ERR_UNSUPPORTED): channels a multiple of 8 up to 2^20; rows, and
+ * sequences, up to 2^31 - 4097 each; activations (rows times row stride) and states up to 2^40
+ * elements; and no launch of 2^32 threads: the norms take rows * ngroups below 2^26, or 2^23 where a
+ * group has more than 1024 channels, the convolution and the selective scan as many tokens and
+ * sequences as their channels leave. Errors as for ssd_forward: every check on the host before any
+ * HIP call, but for the selective scan's workspace, whose size depends on the current device (its
+ * query needs one). */
 typedef struct {
     int64_t batch, seqlen, channels, nseq;
     const int32_t* seq_starts; /* optional, device memory */
@@ -419,7 +424,7 @@ ssd_status ssd_residual_norm(const ssd_tokens* tokens, const void* x, int64_t x_
 
 /* Its gradients from dy (io dtype) and dres (gradient of residual_out, res_dtype; nullable: zero).
  * residual_sum is the residual_out that the forward wrote; x is read only with a scale (else it
- * may be NULL). dx io dtype; dresidual res_dtype (nullable); dweight, dscale (required with a
+ * and its stride are ignored). dx io dtype; dresidual res_dtype (nullable); dweight, dscale (required with a
  * scale, else NULL) f32. */
 ssd_status ssd_residual_norm_backward_workspace(const ssd_tokens* tokens, int64_t* bytes);
 ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* residual_sum,
@@ -432,7 +437,8 @@ ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* resi
 /* Static text for a status code. */
 const char* ssd_status_string(ssd_status status);
 
-/* Library version: major * 10000 + minor * 100 + patch. */
+/* Library version: major * 10000 + minor * 100 + patch. (10500 without and with the operators around
+ * the scan: their symbols tell whether a library has them.) */
 int ssd_version(void);
 
 #ifdef __cplusplus

@@ -9,9 +9,10 @@ channels are adjacent, its rows evenly spaced and apart (a broadcast tensor is r
 16-byte aligned and the row stride a multiple of 8 elements (the selective scan's B and C: of 4
 elements each). Packed prompts: batch 1 and cu_seqlens, int32 offsets [nseq + 1] on the
 device, sequence s being the tokens [cu_seqlens[s], cu_seqlens[s + 1]) (it may be empty); states
-then have nseq entries. Tokens behind the last sequence are not read; forward outputs there are
-left as they are (undefined in fresh tensors) and their gradients are zero. cu_seqlens is not read on the host: offsets that decrease or leave
-[0, seqlen] give undefined results.
+then have nseq entries. Tokens outside every sequence (behind the last, as a rule) have no part in
+any result, whatever lies there; forward outputs there are left as they are (undefined in fresh
+tensors) and their gradients are zero. cu_seqlens is not read on the host: offsets that decrease or
+leave [0, seqlen] give undefined results.
 
 The calls run on the current stream of the inputs' device and allocate their outputs and workspace
 with torch, so they can be captured into a graph. Given outputs (out, final_out, out_state) may not

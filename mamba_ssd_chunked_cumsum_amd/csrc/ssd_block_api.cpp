@@ -1,5 +1,6 @@
 // C ABI of the operators around the scan: argument checks and launches. Every check runs on the
-// host before the first HIP call.
+// host before the first HIP call, but for the selective scan's workspace, whose size depends on the
+// device.
 #include <hip/hip_runtime.h>
 
 #include <atomic>
