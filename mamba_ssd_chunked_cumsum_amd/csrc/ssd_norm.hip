@@ -4,7 +4,8 @@
 // A few operations for each element read and written once: bound by memory. A row (gated: one group
 // of a row) is held in registers, NT threads with NV vectors of 8 each, so each element is loaded
 // once whatever the direction; the row's sums go over the wave by shuffles and, where a row takes
-// more than a wave, over the block through LDS. Short rows take a wave each, four to a block.
+// more than a wave, over the block through LDS. Short rows take a wave each, four to a block (of a row
+// of 64 channels 8 lanes: 16384 x 80 groups of 64 bf16 456 us, backward 646, 1.1 and 1.3 TB/s).
 // Backward, a block walks rows and keeps the sums for the weight (and scale) gradients of its own
 // columns in registers, writing one partial at the end; a second kernel adds the partials in a
 // fixed order. Measured: gated backward of 16384 x 8 groups of 1024 bf16 250 us (5.3 TB/s, the copy

@@ -15,7 +15,8 @@
 // of its 16 tokens in registers, and back. So each exponential is evaluated twice and nothing of size
 // tokens x channels x dstate goes to memory; the vector units bound it. At 2 x 4096 tokens x 5120
 // channels x 16 entries (bf16, gated): 190 us the first kernel, 38 the chain, 635 the main kernel
-// (vector units busy 76%: h and a leave room for two waves a SIMD), 18 + 11 the sums; 857 us a call.
+// (vector units busy 76%: two waves a SIMD, by the registers that h and a take and by the LDS of the
+// staged chunk, 80 KiB a block), 18 + 11 the sums; 850 us a call.
 //
 // dB and dC sum over channels, i.e. over lanes: sums over the 16 channels of a wave are formed 16
 // values at a time, each step adding two lanes' values and merging two registers into one, so
