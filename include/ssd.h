@@ -434,6 +434,101 @@ ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* resi
                                       void* dresidual, float* dweight, float* dscale,
                                       void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---- Operators of layers of linear recurrence. ----------------------------------------------
+ * Beside the scan stand recurrences with one state entry a channel; the scan itself gains decays with
+ * a phase where B and C are rotated by their positions; and behind either stands a norm over groups of
+ * channels. Tokens, strides, alignment, arithmetic, workspaces and errors as for the operators around
+ * the scan above, and their limits; of launches below 2^32 threads: the recurrence takes rows (dense:
+ * of sequences rounded up to 16) times channels / 128 (fp32: / 64), rounded up, below about 2^30, the
+ * rotation rows times ngroups / 4 and nfreq / 4 + (dstate - 2 nfreq) / 8 below 2^32, the group norm
+ * sequences times ngroups below 2^24 where a sequence may have more than 8 tokens. */
+
+/* Gated linear recurrence. For every channel of each sequence, with v = sigmoid(input_gate) x (x where
+ * input_gate is NULL):
+ *     h[t] = a[t] h[t-1] + m[t] v[t];   y = h
+ *     decay given: u = sharpness softplus(decay) sigmoid(gate), a = exp(-u), m = sqrt(1 - a^2)
+ *     decay NULL:  a = sigmoid(gate), m = 1 - a
+ * x, gate, input_gate [rows, channels] io dtype, each with its row stride; decay [channels],
+ * initial_state (nullable: zeros), final_state [nseq, channels] f32. sharpness: positive and finite
+ * (not looked at without a decay). */
+typedef struct {
+    const void *x, *gate, *input_gate;
+    int64_t x_stride, gate_stride, input_gate_stride;
+    const float *decay, *initial_state;
+    float sharpness;
+    int32_t reserved; /* must be 0 */
+} ssd_recurrent;
+
+/* y [rows, channels] io dtype, dense; final_state nullable. */
+ssd_status ssd_recurrence_workspace(const ssd_tokens* tokens, const ssd_recurrent* in,
+                                    int64_t* bytes);
+ssd_status ssd_recurrence(const ssd_tokens* tokens, const ssd_recurrent* in, void* y,
+                          float* final_state, void* workspace, int64_t workspace_bytes,
+                          void* stream);
+
+/* One token for each of `batch` sequences (seqlen 1, not packed): in->initial_state is the state
+ * [batch, channels], state_out the new one (may be the same). */
+ssd_status ssd_recurrence_step(const ssd_tokens* tokens, const ssd_recurrent* in, float* state_out,
+                               void* y, void* stream);
+
+/* Gradients of ssd_recurrence from dy [rows, channels] (io dtype, dense) and dfinal [nseq, channels]
+ * f32 (nullable: zero): dx, dgate, dinput_gate (required with input_gate, else NULL) io dtype, dense;
+ * ddecay (required with decay, else NULL) and dinitial_state (nullable) f32. */
+ssd_status ssd_recurrence_backward_workspace(const ssd_tokens* tokens, const ssd_recurrent* in,
+                                             int64_t* bytes);
+ssd_status ssd_recurrence_backward(const ssd_tokens* tokens, const ssd_recurrent* in,
+                                   const void* dy, const float* dfinal, void* dx, void* dgate,
+                                   void* dinput_gate, float* ddecay, float* dinitial_state,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Rotation of B and C by the positions of their tokens, before ssd_forward or ssd_step: frequency j of
+ * the nfreq turns two of a head's dstate entries, (p, q) = (j, j + nfreq) or, interleaved, (2j, 2j + 1):
+ *     angle = positions[axis of j][row] * frequencies[j];
+ *     (p, q) <- (p cos(angle) - q sin(angle), p sin(angle) + q cos(angle))
+ * The first sections[0] frequencies go by the first axis, the next sections[1] by the second and so on
+ * (up to four axes; the sections sum to nfreq). Entries from 2 nfreq on are copied. C_t . B_s then
+ * depends on the positions by their difference alone: each pair of state entries has the decay of its
+ * head times exp(i angle). `inverse` turns the other way, which is the backward pass: gradients of the
+ * rotated B and C into those of B and C. Angles are formed in 64 bits.
+ * B, C (nullable) [rows, ngroups, dstate] with row strides, B_out, C_out dense, all of io dtype;
+ * positions [naxes, rows] int32 (4-byte aligned), frequencies [nfreq] f32. dstate a multiple of 8,
+ * nfreq of 4, ngroups * dstate up to 2^20 (else SSD_ERR_UNSUPPORTED). */
+typedef struct {
+    int64_t rows, ngroups, dstate, nfreq;
+    int64_t sections[4]; /* unused ones 0 */
+    const int32_t* positions;
+    const float* frequencies;
+    const void *B, *C;
+    int64_t b_stride, c_stride;
+    int32_t naxes, interleaved, inverse;
+    int32_t io_dtype; /* ssd_dtype */
+    int64_t reserved; /* must be 0 */
+} ssd_rotation;
+ssd_status ssd_rotate(const ssd_rotation* in, void* B_out, void* C_out, void* stream);
+
+/* Group norm with the SiLU that may follow (silu nonzero): over each sequence's tokens and each of
+ * ngroups equal runs of the channels (any number of channels each),
+ *     n = (x - mean) / sqrt(variance + eps);  v = weight n + bias;  y = v / (1 + exp(-v)) or v
+ * with the variance of all values (not of a sample). Sequences of one token (batch tokens, seqlen 1)
+ * give the norm of every token by itself. x [rows, channels] io dtype with its row stride, y dense;
+ * weight, bias [channels] f32 (each nullable: 1, 0); stats (nullable) [nseq, ngroups, 2] f32: mean and
+ * 1 / sqrt(variance + eps), what the backward pass takes; 0 and 1 / sqrt(eps) of an empty sequence. */
+ssd_status ssd_group_norm_workspace(const ssd_tokens* tokens, int64_t ngroups, int64_t* bytes);
+ssd_status ssd_group_norm(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                          const float* weight, const float* bias, int64_t ngroups, float eps,
+                          int32_t silu, void* y, float* stats, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/* Its gradients from dy (io dtype, dense) and the stats that the forward wrote: dx io dtype, dweight
+ * and dbias (each required with weight or bias, else NULL) f32. */
+ssd_status ssd_group_norm_backward_workspace(const ssd_tokens* tokens, int64_t ngroups,
+                                             int64_t* bytes);
+ssd_status ssd_group_norm_backward(const ssd_tokens* tokens, const void* x, int64_t x_stride,
+                                   const float* weight, const float* bias, int64_t ngroups,
+                                   int32_t silu, const float* stats, const void* dy, void* dx,
+                                   float* dweight, float* dbias, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* ssd_status_string(ssd_status status);
 

@@ -8,96 +8,11 @@
 #include <cstdint>
 
 #include "../../include/ssd.h"
-#include "ssd_block.h"
-#include "ssd_checks.h"
+#include "ssd_block_checks.h"
 
 namespace {
 
-using ssd::aligned16;
-using ssd::device_ready;
-using ssd::from_hip;
-using ssd::kMaxIndex;
-using ssd::overlap;
-using ssd::Range;
-using ssd::range_of;
-
-constexpr int64_t kMaxChannels = int64_t(1) << 20;
-// Bytes of any tensor: 64-bit offsets reach further, memory does not.
-constexpr double kMaxBytes = 4398046511104.0;
-
-int64_t bytes_of(int32_t dtype) { return dtype == SSD_DTYPE_BF16 ? 2 : 4; }
-
-bool is_dtype(int32_t d) { return d == SSD_DTYPE_F32 || d == SSD_DTYPE_BF16; }
-
-ssd_status check_tokens(const ssd_tokens* t, bool sequences) {
-  if (!t) return SSD_ERR_INVALID_ARGUMENT;
-  if (t->batch <= 0 || t->seqlen <= 0 || t->channels <= 0 || t->reserved != 0 ||
-      !is_dtype(t->io_dtype))
-    return SSD_ERR_INVALID_ARGUMENT;
-  if (t->seq_starts) {
-    if (!sequences || t->batch != 1 || t->nseq <= 0) return SSD_ERR_INVALID_ARGUMENT;
-  } else if (sequences && t->nseq != t->batch) {
-    return SSD_ERR_INVALID_ARGUMENT;
-  }
-  if (t->channels % 8 || t->channels > kMaxChannels) return SSD_ERR_UNSUPPORTED;
-  // one row below 2^31, so that a row index one past the last is an int too; the kernels add up
-  // to a tile of rows to it
-  if (double(t->batch) * double(t->seqlen) > double(kMaxIndex - 4096) || t->nseq > kMaxIndex - 4096)
-    return SSD_ERR_UNSUPPORTED;
-  return SSD_OK;
-}
-
-int64_t rows_of(const ssd_tokens* t) { return t->batch * t->seqlen; }
-
-// Effective row stride: 0 means dense. Negative where it is not acceptable.
-int64_t stride_of(int64_t given, int64_t width, int64_t multiple = 8) {
-  if (given == 0) return width;
-  return given >= width && given % multiple == 0 && given < (int64_t(1) << 32) ? given : -1;
-}
-
-// Bytes of `rows` rows of `width` elements at `stride`.
-int64_t span(int64_t rows, int64_t width, int64_t stride, int64_t e) {
-  return ((rows - 1) * stride + width) * e;
-}
-
-ssd::Rows make_rows(const ssd_tokens* t) {
-  return ssd::Rows{(int)rows_of(t), (int)t->seqlen, (int)(t->seq_starts ? t->nseq : t->batch),
-                   t->seq_starts};
-}
-
-// The buffers of a call: alignment, and no output on an input or another output.
-struct Buffers {
-  enum { kMost = 32 };
-  Range in[kMost], out[kMost];
-  int n_in = 0, n_out = 0;
-  bool ok = true;
-  void input(const void* p, int64_t bytes, uintptr_t align = 16) {
-    if (!p) return;
-    ok = ok && reinterpret_cast<uintptr_t>(p) % align == 0;
-    in[n_in++] = range_of(p, bytes);
-  }
-  void output(const void* p, int64_t bytes) {
-    if (!p) return;
-    ok = ok && aligned16(p);
-    out[n_out++] = range_of(p, bytes);
-  }
-  bool fine() const {
-    if (!ok) return false;
-    for (int i = 0; i < n_out; ++i) {
-      for (int j = 0; j < n_in; ++j)
-        if (overlap(out[i], in[j])) return false;
-      for (int j = 0; j < i; ++j)
-        if (overlap(out[i], out[j])) return false;
-    }
-    return true;
-  }
-};
-
-int64_t starts_bytes(const ssd_tokens* t) { return (t->nseq + 1) * 4; }
-
-void starts_input(Buffers& b, const ssd_tokens* t) {
-  b.input(t->seq_starts, starts_bytes(t), 4);
-}
+using namespace ssd;
 
 // ---- convolution -----------------------------------------------------------------------------------
 
@@ -188,9 +103,6 @@ int64_t sel_state_bytes(const ssd_tokens* t, const ssd_selective* in) {
   return t->nseq * t->channels * in->dstate * 4;
 }
 
-// Blocks of a launch: HIP counts a grid's threads in 32 bits.
-bool grid_fits(double blocks, int threads) { return blocks * threads < 4294967296.0; }
-
 bool selective_grid_fits(const ssd::SelArgs& a) {
   const int width = a.N <= 16 ? 64 : a.N <= 32 ? 32 : 16;  // channels of the backward's tiles
   const double tiles = double(a.C) / width + a.G;
@@ -224,11 +136,6 @@ ssd_status norm_args(const ssd_tokens* t, int64_t ngroups, float eps, const floa
   if (n % 8 || n > kMaxNorm) return SSD_ERR_UNSUPPORTED;
   if (!grid_fits(double(rows_of(t)) * ngroups, n <= 1024 ? 64 : 512)) return SSD_ERR_UNSUPPORTED;
   *a = ssd::NormArgs{(int)rows_of(t), (int)t->channels, (int)ngroups, t->io_dtype, eps, weight};
-  return SSD_OK;
-}
-
-ssd_status with_workspace(const void* ws, int64_t have, int64_t need) {
-  if (need > 0 && (!ws || have < need || !aligned16(ws))) return SSD_ERR_INVALID_ARGUMENT;
   return SSD_OK;
 }
 

@@ -1,0 +1,62 @@
+// Launchers of the operators of layers of linear recurrence (library-internal). Every launcher
+// assumes the host checks of ssd_recurrent_api.cpp have passed.
+#pragma once
+#include "ssd_block.h"
+
+namespace ssd {
+
+// ---- gated linear recurrence ---------------------------------------------------------------------
+struct RecArgs {
+  Rows rows;
+  int C, io;
+  const void *x, *g, *gi;  // gi null: no input gate
+  int64_t xs, gs, is;
+  const float* decay;  // null: the gate is the decay
+  float sharp;
+  const float* h0;
+};
+struct RecGrads {
+  void *dx, *dg, *dgi;
+  float *ddecay, *dh0;
+};
+
+bool recurrence_fits(const RecArgs& a);  // whether its launches do
+int64_t recurrence_bytes(const RecArgs& a);
+hipError_t launch_recurrence(const RecArgs& a, void* y, float* fin, float* ws, hipStream_t s);
+hipError_t launch_recurrence_step(const RecArgs& a, float* state_out, void* y, hipStream_t s);
+int64_t recurrence_backward_bytes(const RecArgs& a);
+hipError_t launch_recurrence_backward(const RecArgs& a, const void* dy, const float* dfinal,
+                                      const RecGrads& g, float* ws, hipStream_t s);
+
+// ---- rotation of B and C -------------------------------------------------------------------------
+struct RotArgs {
+  int64_t rows;
+  int G, N, nf, axes;  // heads, entries of each, frequencies (two entries each), axes
+  int ends[4];         // frequencies up to ends[i] go by axis i
+  int io, interleaved, inverse;
+  const int* pos;  // [axes, rows]
+  const float* freq;
+  const void *b, *c;  // c null: b alone
+  int64_t bs, cs;
+  void *ob, *oc;
+};
+bool rotate_fits(const RotArgs& a);
+hipError_t launch_rotate(const RotArgs& a, hipStream_t s);
+
+// ---- group norm ------------------------------------------------------------------------------------
+struct GroupArgs {
+  Rows rows;
+  int C, G, io, act;
+  float eps;
+  const void* x;
+  int64_t xs;
+  const float *w, *b;  // null: 1, 0
+};
+bool group_norm_fits(const GroupArgs& a);  // whether its launches do
+int64_t group_norm_bytes(const GroupArgs& a);
+hipError_t launch_group_norm(const GroupArgs& a, void* y, float* stats, float* ws, hipStream_t s);
+int64_t group_norm_backward_bytes(const GroupArgs& a);
+hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, const void* dy, void* dx,
+                                      float* dw, float* db, float* ws, hipStream_t s);
+
+}  // namespace ssd

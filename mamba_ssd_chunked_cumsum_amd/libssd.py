@@ -31,7 +31,12 @@ EXPORTS = ("ssd_forward", "ssd_forward_ex", "ssd_forward_noalloc", "ssd_chunk_cu
            "ssd_selective_scan_workspace", "ssd_selective_scan", "ssd_selective_step",
            "ssd_selective_backward_workspace", "ssd_selective_backward", "ssd_gated_norm",
            "ssd_gated_norm_backward_workspace", "ssd_gated_norm_backward", "ssd_residual_norm",
-           "ssd_residual_norm_backward_workspace", "ssd_residual_norm_backward")
+           "ssd_residual_norm_backward_workspace", "ssd_residual_norm_backward",
+           # bound in recurrent.py
+           "ssd_recurrence_workspace", "ssd_recurrence", "ssd_recurrence_step",
+           "ssd_recurrence_backward_workspace", "ssd_recurrence_backward", "ssd_rotate",
+           "ssd_group_norm_workspace", "ssd_group_norm", "ssd_group_norm_backward_workspace",
+           "ssd_group_norm_backward")
 
 
 class SSDProblem(ctypes.Structure):
