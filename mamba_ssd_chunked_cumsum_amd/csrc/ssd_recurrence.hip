@@ -23,8 +23,10 @@ namespace ssd {
 
 namespace {
 
-constexpr int T = 16;      // rows of a wave
+constexpr int T = 16;      // rows of a wave, at most 31
 constexpr int kWaves = 8;  // most waves of a block
+constexpr int kGroup = 8;  // chunks between those that hand on their end state
+constexpr float kLn2 = 0.6931471805599453f;
 template <typename IO>
 constexpr int kV = 4 / (int)sizeof(IO);  // channels of a lane
 
@@ -48,39 +50,58 @@ Plan plan(const Rows& q) {
 int threads_of(const Plan& p) { return 64 * p.waves * p.seqs; }
 
 // ---- one element -----------------------------------------------------------------------------------
+// 1 / (1 + exp(-v)), exact to a few roundings where it is small too (0 below -88).
+__device__ __forceinline__ float one_side(float v) {
+  return __builtin_amdgcn_rcpf(1.f + exp2_fast(-v * kLog2e));
+}
+// sigmoid(v) and sigmoid(-v), both to a few roundings of themselves (the first at least 2^-126). The
+// minimum keeps NaN.
 struct Sig {
-  float p, n;  // sigmoid(v), sigmoid(-v), each exact to a few roundings where it is small too
+  float p, n;
 };
 __device__ __forceinline__ Sig both_sides(float v) {
-  const float e = exp2_fast(-fabsf(v) * kLog2e), big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
-  return v >= 0.f ? Sig{big, small} : Sig{small, big};
+  const float e = __builtin_elementwise_minimum(exp2_fast(-v * kLog2e), 0x1p126f);
+  const float p = __builtin_amdgcn_rcpf(1.f + e);
+  return Sig{p, e * p};
 }
 
-// 1 - exp(-2u) from u >= 0 and a = exp(-u): the series where the difference would cancel (below
-// 2u = 1/4, where the term left out is under 2^-24 of the sum).
-__device__ __forceinline__ float one_minus_square(float u, float a) {
-  const float v = 2.f * u;
-  float s = fmaf(v, -1.f / 6.f, 1.f);
-  s = fmaf(v * s, -1.f / 5.f, 1.f);
-  s = fmaf(v * s, -1.f / 4.f, 1.f);
-  s = fmaf(v * s, -1.f / 3.f, 1.f);
-  s = fmaf(v * s, -1.f / 2.f, 1.f);
-  return v < 0.25f ? v * s : fmaf(-a, a, 1.f);
+// 1 - a^2 from a = 2^-t, t >= 0: where the difference would cancel (below t = 0.36, that is a^2 = 0.61)
+// the polynomial t c(t) of degree 5 that is nearest, to 9e-8 relative.
+__device__ __forceinline__ float one_minus_square(float t, float a) {
+  float s = fmaf(t, 0.03472883999347687f, -0.15147662162780762f);
+  s = fmaf(t, s, 0.44372719526290894f);
+  s = fmaf(t, s, -0.960892379283905f);
+  s = fmaf(t, s, 1.3862942457199097f);
+  return t < 0.36f ? t * s : fmaf(-a, a, 1.f);
 }
 
-// What a token does to a channel's state. k = sharpness softplus(decay).
+// What a token does to a channel's state; rate = sharpness softplus(decay) log2(e).
+struct Step {
+  float a, m;
+};
+template <bool DECAY>
+__device__ __forceinline__ Step step_of(float g, float rate) {
+  if constexpr (!DECAY) {
+    const Sig r = both_sides(g);
+    return Step{r.p, r.n};
+  }
+  const float t = rate * one_side(g), a = exp2_fast(-t);
+  return Step{a, __builtin_amdgcn_sqrtf(one_minus_square(t, a))};
+}
+
+// The same with what the gradients need: r and 1 - r, 1 / m (at most 2^63, so that u / m is 0 where u
+// is).
 template <bool DECAY>
 struct Gate {
-  float a, m;
+  float a, m, inv;
   Sig r;
-  float u, inv;  // with a decay: u and 1 / m (at most 2^63, so that u / m is 0 where u is)
-  __device__ __forceinline__ Gate(float g, float k) {
+  __device__ __forceinline__ Gate(float g, float rate) {
     r = both_sides(g);
     if constexpr (DECAY) {
-      u = k * r.p;
-      a = exp2_fast(-u * kLog2e);
-      const float sq = one_minus_square(u, a);
-      inv = __builtin_amdgcn_rsqf(fmaxf(sq, 1.17549435e-38f));
+      const float t = rate * r.p;
+      a = exp2_fast(-t);
+      const float sq = one_minus_square(t, a);
+      inv = __builtin_amdgcn_rsqf(fmaxf(sq, 0x1p-126f));
       m = sq * inv;
     } else {
       a = r.p;
@@ -89,9 +110,16 @@ struct Gate {
   }
 };
 
+// sharpness softplus(decay) log2(e), to a few roundings: exp(-|d|) with the product's rounding made
+// good, log(1 + e) by its series where e is small, else from the hardware's log2 of the rounded sum and
+// what the rounding lost.
 __device__ __forceinline__ float decay_rate(const RecArgs& q, int c) {
-  const float d = q.decay[c];
-  return q.sharp * (d > 20.f ? d : log1pf(expf(d)));
+  const float d = q.decay[c], v = -fabsf(d), hi = v * kLog2e;
+  const float lo = fmaf(v, kLog2e, -hi) + v * 1.9259629911e-8f;  // log2(e) is 1.9e-8 above kLog2e
+  const float e = exp2_fast(hi), x = fmaf(e, lo * kLn2, e), w = 1.f + x;
+  const float small = x * fmaf(x, fmaf(x, fmaf(x, -0.25f, 1.f / 3.f), -0.5f), 1.f);
+  const float large = fmaf(__builtin_amdgcn_logf(w), kLn2, x - (w - 1.f));
+  return q.sharp * (fmaxf(d, 0.f) + (x < 0x1p-6f ? small : large)) * kLog2e;
 }
 
 // P of a run with a sequence's start in it is -0 (products of decays are never negative): what
@@ -115,24 +143,29 @@ __device__ __forceinline__ void store_word(IO* row, unsigned off, const float (&
   *(uint32_t*)((char*)row + off) = u;
 }
 
-// T rows of n at row r0 of a tensor (null: zeros); the rows past n are not read.
+// T rows of n of several tensors, row by row, so that the first rows can be worked on while the others
+// arrive; the rows past n are not read (zeros).
 template <typename IO>
-__device__ __forceinline__ void load_rows(uint32_t (&u)[T], const void* t, int64_t stride, int r0,
-                                          int n, unsigned off) {
-  const char* p = (const char*)((const IO*)t + r0 * stride);
+struct Source {
+  const char* p;
+  int64_t step;
+  __device__ __forceinline__ Source(const void* t, int64_t stride, int r0)
+      : p((const char*)((const IO*)t + r0 * stride)), step(stride * sizeof(IO)) {}
+  __device__ __forceinline__ uint32_t next(unsigned off) {
+    const uint32_t u = *(const uint32_t*)(p + off);
+    p += step;
+    return u;
+  }
+};
+template <typename F>
+__device__ __forceinline__ void for_rows(int n, F f) {
   if (n == T) {
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-      u[i] = *(const uint32_t*)(p + off);
-      p += stride * sizeof(IO);
-    }
+    for (int i = 0; i < T; ++i) f(i);
   } else {
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-      u[i] = 0;
-      if (i < n) u[i] = *(const uint32_t*)(p + off);
-      p += stride * sizeof(IO);
-    }
+    for (int i = 0; i < T; ++i)
+      if (i < n) f(i);
   }
 }
 
@@ -179,14 +212,38 @@ struct Place {
   }
 };
 
-// Sequence boundaries among a wave's rows (packed).
+// Sequence boundaries among a wave's rows (packed), found by the scalar unit beside the rows' loads.
 struct Marks {
-  uint64_t starts = 0, ends = 0, inside = 0;
-  int seq = -1;  // of row i, in lane i
+  uint32_t starts = 0, ends = 0, inside = 0;  // a bit a row
+  int seq = -1;                               // of row i, in lane i
   bool plain = true;
+  static __device__ __forceinline__ int offset(const Rows& q, int i) {
+    typedef const __attribute__((address_space(4))) int* Words;  // read through scalar loads
+    return ((Words)(uintptr_t)q.starts)[__builtin_amdgcn_readfirstlane(i)];
+  }
   __device__ __forceinline__ void find(const Rows& q, int first, int n) {
-    mark_rows(q, first, first + n, starts, ends, inside, seq);
-    const uint64_t all = n >= 64 ? ~0ull : (1ull << n) - 1;
+    const int lane = threadIdx.x & 63, stop = first + n;
+    const uint32_t all = (1u << n) - 1;
+    const int front = offset(q, 0);
+    for (int r = first; r < stop;) {
+      if (r < front) {  // in front of the first sequence
+        r = min(front, stop);
+        continue;
+      }
+      int lo = 0, hi = q.S;  // as seq_of
+      while (hi - lo > 1) {
+        const int m = lo + ((hi - lo) >> 1);
+        if (offset(q, m) <= r) lo = m; else hi = m;
+      }
+      const int begin = max(offset(q, lo), 0), end = min(offset(q, lo + 1), q.R);
+      if (end <= r) break;  // behind the last
+      const int to = min(end, stop);
+      if (begin == r) starts |= 1u << (r - first);
+      if (to == end) ends |= 1u << (to - 1 - first);
+      inside |= ((1u << (to - first)) - 1) & ~((1u << (r - first)) - 1);
+      seq = lane >= r - first && lane < to - first ? lo : seq;
+      r = to;
+    }
     plain = !starts && !ends && inside == all;
   }
 };
@@ -212,34 +269,72 @@ struct Sums {
 };
 
 // ---- forward ---------------------------------------------------------------------------------------
-// ENDS: only the runs' sums, for the chain. Otherwise y and the final states; `chained`: the states
-// entering the chunks are in sums.H.
-template <typename IO, bool DECAY, bool GATED, bool PACKED, bool ENDS>
-__global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int tiles, Sums sums,
-                                                     int chained, IO* __restrict__ y,
-                                                     float* __restrict__ fin) {
+// Chunks of one call hand on what follows them needs through `slots` [units, C], one 64-bit word a
+// channel: (P, H) of the chunk, or of every kGroup-th chunk its end state, as a run with P = -0. A word
+// is written once, as a whole, so it needs no flag beside it: `kEmpty` until then.
+constexpr uint64_t kEmpty = ~0ull;
+struct Chain {
+  uint64_t* slots;
+  uint32_t* tickets;  // a counter a tile and sequence (packed: a tile), kApart words apart
+  int counters;
+};
+constexpr int kApart = 16;
+__device__ __forceinline__ void publish(uint64_t* slot, float P, float H) {
+  uint32_t h = __float_as_uint(H);
+  if (h == ~0u) h = 0x7fc00000u;  // (a NaN of a caller's, which would look empty)
+  __hip_atomic_store(slot, (uint64_t)__float_as_uint(P) << 32 | h, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__global__ __launch_bounds__(256) void k_rec_clear(Chain chain, int64_t n) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id < chain.counters) chain.tickets[id * kApart] = 0;
+  if (id < n) chain.slots[id] = kEmpty;
+}
+
+// CHAIN: sequences of several chunks. A block belongs to a tile and sequence and takes the next chunk of
+// them by a ticket. It waits only for chunks before its own, whose blocks have lower tickets: those are
+// running or done, and the first of them waits for none, so every wait ends.
+template <typename IO, bool DECAY, bool GATED, bool PACKED, bool CHAIN>
+__global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int tiles, Chain chain,
+                                                     IO* __restrict__ y, float* __restrict__ fin) {
   constexpr int V = kV<IO>;
   __shared__ float2 runs[kWaves][V][64];
+  __shared__ float entry[V][64];
+  __shared__ uint32_t place;
   const int64_t main_blocks = (int64_t)tiles * pl.units;
   if (PACKED && blockIdx.x >= main_blocks) {
     pass_empty(q.rows, q.C, (int)(blockIdx.x - main_blocks), (int)(gridDim.x - main_blocks), q.h0, fin);
     return;
   }
   const int tile = (int)(blockIdx.x % tiles), lane = threadIdx.x & 63;
-  const Place at(q.rows, pl, (int)(blockIdx.x / tiles));
+  int unit = (int)(blockIdx.x / tiles);
+  const int s = PACKED ? 0 : unit % q.rows.S;
+  uint32_t ticket = 0;
+  if (CHAIN && threadIdx.x == 0)
+    ticket = __hip_atomic_fetch_add(chain.tickets + ((int64_t)s * tiles + tile) * kApart, 1u,
+                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   const int c0 = (tile * 64 + lane) * V;
   const bool live = c0 < q.C;
   const int c = live ? c0 : q.C - V;  // idle lanes compute the last channels again
   const unsigned off = (unsigned)c * sizeof(IO);
-  uint32_t rx[T], rg[T], ri[T];
-  load_rows<IO>(rg, q.g, q.gs, at.first, at.n, off);
-  if (GATED) load_rows<IO>(ri, q.gi, q.is, at.first, at.n, off);
-  load_rows<IO>(rx, q.x, q.xs, at.first, at.n, off);
-  Marks mk;
-  if (PACKED && at.n > 0) mk.find(q.rows, at.first, at.n);
   float k[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) k[j] = DECAY ? decay_rate(q, c + j) : 0.f;
+  if (CHAIN) {
+    if (threadIdx.x == 0) place = ticket;
+    __syncthreads();
+    unit = s * pl.chunks + __builtin_amdgcn_readfirstlane(place);
+  }
+  const Place at(q.rows, pl, unit);
+  uint32_t rx[T], rg[T], ri[T];
+  Source<IO> sg(q.g, q.gs, at.first), si(q.gi, q.is, at.first), sx(q.x, q.xs, at.first);
+  for_rows(at.n, [&](int i) {
+    rg[i] = sg.next(off);
+    if (GATED) ri[i] = si.next(off);
+    rx[i] = sx.next(off);
+  });
+  Marks mk;
+  if (PACKED && at.n > 0) mk.find(q.rows, at.first, at.n);
 
   float P[T][V], H[T][V];  // of the rows up to each
   float p[V], h[V];
@@ -248,9 +343,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
   auto row = [&](int i) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const Gate<DECAY> t(word<IO>(rg[i], j), k[j]);
+      const Step t = step_of<DECAY>(word<IO>(rg[i], j), k[j]);
       float v = word<IO>(rx[i], j);
-      if (GATED) v *= both_sides(word<IO>(ri[i], j)).p;
+      if (GATED) v *= one_side(word<IO>(ri[i], j));
       if (PACKED && !mk.plain) {
         if (mk.starts >> i & 1) {
           const float h0 = q.h0 ? q.h0[(int64_t)seq_at(mk.seq, i) * q.C + c + j] : 0.f;
@@ -267,7 +362,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
         p[j] *= t.a;
         h[j] = fmaf(t.a, h[j], t.m * v);
       }
-      if (!ENDS) P[i][j] = p[j], H[i][j] = h[j];
+      P[i][j] = p[j], H[i][j] = h[j];
     }
   };
   if (at.n == T && (!PACKED || mk.plain)) {
@@ -281,33 +376,76 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
 #pragma unroll
   for (int j = 0; j < V; ++j) runs[at.wave][j][lane] = make_float2(p[j], h[j]);
   __syncthreads();
-  if (ENDS) {
-    if (at.wave == 0 && live) {
+  float e[V];  // the state that enters
+  if (CHAIN) {
+    const int chunk = PACKED ? at.unit : at.unit % pl.chunks;
+    if (at.wave == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < V; ++j)
         for (int w = 1; w < pl.waves; ++w) {
           const float2 r = runs[w][j][lane];
           h[j] = enter(r.x, r.y, h[j]);
           p[j] = join(p[j], r.x);
         }
-        sums.P[(int64_t)at.unit * q.C + c + j] = p[j];
-        sums.H[(int64_t)at.unit * q.C + c + j] = h[j];
+      uint64_t* slot = chain.slots + (int64_t)at.unit * q.C + c;
+      const bool hands_on = chunk % kGroup == kGroup - 1, needed = chunk + 1 < pl.chunks;
+      if (needed && !hands_on && live) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) publish(slot + j, p[j], h[j]);
       }
+      const int from = max(chunk / kGroup * kGroup - 1, 0);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        e[j] = !PACKED && q.h0 ? q.h0[(int64_t)at.s * q.C + c + j] : 0.f;
+      uint64_t got[kGroup][V];
+      bool all;
+      do {  // (see above: it ends)
+        all = true;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+          if (from + i < chunk) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              got[i][j] = __hip_atomic_load(slot + (int64_t)(from + i - chunk) * q.C + j,
+                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+              all = all && got[i][j] != kEmpty;
+            }
+          }
+      } while (!__all(all));
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i)
+        if (from + i < chunk) {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            e[j] = enter(__uint_as_float((uint32_t)(got[i][j] >> 32)),
+                         __uint_as_float((uint32_t)got[i][j]), e[j]);
+        }
+      if (needed && hands_on && live) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) publish(slot + j, -0.f, enter(p[j], h[j], e[j]));
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) entry[j][lane] = e[j];
     }
-    return;
+    __syncthreads();
+    if (at.n <= 0) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = entry[j][lane];
+  } else {
+    if (at.n <= 0) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      e[j] = !PACKED && q.h0 ? q.h0[(int64_t)at.s * q.C + c + j] : 0.f;
   }
-  if (at.n <= 0) return;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    float e = 0.f;
-    if (chained) e = sums.H[(int64_t)at.unit * q.C + c + j];
-    else if (!PACKED && q.h0) e = q.h0[(int64_t)at.s * q.C + c + j];
     for (int w = at.lo; w < at.wave; ++w) {
       const float2 r = runs[w][j][lane];
-      e = enter(r.x, r.y, e);
+      e[j] = enter(r.x, r.y, e[j]);
     }
 #pragma unroll
-    for (int i = 0; i < T; ++i) H[i][j] = PACKED ? enter(P[i][j], H[i][j], e) : fmaf(P[i][j], e, H[i][j]);
+    for (int i = 0; i < T; ++i)
+      H[i][j] = PACKED ? enter(P[i][j], H[i][j], e[j]) : fmaf(P[i][j], e[j], H[i][j]);
   }
   if (!live) return;
   IO* out = y + (int64_t)at.first * q.C;
@@ -400,10 +538,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
   const int c = live ? c0 : q.C - V;
   const unsigned off = (unsigned)c * sizeof(IO);
   uint32_t rx[T], rg[T], ri[T], rd[T];
-  load_rows<IO>(rg, q.g, q.gs, at.first, at.n, off);
-  if (GATED) load_rows<IO>(ri, q.gi, q.is, at.first, at.n, off);
-  load_rows<IO>(rx, q.x, q.xs, at.first, at.n, off);
-  load_rows<IO>(rd, dy, q.C, at.first, at.n, off);
+  Source<IO> sg(q.g, q.gs, at.first), si(q.gi, q.is, at.first), sx(q.x, q.xs, at.first),
+      sd(dy, q.C, at.first);
+  for_rows(at.n, [&](int i) {
+    rg[i] = sg.next(off);
+    if (GATED) ri[i] = si.next(off);
+    rx[i] = sx.next(off);
+    rd[i] = sd.next(off);
+  });
   Marks mk;
   if (PACKED && at.n > 0) mk.find(q.rows, at.first, at.n);
   float k[V];
@@ -424,9 +566,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (!ENDS) P[i][j] = p[j], H[i][j] = h[j];
-      const Gate<DECAY> t(word<IO>(rg[i], j), k[j]);
+      const Step t = step_of<DECAY>(word<IO>(rg[i], j), k[j]);
       float v = word<IO>(rx[i], j);
-      if (GATED) v *= both_sides(word<IO>(ri[i], j)).p;
+      if (GATED) v *= one_side(word<IO>(ri[i], j));
       float d = word<IO>(rd[i], j);
       if (PACKED && !mk.plain) {
         if (!(mk.inside >> i & 1)) {
@@ -525,9 +667,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
         ox[j] = GATED ? lm * s.p : lm;
         oi[j] = lm * v * s.n;
         if constexpr (DECAY) {
-          const float av = t.a * t.a * v, ah = t.a * before;
-          og[j] = l * t.r.n * fmaf(av, t.u * t.inv, -t.u * ah);
-          sum[j] = fmaf(l, fmaf(av, t.r.p * t.inv, -t.r.p * ah), sum[j]);
+          const float d = l * fmaf(t.a * t.a * v, t.inv, -t.a * before);  // -dL/dlog a
+          og[j] = d * (t.r.n * (k[j] * t.r.p)) * kLn2;
+          sum[j] = fmaf(d, t.r.p, sum[j]);
         } else {
           og[j] = l * (before - v) * (t.a * t.m);
         }
@@ -567,7 +709,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
       for (int j = 0; j < V; ++j) {
         float t = sum[j];
         for (int w = 1; w < (int)blockDim.x / 64; ++w) t += left[w][j][lane];
-        part[(int64_t)at.unit * q.C + c + j] = t * (q.sharp * both_sides(q.decay[c + j]).p);
+        part[(int64_t)at.unit * q.C + c + j] = t * (q.sharp * one_side(q.decay[c + j]));
       }
     }
   }
@@ -591,9 +733,9 @@ __global__ __launch_bounds__(256) void k_rec_step(RecArgs q, float* state_out, I
   load_f32<4>(q.h0 + b * q.C + c, h);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const Gate<DECAY> t(g.get(j), DECAY ? decay_rate(q, c + j) : 0.f);
+    const Step t = step_of<DECAY>(g.get(j), DECAY ? decay_rate(q, c + j) : 0.f);
     float v = x.get(j);
-    if (GATED) v *= both_sides(gi.get(j)).p;
+    if (GATED) v *= one_side(gi.get(j));
     o[j] = fmaf(t.a, h[j], t.m * v);
   }
   store_vec<float, 4>(state_out + b * q.C + c, o);
@@ -618,9 +760,10 @@ int tiles_of(const RecArgs& a) {
 int64_t sum_floats(const RecArgs& a, const Plan& p) {
   return ((int64_t)p.units * a.C + 63) / 64 * 64;
 }
-dim3 chain_grid(const RecArgs& a, int directions) {
+int64_t counters_of(const RecArgs& a) { return (int64_t)tiles_of(a) * (a.rows.starts ? 1 : a.rows.S); }
+dim3 chain_grid(const RecArgs& a) {  // both directions
   const int64_t n = (a.rows.starts ? 1 : (int64_t)a.rows.S) * a.C;
-  return dim3((unsigned)((n + 255) / 256), directions);
+  return dim3((unsigned)((n + 255) / 256), 2);
 }
 
 }  // namespace
@@ -632,32 +775,35 @@ bool recurrence_fits(const RecArgs& a) {
          fits(double(a.rows.starts ? 1 : a.rows.S) * a.C / 256 + 1, 256);
 }
 
+// Chained: the tickets, then the slots.
 int64_t recurrence_bytes(const RecArgs& a) {
   const Plan p = plan(a.rows);
-  return p.chunks > 1 ? 8 * sum_floats(a, p) : 0;
+  return p.chunks > 1 ? 4 * kApart * counters_of(a) + 8 * (int64_t)p.units * a.C : 0;
 }
 
 hipError_t launch_recurrence(const RecArgs& a, void* y, float* fin, float* ws, hipStream_t s) {
   const Plan p = plan(a.rows);
-  const int tiles = tiles_of(a), chained = p.chunks > 1;
-  const Sums sums{ws, ws ? ws + sum_floats(a, p) : nullptr, nullptr};
+  const int tiles = tiles_of(a);
   const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, fin);
+  const int64_t counters = counters_of(a);
+  const Chain chain{ws ? (uint64_t*)(ws + kApart * counters) : nullptr, (uint32_t*)ws, (int)counters};
+  if (p.chunks > 1) {
+    const int64_t n = (int64_t)p.units * a.C;  // more than counters
+    hipLaunchKernelGGL(k_rec_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, chain, n);
+  }
   return by_kind(a, [&](auto io, auto decay, auto gated) {
     using IO = decltype(io);
     constexpr bool D = decltype(decay)::value, G = decltype(gated)::value;
-    auto run = [&](auto packed) {
-      constexpr bool K = decltype(packed)::value;
-      if (chained) {
-        hipLaunchKernelGGL((k_rec<IO, D, G, K, true>), dim3(blocks), dim3(threads_of(p)), 0, s, a, p,
-                           tiles, sums, 0, (IO*)nullptr, (float*)nullptr);
-        hipLaunchKernelGGL(k_rec_chain, chain_grid(a, 1), dim3(256), 0, s, a, p, sums,
-                           (const float*)nullptr);
-      }
-      hipLaunchKernelGGL((k_rec<IO, D, G, K, false>), dim3(blocks + more), dim3(threads_of(p)), 0, s,
-                         a, p, tiles, sums, chained, (IO*)y, fin);
+    auto run = [&](auto packed, auto chained) {
+      hipLaunchKernelGGL((k_rec<IO, D, G, decltype(packed)::value, decltype(chained)::value>),
+                         dim3(blocks + more), dim3(threads_of(p)), 0, s, a, p, tiles, chain, (IO*)y,
+                         fin);
       return hipGetLastError();
     };
-    return a.rows.starts ? run(std::true_type{}) : run(std::false_type{});
+    auto chains = [&](auto packed) {
+      return p.chunks > 1 ? run(packed, std::true_type{}) : run(packed, std::false_type{});
+    };
+    return a.rows.starts ? chains(std::true_type{}) : chains(std::false_type{});
   });
 }
 
@@ -697,7 +843,7 @@ hipError_t launch_recurrence_backward(const RecArgs& a, const void* dy, const fl
         hipLaunchKernelGGL((k_rec_bwd<IO, D, G, K, true>), dim3(blocks), dim3(threads_of(p)), 0, s, a,
                            p, tiles, sums, 0, (const IO*)dy, dfinal, (IO*)nullptr, (IO*)nullptr,
                            (IO*)nullptr, (float*)nullptr, (float*)nullptr);
-        hipLaunchKernelGGL(k_rec_chain, chain_grid(a, 2), dim3(256), 0, s, a, p, sums, dfinal);
+        hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(256), 0, s, a, p, sums, dfinal);
       }
       hipLaunchKernelGGL((k_rec_bwd<IO, D, G, K, false>), dim3(blocks + more), dim3(threads_of(p)), 0,
                          s, a, p, tiles, sums, chained, (const IO*)dy, dfinal, (IO*)g.dx, (IO*)g.dg,
