@@ -441,7 +441,7 @@ ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* resi
  * the scan above, and their limits; of launches below 2^32 threads: the recurrence takes rows (dense:
  * of sequences rounded up to 16) times channels / 128 (fp32: / 64), rounded up, below about 2^30, the
  * rotation rows times ngroups / 4 and nfreq / 4 + (dstate - 2 nfreq) / 8 below 2^32, the group norm
- * sequences times ngroups below 2^24 where a sequence may have more than 8 tokens. */
+ * sequences times ngroups below 2^26 where a sequence may have more than 8 tokens. */
 
 /* Gated linear recurrence. For every channel of each sequence, with v = sigmoid(input_gate) x (x where
  * input_gate is NULL):

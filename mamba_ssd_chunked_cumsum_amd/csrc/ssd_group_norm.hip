@@ -2,23 +2,26 @@
 // group's channels, v = n w + b, y = v / (1 + exp(-v)); forward and backward.
 //
 // A few operations for each element: bound by memory. Where a sequence's tokens fit a thread's
-// registers (up to 8 of them), a block holds whole groups of them and each element is loaded once.
-// Longer sequences are cut into strips of rows: one kernel leaves each strip's mean and squared
-// deviations (backward: sums of dv and dv n) of every channel, so that a group may have any number of
-// channels; one adds them up, one applies them. The second pass over x (and dy) finds what the last-
-// level cache kept.
+// registers (up to 8 of them), a wave or block holds whole groups of them and each element is loaded
+// once.
+// Longer sequences are cut into strips of rows and tiles of channels: one kernel leaves the mean and
+// squared deviations (backward: sums of g and g n, and what dw and db need) of every group's piece in
+// every strip; the second adds up those of its groups while its first rows are on their way, and
+// finds what the last-level cache kept of x (and dy). A group may have any number of channels.
 //
 // Squared deviations are taken from a value of the strip itself (its first row, channel by channel):
 // their sum about that value is at most n + 1 times the sum about the mean for n rows, so the
 // difference keeps all but a few bits wherever the mean lies.
 #include "ssd_recurrent.h"
-#include "ssd_rows.h"
+#include "ssd_selective.h"
 
 namespace ssd {
 
 namespace {
 
-constexpr int V = 8, kStrip = 64, kTile = 64 * V, kThreads = 256, kWaves = kThreads / 64;
+constexpr int V = 8, kTile = 64 * V, kThreads = 256, kWaves = kThreads / 64;
+constexpr int kBlocks = 512;   // two for each of the card's 256 compute units
+constexpr int kAhead = 4;      // rows of a wave that are loaded together
 constexpr int kHeld = 8;       // tokens that a thread holds
 constexpr int kBlockC = 2048;  // channels of a block that holds whole groups
 
@@ -27,38 +30,55 @@ __device__ __forceinline__ float act_slope(float v) {  // of v sigmoid(v)
   return s * fmaf(v, 1.f - s, 1.f);
 }
 
-// A strip of one sequence, or of all rows (packed: the part of each sequence in it has a slot of
-// its own, strip + sequence, which grows by one from each part to the next).
-struct Strips {
-  int per, n;     // strips of a sequence (dense), strips
-  int64_t slots;  // partial results
+// ---- how a problem is cut --------------------------------------------------------------------------
+// Strips of `rows` rows, of each sequence or (packed) of all rows, where the part of each sequence in a
+// strip has a slot of its own: strip + sequence, which grows by one from each part to the next. In the
+// same way the piece of a group in a tile of channels is piece tile + group.
+struct Cut {
+  int rows, per, strips;  // rows of a strip; strips of a sequence (packed: of all rows); strips
+  int tiles, pieces;
+  int64_t slots;
 };
-Strips strips_of(const Rows& q) {
-  Strips t;
-  const int64_t rows = q.starts ? q.R : q.L;
-  t.per = (int)((rows + kStrip - 1) / kStrip);
-  t.n = q.starts ? t.per : (int)((int64_t)t.per * q.S);
-  t.slots = q.starts ? (int64_t)t.n + q.S : t.n;
+Cut cut_of(const GroupArgs& a) {
+  Cut t;
+  t.tiles = (a.C + kTile - 1) / kTile;
+  t.pieces = t.tiles + a.G;
+  const int64_t rows = a.rows.starts ? a.rows.R : a.rows.L, seqs = a.rows.starts ? 1 : a.rows.S;
+  t.rows = 64;  // shorter where that leaves compute units without blocks
+  while (t.rows > 16 && (rows + t.rows - 1) / t.rows * seqs * t.tiles < kBlocks) t.rows /= 2;
+  t.per = (int)((rows + t.rows - 1) / t.rows);
+  t.strips = (int)(t.per * seqs);
+  t.slots = t.strips + (a.rows.starts ? (int64_t)a.rows.S : 0);
   return t;
+}
+
+__device__ __forceinline__ int offset(const Rows& q, int i) {
+  typedef const __attribute__((address_space(4))) int* Words;  // read through scalar loads
+  return ((Words)(uintptr_t)q.starts)[__builtin_amdgcn_readfirstlane(i)];
 }
 
 // f(sequence, slot, first row, rows) for each part of a sequence in a strip; uniform over the block.
 template <typename F>
-__device__ __forceinline__ void parts(const Rows& q, int per, int strip, F f) {
+__device__ __forceinline__ void parts(const Rows& q, const Cut& t, int strip, F f) {
   if (!q.starts) {
-    const int s = strip / per, at = strip % per * kStrip;
-    f(s, (int64_t)strip, s * q.L + at, min(q.L - at, kStrip));
+    const int s = strip / t.per, at = strip % t.per * t.rows;
+    f(s, (int64_t)strip, s * q.L + at, min(q.L - at, t.rows));
     return;
   }
-  const int stop = min(q.R - strip * kStrip, kStrip) + strip * kStrip;
-  for (int r = strip * kStrip; r < stop;) {
-    const int s = seq_of(q, r);
-    if (s < 0) {
-      r = after_gap(q, r);
+  const int front = offset(q, 0), begin = strip * t.rows, stop = min(q.R - begin, t.rows) + begin;
+  for (int r = begin; r < stop;) {
+    if (r < front) {
+      r = min(front, stop);
       continue;
     }
-    const int end = min(seq_end(q, s), stop);
-    f(s, (int64_t)strip + s, r, end - r);
+    int lo = 0, hi = q.S;  // as seq_of
+    while (hi - lo > 1) {
+      const int m = lo + ((hi - lo) >> 1);
+      if (offset(q, m) <= r) lo = m; else hi = m;
+    }
+    const int end = min(offset(q, lo + 1), stop);
+    if (end <= r) return;  // behind the last
+    f(lo, (int64_t)strip + lo, r, end - r);
     r = end;
   }
 }
@@ -67,120 +87,185 @@ __device__ __forceinline__ void parts(const Rows& q, int per, int strip, F f) {
 struct Slots {
   int begin, end, strip0, n;
   int64_t first;
-  __device__ __forceinline__ Slots(const Rows& q, int per, int s) {
+  __device__ __forceinline__ Slots(const Rows& q, const Cut& t, int s) {
     begin = seq_begin(q, s);
     end = max(seq_end(q, s), begin);
     if (q.starts) {
-      strip0 = begin / kStrip;
+      strip0 = begin / t.rows;
       first = (int64_t)strip0 + s;
-      n = end > begin ? (end - 1) / kStrip - strip0 + 1 : 0;
+      n = end > begin ? (end - 1) / t.rows - strip0 + 1 : 0;
     } else {
       strip0 = 0;
-      first = (int64_t)s * per;
-      n = per;
+      first = (int64_t)s * t.per;
+      n = t.per;
     }
   }
-  __device__ __forceinline__ int rows(const Rows& q, int i) const {
-    if (!q.starts) return min(q.L - i * kStrip, kStrip);
-    const int at = (strip0 + i) * kStrip;
-    return min(end, q.R - at > kStrip ? at + kStrip : q.R) - max(begin, at);
+  __device__ __forceinline__ int rows(const Rows& q, const Cut& t, int i) const {
+    if (!q.starts) return min(q.L - i * t.rows, t.rows);
+    const int at = (strip0 + i) * t.rows;
+    return min(end, q.R - at > t.rows ? at + t.rows : q.R) - max(begin, at);
   }
 };
 
-// Sums over the waves of a block, in order, in wave 0. red: [waves][64 * 2 V].
-template <int N>
-__device__ __forceinline__ void add_waves(float (&v)[N], float (&red)[kWaves][N][64]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __syncthreads();
+// Rows [r, r + n) of a wave's share (every kWaves-th), kAhead at a time: load(k, row) for each, then
+// work(k, row); k is known at compile time.
+template <typename L, typename W>
+__device__ __forceinline__ void walk(int r, int n, L load, W work) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int i = wave;
+  for (; i + (kAhead - 1) * kWaves < n; i += kAhead * kWaves) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) red[wave][i][lane] = v[i];
-  __syncthreads();
-  if (wave == 0) {
+    for (int k = 0; k < kAhead; ++k) load(k, r + i + k * kWaves);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = ((v[i] + red[1][i][lane]) + red[2][i][lane]) + red[3][i][lane];
+    for (int k = 0; k < kAhead; ++k) work(k, r + i + k * kWaves);
+  }
+  if (i < n) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i + k * kWaves < n) load(k, r + i + k * kWaves);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i + k * kWaves < n) work(k, r + i + k * kWaves);
   }
 }
 
-__device__ __forceinline__ double block_sum(double v, double (&red)[kWaves]) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return ((red[0] + red[1]) + red[2]) + red[3];
+// Sums over the waves of a block, in order: column c of value i to out[i][c] in LDS, from where every
+// thread may take it.
+struct Columns {
+  float red[kWaves][2][kTile];
+  __device__ __forceinline__ void add(const float (&a)[V], const float (&b)[V]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();  // what was here has been read
+    store_vec<float, V>(&red[wave][0][lane * V], a);
+    store_vec<float, V>(&red[wave][1][lane * V], b);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * kTile; i += kThreads) {
+      float* p = &red[0][0][i];
+      *p = ((p[0] + p[2 * kTile]) + p[4 * kTile]) + p[6 * kTile];
+    }
+    __syncthreads();
+  }
+};
+
+// f(group, first channel, channels, lane of K) for every group with channels in the tile, K threads
+// each: f adds up what it finds over the group's channels in this tile.
+template <typename F>
+__device__ __forceinline__ void groups_of_tile(const GroupArgs& q, int tile, F f) {
+  const int cg = q.C / q.G, c0 = tile * kTile, c1 = min(c0 + kTile, q.C);
+  const int g0 = c0 / cg, g1 = (c1 - 1) / cg + 1;
+  const int n = g1 - g0, per = n <= 4 ? 64 : n <= 8 ? 32 : n <= 16 ? 16 : n <= 32 ? 8 : n <= 64 ? 4 : 1;
+  for (int g = g0 + (int)threadIdx.x / per; g < g1; g += kThreads / per) {
+    const int a = max(g * cg, c0), b = min((g + 1) * cg, c1);
+    f(g, a - c0, b - a, (int)threadIdx.x % per, per);
+  }
+}
+template <typename F>
+__device__ __forceinline__ F sum_of(F v, int per) {  // over neighbouring threads, in each of them
+  for (int m = per >> 1; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
+  return v;
 }
 
-// ---- strips: forward ---------------------------------------------------------------------------------
-// part [slots, 2, C]: means, sums of squared deviations.
+// ---- sums over a sequence and group ------------------------------------------------------------------
+// Mean and 1 / sqrt(variance + eps) of a group from its pieces (mean, squared deviations), or (BACK) the
+// means of g and g n from their sums. `per` threads share it; sums in 64 bits, in a fixed order.
+template <bool BACK>
+__device__ __forceinline__ float2 total_of(const GroupArgs& q, const Cut& t, const float2* part, int s,
+                                           int g, int lane, int per) {
+  const int cg = q.C / q.G, t0 = g * cg / kTile, n = ((g + 1) * cg - 1) / kTile - t0 + 1;
+  const Slots at(q.rows, t, s);
+  double a = 0., b = 0., dev = 0.;
+  const int64_t all = (int64_t)at.n * n;
+  constexpr int U = 4;  // loads issued together
+  for (int64_t i0 = lane; i0 < all; i0 += U * per) {
+    float2 v[U];
+    int slot[U], tile[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = min(i0 + u * per, all - 1);
+      slot[u] = (int)(n == 1 ? i : i / n);
+      tile[u] = t0 + (n == 1 ? 0 : (int)(i - (int64_t)slot[u] * n));
+      v[u] = part[(at.first + slot[u]) * t.pieces + tile[u] + g];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * per >= all) break;
+      if (BACK) {
+        a += v[u].x;
+        b += v[u].y;
+      } else {
+        const int width = min((g + 1) * cg, (tile[u] + 1) * kTile) - max(g * cg, tile[u] * kTile);
+        const double m = v[u].x, k = (double)at.rows(q.rows, t, slot[u]) * width;
+        a += k * m;
+        b += k * m * m;  // (in 64 bits the difference below loses nothing that 32 hold)
+        dev += v[u].y;
+      }
+    }
+  }
+  a = sum_of(a, per);
+  b = sum_of(b, per);
+  const double count = (double)max(at.end - at.begin, 1) * cg;
+  if (BACK) return make_float2((float)(a / count), (float)(b / count));
+  dev = sum_of(dev, per);
+  const double mean = a / count, var = (dev + fmax(b - a * mean, 0.)) / count;
+  return make_float2((float)mean, (float)(1. / sqrt(var + q.eps)));
+}
+
+// out [S, G]: where a block of the second pass would have too much to add up, or stats are asked for
+// of sequences without tokens (0 and 1 / sqrt(eps)). A wave each.
+template <bool BACK>
+__global__ __launch_bounds__(kThreads) void k_gn_totals(GroupArgs q, Cut t, const float2* part,
+                                                        float2* out) {
+  const int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  if (u >= (int64_t)q.rows.S * q.G) return;
+  const float2 v = total_of<BACK>(q, t, part, (int)(u / q.G), (int)(u % q.G), threadIdx.x & 63, 64);
+  if ((threadIdx.x & 63) == 0) out[u] = v;
+}
+
+// ---- forward -----------------------------------------------------------------------------------------
+// part [slots, pieces]: mean and sum of squared deviations.
 template <typename IO>
-__global__ __launch_bounds__(kThreads) void k_gn_parts(GroupArgs q, int per, int tiles, float* part) {
-  __shared__ float red[kWaves][2 * V][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c0 = (int)(blockIdx.x % tiles) * kTile + lane * V;
-  const bool live = c0 < q.C;
-  const int c = live ? c0 : q.C - V;
+__global__ __launch_bounds__(kThreads) void k_gn_parts(GroupArgs q, Cut t, float2* part) {
+  __shared__ Columns col;
+  const int lane = threadIdx.x & 63, tile = (int)(blockIdx.x % t.tiles);
+  const int c = min(tile * kTile + lane * V, q.C - V);  // idle lanes load the last channels again
   const IO* x = (const IO*)q.x + c;
-  parts(q.rows, per, (int)(blockIdx.x / tiles), [&](int, int64_t slot, int r, int n) {
-    Vec<IO, V> first, v;
-    float sum[2 * V];
+  parts(q.rows, t, (int)(blockIdx.x / t.tiles), [&](int, int64_t slot, int r, int n) {
+    Vec<IO, V> first, v[kAhead];
+    float sum[V], sq[V];
     first.load(x + r * q.xs);
 #pragma unroll
-    for (int j = 0; j < 2 * V; ++j) sum[j] = 0.f;
-#pragma unroll 4
-    for (int i = wave; i < n; i += kWaves) {
-      v.load(x + (int64_t)(r + i) * q.xs);
+    for (int j = 0; j < V; ++j) sum[j] = sq[j] = 0.f;
+    walk(r, n, [&](int k, int row) { v[k].load(x + row * q.xs); },
+         [&](int k, int) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float d = v.get(j) - first.get(j);
-        sum[j] += d;
-        sum[V + j] = fmaf(d, d, sum[V + j]);
+           for (int j = 0; j < V; ++j) {
+             const float d = v[k].get(j) - first.get(j);
+             sum[j] += d;
+             sq[j] = fmaf(d, d, sq[j]);
+           }
+         });
+    col.add(sum, sq);
+    // each channel's mean and deviations, from its first row's value
+    const float rows = (float)n;
+    const IO* top = (const IO*)q.x + r * q.xs + tile * kTile;
+    groups_of_tile(q, tile, [&](int g, int c0, int width, int me, int per) {
+      float mean = 0.f, dev = 0.f;
+      for (int i = c0 + me; i < c0 + width; i += per) {
+        const float d = col.red[0][0][i] / rows;
+        mean += Io<IO>::load(top, i) + d;
+        dev += fmaxf(fmaf(-d, col.red[0][0][i], col.red[0][1][i]), 0.f);
       }
-    }
-    add_waves(sum, red);
-    if (wave == 0 && live) {
-      float mean[V], dev[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float d = sum[j] / n;
-        mean[j] = first.get(j) + d;
-        dev[j] = fmaxf(fmaf(-d, sum[j], sum[V + j]), 0.f);
+      mean = sum_of(mean, per) / width;
+      for (int i = c0 + me; i < c0 + width; i += per) {
+        const float d = Io<IO>::load(top, i) + col.red[0][0][i] / rows - mean;
+        dev = fmaf(rows * d, d, dev);
       }
-      store_vec<float, V>(part + slot * 2 * q.C + c, mean);
-      store_vec<float, V>(part + (slot * 2 + 1) * q.C + c, dev);
-    }
+      dev = sum_of(dev, per);
+      if (me == 0) part[slot * t.pieces + tile + g] = make_float2(mean, dev);
+    });
   });
 }
 
-// A block a sequence and group: stats [S, G, 2], mean and 1 / sqrt(variance + eps); (0, 1 / sqrt(eps))
-// of a sequence without tokens. Sums in 64 bits: a thread adds as many values as the sequence is long.
-__global__ __launch_bounds__(kThreads) void k_gn_stats(GroupArgs q, int per, const float* part,
-                                                       float* stats) {
-  __shared__ double red[kWaves];
-  const int s = (int)(blockIdx.x / q.G), g = (int)(blockIdx.x % q.G), cg = q.C / q.G;
-  const Slots at(q.rows, per, s);
-  const double count = (double)(at.end - at.begin) * cg;
-  const int64_t all = (int64_t)at.n * cg;
-  double sum = 0.;
-  for (int64_t i = threadIdx.x; i < all; i += kThreads) {
-    const int slot = (int)(i / cg), c = g * cg + (int)(i % cg);
-    sum += (double)at.rows(q.rows, slot) * part[(at.first + slot) * 2 * q.C + c];
-  }
-  const double mean = at.n ? block_sum(sum, red) / count : 0.;
-  double dev = 0.;
-  for (int64_t i = threadIdx.x; i < all; i += kThreads) {
-    const int slot = (int)(i / cg), c = g * cg + (int)(i % cg);
-    const float* p = part + (at.first + slot) * 2 * q.C + c;
-    const double d = p[0] - mean;
-    dev += at.rows(q.rows, slot) * d * d + p[q.C];
-  }
-  const double var = at.n ? block_sum(dev, red) / count : 0.;
-  if (threadIdx.x == 0) {
-    stats[2 * (int64_t)blockIdx.x] = (float)mean;
-    stats[2 * (int64_t)blockIdx.x + 1] = (float)(1. / sqrt(var + q.eps));
-  }
-}
-
-// w rstd, mean and b of a thread's channels in sequence s.
 struct Affine {
   float w[V], b[V];
   __device__ __forceinline__ Affine(const GroupArgs& q, int c) {
@@ -190,166 +275,203 @@ struct Affine {
     if (q.b) load_f32<V>(q.b + c, b);
   }
 };
-__device__ __forceinline__ void load_stats(const GroupArgs& q, const float* stats, int s, int c,
-                                           float (&mean)[V], float (&rstd)[V]) {
-  const int cg = q.C / q.G;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const float2 st = reinterpret_cast<const float2*>(stats)[(int64_t)s * q.G + (c + j) / cg];
-    mean[j] = st.x;
-    rstd[j] = st.y;
-  }
-}
 
-template <typename IO>
-__global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, int per, int tiles,
-                                                       const float* stats, IO* y) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (int)(blockIdx.x % tiles) * kTile + lane * V;
-  if (c >= q.C) return;
-  const IO* x = (const IO*)q.x + c;
-  const Affine af(q, c);
-  parts(q.rows, per, (int)(blockIdx.x / tiles), [&](int s, int64_t, int r, int n) {
-    float mean[V], rstd[V], o[V];
-    load_stats(q, stats, s, c, mean, rstd);
-#pragma unroll 4
-    for (int i = wave; i < n; i += kWaves) {
-      Vec<IO, V> v;
-      v.load(x + (int64_t)(r + i) * q.xs);
+// A pair a group of the tile (statistics, or means of the backward pass), of sequence s: read, or added
+// up here (`add`); to v of this thread's channels.
+struct Pairs {
+  float2 of[kTile];
+  template <bool BACK>
+  __device__ __forceinline__ void get(const GroupArgs& q, const Cut& t, const float2* part,
+                                      const float2* ready, int s, int tile, int c, float2 (&v)[V],
+                                      float2* out) {
+    const int cg = q.C / q.G;
+    if (ready) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        o[j] = fmaf((v.get(j) - mean[j]) * rstd[j], af.w[j], af.b[j]);
-        if (q.act) o[j] *= sigmoid(o[j]);
-      }
-      store_vec<IO, V>(y + (int64_t)(r + i) * q.C + c, o);
+      for (int j = 0; j < V; ++j) v[j] = ready[(int64_t)s * q.G + (c + j) / cg];
+      return;
     }
-  });
-}
+    const int g0 = tile * kTile / cg;
+    __syncthreads();  // what was here has been read
+    groups_of_tile(q, tile, [&](int g, int, int, int me, int per) {
+      const float2 p = total_of<BACK>(q, t, part, s, g, me, per);
+      if (me == 0) {
+        of[g - g0] = p;
+        if (out) out[(int64_t)s * q.G + g] = p;
+      }
+    });
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = of[(c + j) / cg - g0];
+  }
+};
 
-// ---- strips: backward --------------------------------------------------------------------------------
-// part [slots, 2, C]: sums of dv and of dv n over a part's rows.
+// stats: written where given and not `ready` (by each strip alike: the same bits).
 template <typename IO>
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, int per, int tiles,
-                                                           const float* stats, const IO* dy,
-                                                           float* part) {
-  __shared__ float red[kWaves][2 * V][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c0 = (int)(blockIdx.x % tiles) * kTile + lane * V;
+__global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const float2* part,
+                                                       const float2* ready, float2* stats, IO* y) {
+  __shared__ Pairs pairs;
+  const int lane = threadIdx.x & 63, tile = (int)(blockIdx.x % t.tiles);
+  const int c0 = tile * kTile + lane * V, c = min(c0, q.C - V);
   const bool live = c0 < q.C;
-  const int c = live ? c0 : q.C - V;
   const IO* x = (const IO*)q.x + c;
   const Affine af(q, c);
-  parts(q.rows, per, (int)(blockIdx.x / tiles), [&](int s, int64_t slot, int r, int n) {
-    float mean[V], rstd[V], sum[2 * V];
-    load_stats(q, stats, s, c, mean, rstd);
+  parts(q.rows, t, (int)(blockIdx.x / t.tiles), [&](int s, int64_t, int r, int n) {
+    float2 st[V];
+    float o[V];
+    Vec<IO, V> v[kAhead];
+    pairs.get<false>(q, t, part, ready, s, tile, c, st, stats);
+    walk(r, n, [&](int k, int row) { v[k].load(x + row * q.xs); },
+         [&](int k, int row) {
 #pragma unroll
-    for (int j = 0; j < 2 * V; ++j) sum[j] = 0.f;
-#pragma unroll 4
-    for (int i = wave; i < n; i += kWaves) {
-      Vec<IO, V> v, d;
-      v.load(x + (int64_t)(r + i) * q.xs);
-      d.load(dy + (int64_t)(r + i) * q.C + c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float nv = (v.get(j) - mean[j]) * rstd[j];
-        float dv = d.get(j);
-        if (q.act) dv *= act_slope(fmaf(nv, af.w[j], af.b[j]));
-        sum[j] += dv;
-        sum[V + j] = fmaf(dv, nv, sum[V + j]);
-      }
-    }
-    add_waves(sum, red);
-    if (wave == 0 && live) {
-      float a[V], b[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) a[j] = sum[j], b[j] = sum[V + j];
-      store_vec<float, V>(part + slot * 2 * q.C + c, a);
-      store_vec<float, V>(part + (slot * 2 + 1) * q.C + c, b);
-    }
+           for (int j = 0; j < V; ++j) {
+             o[j] = fmaf((v[k].get(j) - st[j].x) * st[j].y, af.w[j], af.b[j]);
+             if (q.act) o[j] *= sigmoid(o[j]);
+           }
+           if (live) store_vec<IO, V>(y + (int64_t)row * q.C + c, o);
+         });
   });
 }
 
-// Sums over a sequence's slots, in 64 bits: total [S, 2, C]. 64 columns a block, four groups of slots.
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_total(GroupArgs q, int per, int cols,
-                                                           const float* part, float* total) {
-  __shared__ double red[kWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int s = (int)(blockIdx.x / cols);
-  const int64_t m = (int64_t)(blockIdx.x % cols) * 64 + lane, M = 2 * (int64_t)q.C;
-  const Slots at(q.rows, per, s);
-  double sum = 0.;
-  if (m < M) {
-#pragma unroll 4
-    for (int i = wave; i < at.n; i += kWaves) sum += part[(at.first + i) * M + m];
-  }
-  red[wave][lane] = sum;
-  __syncthreads();
-  if (wave == 0 && m < M)
-    total[s * M + m] = (float)(((sum + red[1][lane]) + red[2][lane]) + red[3][lane]);
-}
-
-// Means over each sequence and group of g = dv w and of g n: mid [S, G, 2]. A wave each.
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_means(GroupArgs q, const float* total, float* mid) {
-  const int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (u >= (int64_t)q.rows.S * q.G) return;
-  const int s = (int)(u / q.G), g = (int)(u % q.G), cg = q.C / q.G;
-  float a = 0.f, b = 0.f;
-  for (int i = threadIdx.x & 63; i < cg; i += 64) {
-    const int c = g * cg + i;
-    const float w = q.w ? q.w[c] : 1.f;
-    const float* t = total + (int64_t)s * 2 * q.C + c;
-    a = fmaf(w, t[0], a);
-    b = fmaf(w, t[q.C], b);
-  }
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    a += __shfl_xor(a, m, kWave);
-    b += __shfl_xor(b, m, kWave);
-  }
-  const float count = (float)max(seq_end(q.rows, s) - seq_begin(q.rows, s), 1) * cg;
-  if ((threadIdx.x & 63) == 0)
-    reinterpret_cast<float2*>(mid)[u] = make_float2(a / count, b / count);
-}
-
-// dx = rstd (g - mean(g) - n mean(g n)); zero in rows of no sequence.
+// ---- backward ----------------------------------------------------------------------------------------
+// part [slots, pieces]: sums of g = w dv and of g n. chan [strips, 2, C]: sums of dv (db), of dv n (dw).
 template <typename IO>
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, int per, int tiles,
-                                                           const float* stats, const float* mid,
-                                                           const IO* dy, IO* dx) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (int)(blockIdx.x % tiles) * kTile + lane * V;
-  if (c >= q.C) return;
+__global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, Cut t, const float2* stats,
+                                                           const IO* dy, float2* part, float* chan) {
+  __shared__ Columns col;
+  const int lane = threadIdx.x & 63, tile = (int)(blockIdx.x % t.tiles);
+  const int strip = (int)(blockIdx.x / t.tiles);
+  const int c = min(tile * kTile + lane * V, q.C - V), cg = q.C / q.G;
   const IO* x = (const IO*)q.x + c;
+  const IO* d = dy + c;
   const Affine af(q, c);
-  const int strip = (int)(blockIdx.x / tiles);
+  float db[kTile / kThreads], dw[kTile / kThreads];  // of channels tile * kTile + threadIdx.x + i 256
+#pragma unroll
+  for (int i = 0; i < kTile / kThreads; ++i) db[i] = dw[i] = 0.f;
+  parts(q.rows, t, strip, [&](int s, int64_t slot, int r, int n) {
+    float2 st[V];
+    float a[V], b[V];
+    Vec<IO, V> v[kAhead], e[kAhead];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      st[j] = stats[(int64_t)s * q.G + (c + j) / cg];
+      a[j] = b[j] = 0.f;
+    }
+    walk(r, n,
+         [&](int k, int row) {
+           v[k].load(x + row * q.xs);
+           e[k].load(d + (int64_t)row * q.C);
+         },
+         [&](int k, int) {
+#pragma unroll
+           for (int j = 0; j < V; ++j) {
+             const float nv = (v[k].get(j) - st[j].x) * st[j].y;
+             float dv = e[k].get(j);
+             if (q.act) dv *= act_slope(fmaf(nv, af.w[j], af.b[j]));
+             a[j] += dv;
+             b[j] = fmaf(dv, nv, b[j]);
+           }
+         });
+    col.add(a, b);
+    groups_of_tile(q, tile, [&](int g, int c0, int width, int me, int per) {
+      float m1 = 0.f, m2 = 0.f;
+      for (int i = c0 + me; i < c0 + width; i += per) {
+        const float w = q.w ? q.w[tile * kTile + i] : 1.f;
+        m1 = fmaf(w, col.red[0][0][i], m1);
+        m2 = fmaf(w, col.red[0][1][i], m2);
+      }
+      m1 = sum_of(m1, per);
+      m2 = sum_of(m2, per);
+      if (me == 0) part[slot * t.pieces + tile + g] = make_float2(m1, m2);
+    });
+#pragma unroll
+    for (int i = 0; i < kTile / kThreads; ++i) {
+      db[i] += col.red[0][0][threadIdx.x + i * kThreads];
+      dw[i] += col.red[0][1][threadIdx.x + i * kThreads];
+    }
+  });
+  if (!chan) return;
+#pragma unroll
+  for (int i = 0; i < kTile / kThreads; ++i) {
+    const int at = tile * kTile + threadIdx.x + i * kThreads;
+    if (at < q.C) {
+      chan[(int64_t)strip * 2 * q.C + at] = db[i];
+      chan[((int64_t)strip * 2 + 1) * q.C + at] = dw[i];
+    }
+  }
+}
+
+// dx = rstd (g - mean(g) - n mean(g n)); zero in rows of no sequence. The blocks behind the strips' add
+// up the columns of chan, 64 each, in a fixed order.
+template <typename IO>
+__global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, Cut t, const float2* stats,
+                                                           const float2* part, const float2* ready,
+                                                           const float* chan, const IO* dy, IO* dx,
+                                                           float* dw, float* db) {
+  __shared__ Pairs pairs;
+  const int64_t main_blocks = (int64_t)t.strips * t.tiles;
+  const int lane = threadIdx.x & 63;
+  if (blockIdx.x >= main_blocks) {
+    double* red = reinterpret_cast<double*>(&pairs);
+    const int64_t m = (blockIdx.x - main_blocks) * 64 + lane, M = 2 * (int64_t)q.C;
+    double sum = 0.;
+    if (m < M) {
+#pragma unroll 8
+      for (int i = threadIdx.x >> 6; i < t.strips; i += kWaves) sum += chan[i * M + m];
+    }
+    red[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < 64 && m < M) {
+      const float v = (float)(((sum + red[64 + lane]) + red[128 + lane]) + red[192 + lane]);
+      if (m < q.C) {
+        if (db) db[m] = v;
+      } else if (dw) {
+        dw[m - q.C] = v;
+      }
+    }
+    return;
+  }
+  const int tile = (int)(blockIdx.x % t.tiles), strip = (int)(blockIdx.x / t.tiles), cg = q.C / q.G;
+  const int c0 = tile * kTile + lane * V, c = min(c0, q.C - V);
+  const bool live = c0 < q.C;
+  const IO* x = (const IO*)q.x + c;
+  const IO* d = dy + c;
+  const Affine af(q, c);
   float o[V];
-  if (q.rows.starts) {
+  int done = strip * t.rows;  // packed: rows up to here are in a sequence or have been cleared
+  const int wave = threadIdx.x >> 6;
+  auto clear = [&](int to) {
 #pragma unroll
     for (int j = 0; j < V; ++j) o[j] = 0.f;
-    const int stop = min(q.rows.R - strip * kStrip, kStrip);
-    for (int i = wave; i < stop; i += kWaves)
-      if (seq_of(q.rows, strip * kStrip + i) < 0)
-        store_vec<IO, V>(dx + (int64_t)(strip * kStrip + i) * q.C + c, o);
-  }
-  parts(q.rows, per, strip, [&](int s, int64_t, int r, int n) {
-    float mean[V], rstd[V], m1[V], m2[V];
-    load_stats(q, stats, s, c, mean, rstd);
-    load_stats(q, mid, s, c, m1, m2);
-#pragma unroll 4
-    for (int i = wave; i < n; i += kWaves) {
-      Vec<IO, V> v, d;
-      v.load(x + (int64_t)(r + i) * q.xs);
-      d.load(dy + (int64_t)(r + i) * q.C + c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float nv = (v.get(j) - mean[j]) * rstd[j];
-        float g = d.get(j) * af.w[j];
-        if (q.act) g *= act_slope(fmaf(nv, af.w[j], af.b[j]));
-        o[j] = rstd[j] * (g - m1[j] - nv * m2[j]);
-      }
-      store_vec<IO, V>(dx + (int64_t)(r + i) * q.C + c, o);
+    if (live)
+      for (int i = done + wave; i < to; i += kWaves) store_vec<IO, V>(dx + (int64_t)i * q.C + c, o);
+  };
+  parts(q.rows, t, strip, [&](int s, int64_t, int r, int n) {
+    float2 st[V], m[V];
+    Vec<IO, V> v[kAhead], e[kAhead];
+    if (q.rows.starts) {
+      clear(r);
+      done = r + n;
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) st[j] = stats[(int64_t)s * q.G + (c + j) / cg];
+    pairs.get<true>(q, t, part, ready, s, tile, c, m, nullptr);
+    walk(r, n,
+         [&](int k, int row) {
+           v[k].load(x + row * q.xs);
+           e[k].load(d + (int64_t)row * q.C);
+         },
+         [&](int k, int row) {
+#pragma unroll
+           for (int j = 0; j < V; ++j) {
+             const float nv = (v[k].get(j) - st[j].x) * st[j].y;
+             float g = e[k].get(j) * af.w[j];
+             if (q.act) g *= act_slope(fmaf(nv, af.w[j], af.b[j]));
+             o[j] = st[j].y * (g - m[j].x - nv * m[j].y);
+           }
+           if (live) store_vec<IO, V>(dx + (int64_t)row * q.C + c, o);
+         });
   });
+  if (q.rows.starts) clear(min(q.rows.R - strip * t.rows, t.rows) + strip * t.rows);
 }
 
 // ---- sequences of a few tokens -----------------------------------------------------------------------
@@ -507,6 +629,126 @@ __global__ __launch_bounds__(kThreads) void k_gn_few_bwd(GroupArgs q, Few f, int
   }
 }
 
+// ---- single tokens -----------------------------------------------------------------------------------
+// Sequences of one token whose groups are 1, 2, 4 .. 64 vectors: the lanes of a group are neighbours in a
+// wave, and a thread takes the same eight channels of NV tokens (backward: of every walkers-th), whose
+// loads it issues together and which share weight and bias. No LDS and no barrier.
+bool single_tokens(const GroupArgs& a) {
+  const int cg = a.C / a.G, vg = cg / V;
+  return !a.rows.starts && a.rows.L == 1 && cg % V == 0 && vg <= 64 && (vg & (vg - 1)) == 0;
+}
+
+__device__ __forceinline__ float lanes_sum(float v, int vg) {  // vg: uniform
+  if (vg >= 2) v = add_dpp<0xB1>(v);    // quad_perm [1,0,3,2]
+  if (vg >= 4) v = add_dpp<0x4E>(v);    // quad_perm [2,3,0,1]
+  if (vg >= 8) v = add_dpp<0x141>(v);   // row_half_mirror
+  if (vg >= 16) v = add_dpp<0x140>(v);  // row_mirror
+  if (vg >= 32) v += __shfl_xor(v, 16, kWave);
+  if (vg >= 64) v += __shfl_xor(v, 32, kWave);
+  return v;
+}
+
+// The n-th of this launch's threads as (row of `width`, place in it).
+struct Flat {
+  int64_t row;
+  int at;
+  __device__ __forceinline__ Flat(int width) {
+    const int64_t first = (int64_t)blockIdx.x * kThreads;
+    const unsigned rest = (unsigned)(first % width) + threadIdx.x;
+    row = first / width + rest / width;
+    at = (int)(rest % width);
+  }
+};
+
+template <typename IO, int NV>
+__global__ __launch_bounds__(kThreads) void k_gn_tokens(GroupArgs q, float2* stats, IO* y) {
+  const int cg = q.C / q.G, vg = cg / V;
+  const Flat f(q.C / V);
+  const int64_t s0 = f.row * NV;
+  if (s0 >= q.rows.S) return;  // whole groups
+  const int c = f.at * V;
+  Vec<IO, V> v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i].load((const IO*)q.x + min(s0 + i, (int64_t)q.rows.S - 1) * q.xs + c);
+  const Affine af(q, c);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (s0 + i >= q.rows.S) break;
+    float sum = 0.f, dev = 0.f, o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum += v[i].get(j);
+    const float mean = lanes_sum(sum, vg) / cg;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = v[i].get(j) - mean;
+      dev = fmaf(d, d, dev);
+    }
+    const float rstd = 1.f / sqrtf(lanes_sum(dev, vg) / cg + q.eps);
+    if (stats && f.at % vg == 0) stats[(s0 + i) * q.G + c / cg] = make_float2(mean, rstd);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      o[j] = fmaf((v[i].get(j) - mean) * rstd, af.w[j], af.b[j]);
+      if (q.act) o[j] *= sigmoid(o[j]);
+    }
+    store_vec<IO, V>(y + (s0 + i) * q.C + c, o);
+  }
+}
+
+// part [walkers, 2, C]: sums of dv (db) and of dv n (dw).
+template <typename IO, int NV>
+__global__ __launch_bounds__(kThreads) void k_gn_tokens_bwd(GroupArgs q, int walkers, const float2* stats,
+                                                            const IO* dy, IO* dx, float* part) {
+  const int cg = q.C / q.G, vg = cg / V;
+  const Flat f(q.C / V);
+  if (f.row >= walkers) return;
+  const int c = f.at * V, g = c / cg;
+  const Affine af(q, c);
+  float dw[V], db[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.f;
+  for (int64_t s0 = f.row; s0 < q.rows.S; s0 += (int64_t)NV * walkers) {
+    Vec<IO, V> v[NV], d[NV];
+    float2 st[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t s = min(s0 + (int64_t)i * walkers, (int64_t)q.rows.S - 1);
+      v[i].load((const IO*)q.x + s * q.xs + c);
+      d[i].load(dy + s * q.C + c);
+      st[i] = stats[s * q.G + g];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t s = s0 + (int64_t)i * walkers;
+      if (s >= q.rows.S) break;
+      float n[V], e[V], a = 0.f, b = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        n[j] = (v[i].get(j) - st[i].x) * st[i].y;
+        e[j] = d[i].get(j);
+        if (q.act) e[j] *= act_slope(fmaf(n[j], af.w[j], af.b[j]));
+        db[j] += e[j];
+        dw[j] = fmaf(e[j], n[j], dw[j]);
+        e[j] *= af.w[j];
+        a += e[j];
+        b = fmaf(e[j], n[j], b);
+      }
+      const float m1 = lanes_sum(a, vg) / cg, m2 = lanes_sum(b, vg) / cg;
+#pragma unroll
+      for (int j = 0; j < V; ++j) e[j] = st[i].y * (e[j] - m1 - n[j] * m2);
+      store_vec<IO, V>(dx + s * q.C + c, e);
+    }
+  }
+  float* p = part + f.row * 2 * q.C + c;
+  store_vec<float, V>(p, db);
+  store_vec<float, V>(p + q.C, dw);
+}
+
+// Walkers of every vector of channels: 131072 threads, two waves a SIMD, and at least 4 tokens each.
+int token_walkers(const GroupArgs& a) {
+  const int64_t want = ((int64_t)a.rows.S + 3) / 4, most = 131072 / (a.C / V);
+  return (int)(want < most ? want : most < 1 ? 1 : most);
+}
+
 // Blocks of a slice that walk the sequences: at most 1024 in all, at least 4 turns each.
 int walkers_of(const GroupArgs& a, const Few& f) {
   const int64_t turns = ((int64_t)a.rows.S + f.seqs - 1) / f.seqs;
@@ -514,34 +756,54 @@ int walkers_of(const GroupArgs& a, const Few& f) {
   return (int)(want < most ? want : most < 1 ? 1 : most);
 }
 
-int tiles_of(const GroupArgs& a) { return (a.C + kTile - 1) / kTile; }
-
 int64_t up64(int64_t floats) { return (floats + 63) / 64 * 64; }
+
+// A block of the second pass adds up its groups' pieces by itself up to 16 values a thread. (Sums of
+// sequences without tokens have no block, so packed stats are always written by a kernel of their own.)
+bool adds_itself(const GroupArgs& a, const Cut& t, bool stats) {
+  if (stats && a.rows.starts) return false;
+  const int cg = a.C / a.G;
+  const int64_t groups = kTile / cg + 2, pieces = cg / kTile + 2;
+  return groups * pieces * t.per <= 16 * kThreads;
+}
 
 }  // namespace
 
-int64_t group_norm_bytes(const GroupArgs& a) {
-  if (few_tokens(a)) return 0;
-  const Strips t = strips_of(a.rows);
-  return 4 * (up64(t.slots * 2 * a.C) + (int64_t)a.rows.S * a.G * 2);
-}
-
 bool group_norm_fits(const GroupArgs& a) {
   auto fits = [](double blocks) { return blocks * kThreads < 4294967296.0; };
+  if (single_tokens(a)) return fits(double(a.rows.S) * (a.C / V) / kThreads + 1);
   if (few_tokens(a)) {
     const Few f = few_of(a);
     return fits((double(a.rows.S) / f.seqs + 1) * f.slices);
   }
-  const double strips = a.rows.starts ? double(a.rows.R) / kStrip + 1
-                                      : (double(a.rows.L) / kStrip + 1) * a.rows.S;
-  const double slots = strips + (a.rows.starts ? a.rows.S : 0);
-  return fits(strips * tiles_of(a)) && fits(double(a.rows.S) * a.G) &&
-         fits(double(a.rows.S) * (a.C / 32 + 1)) && slots * 2 * a.C < 1099511627776.0;
+  const double tiles = a.C / kTile + 1, rows = a.rows.starts ? a.rows.R : a.rows.L;
+  const double strips = (rows / 16 + 1) * (a.rows.starts ? 1 : a.rows.S);
+  return fits(strips * tiles + a.C) && fits(double(a.rows.S) * a.G / kWaves + 1) &&
+         (strips + a.rows.S) * (tiles + a.G) < 1099511627776.0 && strips < 2147483648.0;
 }
 
-hipError_t launch_group_norm(const GroupArgs& a, void* y, float* stats, float* ws, hipStream_t s) {
+int64_t group_norm_bytes(const GroupArgs& a) {
+  if (single_tokens(a) || few_tokens(a)) return 0;
+  const Cut t = cut_of(a);
+  return 8 * (up64(t.slots * t.pieces) + (int64_t)a.rows.S * a.G);
+}
+
+hipError_t launch_group_norm(const GroupArgs& a, void* y, float* stats, float* ws,
+                             hipStream_t s) {
   auto run = [&](auto io) {
     using IO = decltype(io);
+    if (single_tokens(a)) {
+      auto go = [&](auto tokens) {
+        constexpr int NV = decltype(tokens)::value;
+        const int64_t n = ((int64_t)a.rows.S + NV - 1) / NV * (a.C / V);
+        hipLaunchKernelGGL((k_gn_tokens<IO, NV>), dim3((unsigned)((n + kThreads - 1) / kThreads)),
+                           dim3(kThreads), 0, s, a, (float2*)stats, (IO*)y);
+        return hipGetLastError();
+      };
+      // four tokens a thread once that leaves four waves a SIMD
+      if ((int64_t)a.rows.S * (a.C / V) >= 4 * 262144) return go(std::integral_constant<int, 4>{});
+      return go(std::integral_constant<int, 1>{});
+    }
     if (few_tokens(a)) {
       const Few f = few_of(a);
       const int64_t blocks = ((int64_t)a.rows.S + f.seqs - 1) / f.seqs * f.slices;
@@ -549,33 +811,46 @@ hipError_t launch_group_norm(const GroupArgs& a, void* y, float* stats, float* w
                          (IO*)y);
       return hipGetLastError();
     }
-    const Strips t = strips_of(a.rows);
-    const int tiles = tiles_of(a);
-    if (!stats) stats = ws + up64(t.slots * 2 * a.C);
-    const dim3 grid((unsigned)((int64_t)t.n * tiles));
-    hipLaunchKernelGGL((k_gn_parts<IO>), grid, dim3(kThreads), 0, s, a, t.per, tiles, ws);
-    hipLaunchKernelGGL(k_gn_stats, dim3((unsigned)((int64_t)a.rows.S * a.G)), dim3(kThreads), 0, s, a,
-                       t.per, ws, stats);
-    hipLaunchKernelGGL((k_gn_apply<IO>), grid, dim3(kThreads), 0, s, a, t.per, tiles, stats, (IO*)y);
+    const Cut t = cut_of(a);
+    float2 *part = (float2*)ws, *ready = nullptr;
+    const dim3 grid((unsigned)((int64_t)t.strips * t.tiles));
+    hipLaunchKernelGGL((k_gn_parts<IO>), grid, dim3(kThreads), 0, s, a, t, part);
+    if (!adds_itself(a, t, stats != nullptr)) {
+      ready = stats ? (float2*)stats : part + up64(t.slots * t.pieces);
+      hipLaunchKernelGGL((k_gn_totals<false>),
+                         dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
+                         dim3(kThreads), 0, s, a, t, part, ready);
+    }
+    hipLaunchKernelGGL((k_gn_apply<IO>), grid, dim3(kThreads), 0, s, a, t, part, ready,
+                       (float2*)stats, (IO*)y);
     return hipGetLastError();
   };
   return a.io == kIoBf16 ? run(u16{}) : run(float{});
 }
 
 int64_t group_norm_backward_bytes(const GroupArgs& a) {
+  if (single_tokens(a)) return 4 * (int64_t)token_walkers(a) * 2 * a.C;
   if (few_tokens(a)) {
     const Few f = few_of(a);
     return 4 * (int64_t)walkers_of(a, f) * f.seqs * 2 * a.C;
   }
-  const Strips t = strips_of(a.rows);
-  return 4 * (up64(t.slots * 2 * a.C) + up64((int64_t)a.rows.S * 2 * a.C) +
-              (int64_t)a.rows.S * a.G * 2);
+  const Cut t = cut_of(a);
+  return 8 * (up64(t.slots * t.pieces) + up64((int64_t)a.rows.S * a.G) + (int64_t)t.strips * a.C);
 }
 
 hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, const void* dy, void* dx,
                                       float* dw, float* db, float* ws, hipStream_t s) {
   auto run = [&](auto io) {
     using IO = decltype(io);
+    if (single_tokens(a)) {
+      const int w = token_walkers(a);
+      const int64_t n = (int64_t)w * (a.C / V);
+      hipLaunchKernelGGL((k_gn_tokens_bwd<IO, 4>), dim3((unsigned)((n + kThreads - 1) / kThreads)),
+                         dim3(kThreads), 0, s, a, w, (const float2*)stats, (const IO*)dy, (IO*)dx, ws);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess || !(dw || db)) return e;
+      return launch_column_sums(ws, w, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
+    }
     if (few_tokens(a)) {
       const Few f = few_of(a);
       const int w = walkers_of(a, f);
@@ -585,23 +860,22 @@ hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, co
       if (e != hipSuccess || !(dw || db)) return e;
       return launch_column_sums(ws, w * f.seqs, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
     }
-    const Strips t = strips_of(a.rows);
-    const int tiles = tiles_of(a), cols = (2 * a.C + 63) / 64;
-    float* total = ws + up64(t.slots * 2 * a.C);
-    float* mid = total + up64((int64_t)a.rows.S * 2 * a.C);
-    const dim3 grid((unsigned)((int64_t)t.n * tiles));
-    hipLaunchKernelGGL((k_gn_bwd_parts<IO>), grid, dim3(kThreads), 0, s, a, t.per, tiles, stats,
-                       (const IO*)dy, ws);
-    hipLaunchKernelGGL(k_gn_bwd_total, dim3((unsigned)((int64_t)a.rows.S * cols)), dim3(kThreads), 0, s,
-                       a, t.per, cols, ws, total);
-    hipLaunchKernelGGL(k_gn_bwd_means,
-                       dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
-                       dim3(kThreads), 0, s, a, total, mid);
-    hipLaunchKernelGGL((k_gn_bwd_apply<IO>), grid, dim3(kThreads), 0, s, a, t.per, tiles, stats, mid,
-                       (const IO*)dy, (IO*)dx);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !(dw || db)) return e;
-    return launch_column_sums(total, a.rows.S, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
+    const Cut t = cut_of(a);
+    float2 *part = (float2*)ws, *ready = nullptr, *mid = part + up64(t.slots * t.pieces);
+    float* chan = dw || db ? (float*)(mid + up64((int64_t)a.rows.S * a.G)) : nullptr;
+    const unsigned blocks = (unsigned)((int64_t)t.strips * t.tiles);
+    const unsigned more = chan ? (2 * a.C + 63) / 64 : 0;
+    hipLaunchKernelGGL((k_gn_bwd_parts<IO>), dim3(blocks), dim3(kThreads), 0, s, a, t,
+                       (const float2*)stats, (const IO*)dy, part, chan);
+    if (!adds_itself(a, t, false)) {
+      ready = mid;
+      hipLaunchKernelGGL((k_gn_totals<true>),
+                         dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
+                         dim3(kThreads), 0, s, a, t, part, ready);
+    }
+    hipLaunchKernelGGL((k_gn_bwd_apply<IO>), dim3(blocks + more), dim3(kThreads), 0, s, a, t,
+                       (const float2*)stats, part, ready, chan, (const IO*)dy, (IO*)dx, dw, db);
+    return hipGetLastError();
   };
   return a.io == kIoBf16 ? run(u16{}) : run(float{});
 }

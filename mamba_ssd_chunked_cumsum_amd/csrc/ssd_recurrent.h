@@ -54,7 +54,8 @@ struct GroupArgs {
 };
 bool group_norm_fits(const GroupArgs& a);  // whether its launches do
 int64_t group_norm_bytes(const GroupArgs& a);
-hipError_t launch_group_norm(const GroupArgs& a, void* y, float* stats, float* ws, hipStream_t s);
+hipError_t launch_group_norm(const GroupArgs& a, void* y, float* stats, float* ws,
+                             hipStream_t s);
 int64_t group_norm_backward_bytes(const GroupArgs& a);
 hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, const void* dy, void* dx,
                                       float* dw, float* db, float* ws, hipStream_t s);

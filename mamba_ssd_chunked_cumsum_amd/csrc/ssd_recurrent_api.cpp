@@ -41,6 +41,14 @@ ssd_status recurrence_args(const ssd_tokens* t, const ssd_recurrent* in, RecArgs
 
 int64_t state_bytes(const ssd_tokens* t) { return t->nseq * t->channels * 4; }
 
+// The workspace as one more output.
+ssd_status take_workspace(Buffers* b, void* workspace, int64_t have, int64_t need) {
+  const ssd_status st = with_workspace(workspace, have, need);
+  if (st != SSD_OK || !need) return st;
+  b->output(workspace, need);
+  return b->fine() ? SSD_OK : SSD_ERR_INVALID_ARGUMENT;
+}
+
 // ---- group norm ------------------------------------------------------------------------------------
 
 ssd_status group_args(const ssd_tokens* t, const void* x, int64_t x_stride, const float* weight,
@@ -87,10 +95,9 @@ ssd_status ssd_recurrence(const ssd_tokens* t, const ssd_recurrent* in, void* y,
   b.input(in->initial_state, state_bytes(t));
   b.output(y, rows_of(t) * t->channels * bytes_of(t->io_dtype));
   b.output(final_state, state_bytes(t));
-  st = with_workspace(workspace, workspace_bytes, need);
-  if (st != SSD_OK) return st;
-  if (need) b.output(workspace, need);
   if (!b.fine()) return SSD_ERR_INVALID_ARGUMENT;
+  st = take_workspace(&b, workspace, workspace_bytes, need);
+  if (st != SSD_OK) return st;
   st = device_ready();
   if (st != SSD_OK) return st;
   return from_hip(launch_recurrence(a, y, final_state, static_cast<float*>(workspace),
@@ -147,10 +154,9 @@ ssd_status ssd_recurrence_backward(const ssd_tokens* t, const ssd_recurrent* in,
   b.output(dinput_gate, act);
   b.output(ddecay, t->channels * 4);
   b.output(dinitial_state, state_bytes(t));
-  st = with_workspace(workspace, workspace_bytes, need);
-  if (st != SSD_OK) return st;
-  if (need) b.output(workspace, need);
   if (!b.fine()) return SSD_ERR_INVALID_ARGUMENT;
+  st = take_workspace(&b, workspace, workspace_bytes, need);
+  if (st != SSD_OK) return st;
   st = device_ready();
   if (st != SSD_OK) return st;
   const RecGrads g{dx, dgate, dinput_gate, ddecay, dinitial_state};
@@ -213,13 +219,11 @@ ssd_status ssd_group_norm(const ssd_tokens* t, const void* x, int64_t x_stride, 
   ssd_status st = group_args(t, x, x_stride, weight, bias, ngroups, eps, silu, &a, &b);
   if (st != SSD_OK) return st;
   if (!x || !y) return SSD_ERR_INVALID_ARGUMENT;
-  const int64_t need = group_norm_bytes(a);
   b.output(y, rows_of(t) * t->channels * bytes_of(t->io_dtype));
   b.output(stats, t->nseq * ngroups * 8);
-  st = with_workspace(workspace, workspace_bytes, need);
-  if (st != SSD_OK) return st;
-  if (need) b.output(workspace, need);
   if (!b.fine()) return SSD_ERR_INVALID_ARGUMENT;
+  st = take_workspace(&b, workspace, workspace_bytes, group_norm_bytes(a));
+  if (st != SSD_OK) return st;
   st = device_ready();
   if (st != SSD_OK) return st;
   return from_hip(launch_group_norm(a, y, stats, static_cast<float*>(workspace),
@@ -249,16 +253,14 @@ ssd_status ssd_group_norm_backward(const ssd_tokens* t, const void* x, int64_t x
       (bias != nullptr) != (dbias != nullptr))
     return SSD_ERR_INVALID_ARGUMENT;
   const int64_t act = rows_of(t) * t->channels * bytes_of(t->io_dtype);
-  const int64_t need = group_norm_backward_bytes(a);
   b.input(stats, t->nseq * ngroups * 8);
   b.input(dy, act);
   b.output(dx, act);
   b.output(dweight, t->channels * 4);
   b.output(dbias, t->channels * 4);
-  st = with_workspace(workspace, workspace_bytes, need);
-  if (st != SSD_OK) return st;
-  if (need) b.output(workspace, need);
   if (!b.fine()) return SSD_ERR_INVALID_ARGUMENT;
+  st = take_workspace(&b, workspace, workspace_bytes, group_norm_backward_bytes(a));
+  if (st != SSD_OK) return st;
   st = device_ready();
   if (st != SSD_OK) return st;
   return from_hip(launch_group_norm_backward(a, stats, dy, dx, dweight, dbias,

@@ -562,7 +562,9 @@ def test_refusals_write_nothing():
 
 
 def test_offsets_beyond_32_bits():
-    """Tensors of more than 2^31 elements: the last sequences are what they are alone, bit for bit."""
+    """Tensors of more than 2^31 elements: the last sequences are what they are alone, bit for bit; the
+    group norm's strips may be cut differently there, so its outputs, sums in another order rounded to
+    bf16, are held to one step of that type, twice the half step each may be off."""
     note("offsets beyond 32 bits")
     S, L, C = 2701, 100, 8192
     assert S * L * C > 2 ** 31
@@ -596,7 +598,11 @@ def test_offsets_beyond_32_bits():
     for i, call in enumerate(pairs):
         got = last(call(x, gate, dy))
         want = call(last(x), last(gate), last(dy))
-        assert torch.equal(got, want), i
+        if i in (2, 3):
+            step = torch.finfo(torch.bfloat16).eps * want.float().abs() + 2.0 ** -20
+            assert torch.all((got.float() - want.float()).abs() <= step), i
+        else:
+            assert torch.equal(got, want), i
         del got, want
     del x, gate, dy
     torch.cuda.empty_cache()

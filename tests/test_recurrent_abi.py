@@ -234,7 +234,7 @@ def groups_of_norm(n):
     (lambda n: rows_of_recurrence(n, 1024), 2 ** 27 - 2 ** 20, 2 ** 27),
     (rows_of_rotation, 2 ** 31 - 4097, 2 ** 31 - 4096),
     (lambda n: rows_of_rotation(n, 16), 2 ** 30 - 65, 2 ** 30),
-    (groups_of_norm, 2 ** 18 - 1, 2 ** 18)])
+    (groups_of_norm, 2 ** 20 - 1, 2 ** 20)])
 def test_stated_limits(call, taken, refused):
     assert call(taken) == NO_DEVICE
     assert call(refused) == UNSUPPORTED
