@@ -121,6 +121,12 @@ def _rows(t, name, shape, dtype, dev, lead=2):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     size, stride = t.shape, t.stride()
+    # the common slice of wider rows, checked at once: rows of a batch, their values side by side
+    if len(size) == lead + 1 and stride[lead] == 1 and size[lead - 1] > 1:
+        row = stride[lead - 1]
+        if row >= size[lead] and (lead == 1 or size[0] == 1 or stride[0] == row * size[1]) \
+                and lead <= 2 and t.dtype == dtype and t.is_cuda and t.device == dev:
+            return t.data_ptr(), row
     width = 1
     for i in range(len(size) - 1, lead - 1, -1):
         if size[i] != 1 and stride[i] != width:

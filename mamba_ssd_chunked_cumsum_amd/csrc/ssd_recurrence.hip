@@ -5,15 +5,15 @@
 //                            m = sqrt(1 - a^2)
 //   without:                 a = sigmoid(gate), m = 1 - a
 //
-// A few dozen operations for each element read once: bound by memory if the rows are read once and
-// the exponentials evaluated once. The tokens of a sequence are sequential, but the recurrence is
-// linear, so a run of rows is summed up by two numbers a channel, the product P of its a and its
-// end state H from a zero state: h_end = P h_in + H. The adjoint runs the same way backwards
+// About 30 vector operations for each element read once: bound by memory if the rows are read once and
+// the exponentials evaluated once, and not by much. The tokens of a sequence are sequential, but the
+// recurrence is linear, so a run of rows is summed up by two numbers a channel, the product P of its a
+// and its end state H from a zero state: h_end = P h_in + H. The adjoint runs the same way backwards
 // (l_t = dy_t + a_{t+1} l_{t+1}; what leaves the run to the left is P c_in + G with the same P).
 //
 // A lane holds the channels of four bytes (two bf16, one fp32), a wave 64 lanes and T rows, all of
 // whose loads are issued at once; the waves of a block take consecutive rows (a chunk) and combine
-// their (P, H) through LDS. Chunks are chained by a kernel between two passes over the rows.
+// their (P, H) through LDS.
 #include <cmath>
 
 #include "ssd_recurrent.h"
@@ -23,25 +23,31 @@ namespace ssd {
 
 namespace {
 
-constexpr int T = 16;      // rows of a wave, at most 31
-constexpr int kWaves = 8;  // most waves of a block
 constexpr int kGroup = 8;  // chunks between those that hand on their end state
 constexpr float kLn2 = 0.6931471805599453f;
-template <typename IO>
-constexpr int kV = 4 / (int)sizeof(IO);  // channels of a lane
+
+// Rows of a wave (at most 31), waves of a block, bytes of a lane: of the forward, and of the backward's
+// two passes, whose chunks have the same rows.
+struct Fwd { static constexpr int T = 16, W = 8, B = 4; };
+struct Sum { static constexpr int T = 8, W = 4, B = 4; };
+struct Bwd { static constexpr int T = 8, W = 4, B = 4; };
+static_assert(Sum::T * Sum::W == Bwd::T * Bwd::W, "");
+template <typename IO, typename X>
+constexpr int kV = X::B / (int)sizeof(IO);  // channels of a lane
 
 // How the rows are cut. Dense: `chunks` of each sequence, of `waves` waves each; where a sequence is
 // one chunk, a block takes `seqs` of them. Packed: chunks of all rows, wherever sequences begin.
 struct Plan {
   int waves, seqs, chunks, units;  // units: blocks of one channel tile
 };
+template <typename X>
 Plan plan(const Rows& q) {
   Plan p;
   const int64_t rows = q.starts ? q.R : q.L;
-  const int64_t need = (rows + T - 1) / T;
-  p.waves = (int)(need < kWaves ? need : kWaves);
-  p.chunks = (int)((need + kWaves - 1) / kWaves);
-  p.seqs = q.starts || p.chunks > 1 ? 1 : kWaves / p.waves;
+  const int64_t need = (rows + X::T - 1) / X::T;
+  p.waves = (int)(need < X::W ? need : X::W);
+  p.chunks = (int)((need + X::W - 1) / X::W);
+  p.seqs = q.starts || p.chunks > 1 ? 1 : X::W / p.waves;
   if (!q.starts && p.seqs > q.S) p.seqs = q.S;
   p.units = q.starts ? p.chunks
                      : (int)(p.chunks > 1 ? (int64_t)p.chunks * q.S : ((int64_t)q.S + p.seqs - 1) / p.seqs);
@@ -54,16 +60,15 @@ int threads_of(const Plan& p) { return 64 * p.waves * p.seqs; }
 __device__ __forceinline__ float one_side(float v) {
   return __builtin_amdgcn_rcpf(1.f + exp2_fast(-v * kLog2e));
 }
-// sigmoid(v) and sigmoid(-v), both to a few roundings of themselves (the first at least 2^-126). The
-// minimum keeps NaN.
+// exp(-v), at most 2^126 (the minimum keeps NaN), and from it sigmoid(v), at least 2^-126, and
+// sigmoid(-v), both to a few roundings of themselves.
+__device__ __forceinline__ float exp_minus(float v) {
+  return __builtin_elementwise_minimum(exp2_fast(-v * kLog2e), 0x1p126f);
+}
 struct Sig {
   float p, n;
+  __device__ __forceinline__ explicit Sig(float e) : p(__builtin_amdgcn_rcpf(1.f + e)), n(e * p) {}
 };
-__device__ __forceinline__ Sig both_sides(float v) {
-  const float e = __builtin_elementwise_minimum(exp2_fast(-v * kLog2e), 0x1p126f);
-  const float p = __builtin_amdgcn_rcpf(1.f + e);
-  return Sig{p, e * p};
-}
 
 // 1 - a^2 from a = 2^-t, t >= 0: where the difference would cancel (below t = 0.36, that is a^2 = 0.61)
 // the polynomial t c(t) of degree 5 that is nearest, to 9e-8 relative.
@@ -79,36 +84,16 @@ __device__ __forceinline__ float one_minus_square(float t, float a) {
 struct Step {
   float a, m;
 };
-template <bool DECAY>
-__device__ __forceinline__ Step step_of(float g, float rate) {
-  if constexpr (!DECAY) {
-    const Sig r = both_sides(g);
-    return Step{r.p, r.n};
-  }
-  const float t = rate * one_side(g), a = exp2_fast(-t);
+__device__ __forceinline__ Step decayed(float r, float rate) {
+  const float t = rate * r, a = exp2_fast(-t);
   return Step{a, __builtin_amdgcn_sqrtf(one_minus_square(t, a))};
 }
-
-// The same with what the gradients need: r and 1 - r, 1 / m (at most 2^63, so that u / m is 0 where u
-// is).
 template <bool DECAY>
-struct Gate {
-  float a, m, inv;
-  Sig r;
-  __device__ __forceinline__ Gate(float g, float rate) {
-    r = both_sides(g);
-    if constexpr (DECAY) {
-      const float t = rate * r.p;
-      a = exp2_fast(-t);
-      const float sq = one_minus_square(t, a);
-      inv = __builtin_amdgcn_rsqf(fmaxf(sq, 0x1p-126f));
-      m = sq * inv;
-    } else {
-      a = r.p;
-      m = r.n;
-    }
-  }
-};
+__device__ __forceinline__ Step step_of(float g, float rate) {
+  if constexpr (DECAY) return decayed(one_side(g), rate);
+  const Sig r(exp_minus(g));
+  return Step{r.p, r.n};
+}
 
 // sharpness softplus(decay) log2(e), to a few roundings: exp(-|d|) with the product's rounding made
 // good, log(1 + e) by its series where e is small, else from the hardware's log2 of the rounded sum and
@@ -129,42 +114,71 @@ __device__ __forceinline__ float enter(float P, float H, float h) { return cut(P
 __device__ __forceinline__ float join(float P, float Q) { return cut(P) || cut(Q) ? -0.f : P * Q; }
 
 // ---- rows of a wave --------------------------------------------------------------------------------
-// Value j of the raw word of a lane's channels.
-template <typename IO>
-__device__ __forceinline__ float word(uint32_t u, int j) {
-  if constexpr (sizeof(IO) == 4) return __uint_as_float(u);
-  else return __uint_as_float(j ? u & 0xffff0000u : u << 16);
-}
-template <typename IO>
-__device__ __forceinline__ void store_word(IO* row, unsigned off, const float (&v)[kV<IO>]) {
-  uint32_t u;
-  if constexpr (sizeof(IO) == 4) u = __float_as_uint(v[0]);
-  else u = pack_bf16(v[0], v[1]);
-  *(uint32_t*)((char*)row + off) = u;
+// The channels of a lane, B bytes of a row, as loaded.
+template <typename IO, int B>
+struct Word {
+  uint32_t u[B / 4];
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(u[j]);
+    else return __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+  }
+};
+
+// stream: past the caches, for outputs far larger than they are.
+template <typename IO, int B, int V>
+__device__ __forceinline__ void store_word(IO* row, unsigned off, const float (&v)[V], int stream) {
+  typedef uint32_t words __attribute__((ext_vector_type(B / 4)));
+  words u;
+#pragma unroll
+  for (int i = 0; i < B / 4; ++i) {
+    if constexpr (sizeof(IO) == 4) u[i] = __float_as_uint(v[i]);
+    else u[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  }
+  words* p = (words*)((char*)row + off);
+  if (stream) {  // (the empty statements keep the two stores from becoming a plain one)
+    asm volatile("" ::: "memory");
+    __builtin_nontemporal_store(u, p);
+    asm volatile("" ::: "memory");
+  } else {
+    *p = u;
+  }
 }
 
-// T rows of n of several tensors, row by row, so that the first rows can be worked on while the others
-// arrive; the rows past n are not read (zeros).
-template <typename IO>
+// Rows of several tensors, one after another, so that the first rows can be worked on while the others
+// arrive.
+template <typename IO, int B>
 struct Source {
   const char* p;
   int64_t step;
   __device__ __forceinline__ Source(const void* t, int64_t stride, int r0)
       : p((const char*)((const IO*)t + r0 * stride)), step(stride * sizeof(IO)) {}
-  __device__ __forceinline__ uint32_t next(unsigned off) {
-    const uint32_t u = *(const uint32_t*)(p + off);
+  __device__ __forceinline__ void next(Word<IO, B>& w, unsigned off) {
+    typedef uint32_t words __attribute__((ext_vector_type(B / 4)));
+    const words v = *(const words*)(p + off);
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) w.u[i] = v[i];
     p += step;
-    return u;
   }
 };
-template <typename F>
-__device__ __forceinline__ void for_rows(int n, F f) {
-  if (n == T) {
+template <int T, typename F>
+__device__ __forceinline__ void for_rows(bool all, int n, F f) {
+  if (all) {
 #pragma unroll
     for (int i = 0; i < T; ++i) f(i);
   } else {
 #pragma unroll
     for (int i = 0; i < T; ++i)
+      if (i < n) f(i);
+  }
+}
+template <int T, typename F>
+__device__ __forceinline__ void for_rows_back(bool all, int n, F f) {
+  if (all) {
+#pragma unroll
+    for (int i = T - 1; i >= 0; --i) f(i);
+  } else {
+#pragma unroll
+    for (int i = T - 1; i >= 0; --i)
       if (i < n) f(i);
   }
 }
@@ -175,7 +189,7 @@ struct Place {
   int s, part;               // dense: its sequence; its place among the sequence's waves here
   bool last;                 // dense: the sequence ends in these rows
   int lo, hi;                // waves whose runs this one's joins
-  __device__ __forceinline__ Place(const Rows& q, const Plan& p, int unit_) {
+  __device__ __forceinline__ Place(const Rows& q, const Plan& p, int T, int unit_) {
     unit = unit_;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     part = wave;
@@ -209,6 +223,19 @@ struct Place {
     n = at < q.L ? min((int)(q.L - at), T) : 0;
     first = n ? s * q.L + (int)at : 0;
     last = n && at + n == q.L;
+  }
+};
+
+// Channels of a lane.
+template <int V>
+struct Lane {
+  int c, lane;
+  bool live;
+  __device__ __forceinline__ Lane(const RecArgs& q, int tile) {
+    lane = threadIdx.x & 63;
+    const int c0 = (tile * 64 + lane) * V;
+    live = c0 < q.C;
+    c = live ? c0 : q.C - V;  // idle lanes compute the last channels again
   }
 };
 
@@ -263,11 +290,6 @@ int empty_blocks(const RecArgs& a, const Plan& p, const float* to) {
   return (int)(n < 4096 ? n : 4096);
 }
 
-// Sums of the runs, [units, C] each.
-struct Sums {
-  float *P, *H, *G;
-};
-
 // ---- forward ---------------------------------------------------------------------------------------
 // Chunks of one call hand on what follows them needs through `slots` [units, C], one 64-bit word a
 // channel: (P, H) of the chunk, or of every kGroup-th chunk its end state, as a run with P = -0. A word
@@ -294,11 +316,11 @@ __global__ __launch_bounds__(256) void k_rec_clear(Chain chain, int64_t n) {
 // CHAIN: sequences of several chunks. A block belongs to a tile and sequence and takes the next chunk of
 // them by a ticket. It waits only for chunks before its own, whose blocks have lower tickets: those are
 // running or done, and the first of them waits for none, so every wait ends.
-template <typename IO, bool DECAY, bool GATED, bool PACKED, bool CHAIN>
-__global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int tiles, Chain chain,
-                                                     IO* __restrict__ y, float* __restrict__ fin) {
-  constexpr int V = kV<IO>;
-  __shared__ float2 runs[kWaves][V][64];
+template <typename X, typename IO, bool DECAY, bool GATED, bool PACKED, bool CHAIN>
+__global__ __launch_bounds__(64 * X::W) void k_rec(RecArgs q, Plan pl, int tiles, Chain chain,
+                                                   IO* __restrict__ y, float* __restrict__ fin) {
+  constexpr int V = kV<IO, X>, T = X::T, B = X::B;
+  __shared__ float2 runs[X::W][V][64];
   __shared__ float entry[V][64];
   __shared__ uint32_t place;
   const int64_t main_blocks = (int64_t)tiles * pl.units;
@@ -306,16 +328,15 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
     pass_empty(q.rows, q.C, (int)(blockIdx.x - main_blocks), (int)(gridDim.x - main_blocks), q.h0, fin);
     return;
   }
-  const int tile = (int)(blockIdx.x % tiles), lane = threadIdx.x & 63;
+  const int tile = (int)(blockIdx.x % tiles);
   int unit = (int)(blockIdx.x / tiles);
   const int s = PACKED ? 0 : unit % q.rows.S;
   uint32_t ticket = 0;
   if (CHAIN && threadIdx.x == 0)
     ticket = __hip_atomic_fetch_add(chain.tickets + ((int64_t)s * tiles + tile) * kApart, 1u,
                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const int c0 = (tile * 64 + lane) * V;
-  const bool live = c0 < q.C;
-  const int c = live ? c0 : q.C - V;  // idle lanes compute the last channels again
+  const Lane<V> me(q, tile);
+  const int c = me.c, lane = me.lane;
   const unsigned off = (unsigned)c * sizeof(IO);
   float k[V];
 #pragma unroll
@@ -325,27 +346,28 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
     __syncthreads();
     unit = s * pl.chunks + __builtin_amdgcn_readfirstlane(place);
   }
-  const Place at(q.rows, pl, unit);
-  uint32_t rx[T], rg[T], ri[T];
-  Source<IO> sg(q.g, q.gs, at.first), si(q.gi, q.is, at.first), sx(q.x, q.xs, at.first);
-  for_rows(at.n, [&](int i) {
-    rg[i] = sg.next(off);
-    if (GATED) ri[i] = si.next(off);
-    rx[i] = sx.next(off);
+  const Place at(q.rows, pl, T, unit);
+  Word<IO, B> rx[T], rg[T], ri[T];
+  Source<IO, B> sg(q.g, q.gs, at.first), si(q.gi, q.is, at.first), sx(q.x, q.xs, at.first);
+  for_rows<T>(at.n == T, at.n, [&](int i) {
+    sg.next(rg[i], off);
+    if (GATED) si.next(ri[i], off);
+    sx.next(rx[i], off);
   });
   Marks mk;
   if (PACKED && at.n > 0) mk.find(q.rows, at.first, at.n);
+  const bool plain = at.n == T && (!PACKED || mk.plain);
 
   float P[T][V], H[T][V];  // of the rows up to each
   float p[V], h[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) p[j] = 1.f, h[j] = 0.f;
-  auto row = [&](int i) {
+  for_rows<T>(plain, at.n, [&](int i) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const Step t = step_of<DECAY>(word<IO>(rg[i], j), k[j]);
-      float v = word<IO>(rx[i], j);
-      if (GATED) v *= one_side(word<IO>(ri[i], j));
+      const Step t = step_of<DECAY>(rg[i][j], k[j]);
+      float v = rx[i][j];
+      if (GATED) v *= one_side(ri[i][j]);
       if (PACKED && !mk.plain) {
         if (mk.starts >> i & 1) {
           const float h0 = q.h0 ? q.h0[(int64_t)seq_at(mk.seq, i) * q.C + c + j] : 0.f;
@@ -364,15 +386,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
       }
       P[i][j] = p[j], H[i][j] = h[j];
     }
-  };
-  if (at.n == T && (!PACKED || mk.plain)) {
-#pragma unroll
-    for (int i = 0; i < T; ++i) row(i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-      if (i < at.n) row(i);
-  }
+  });
 #pragma unroll
   for (int j = 0; j < V; ++j) runs[at.wave][j][lane] = make_float2(p[j], h[j]);
   __syncthreads();
@@ -389,7 +403,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
         }
       uint64_t* slot = chain.slots + (int64_t)at.unit * q.C + c;
       const bool hands_on = chunk % kGroup == kGroup - 1, needed = chunk + 1 < pl.chunks;
-      if (needed && !hands_on && live) {
+      if (needed && !hands_on && me.live) {
 #pragma unroll
         for (int j = 0; j < V; ++j) publish(slot + j, p[j], h[j]);
       }
@@ -420,7 +434,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
             e[j] = enter(__uint_as_float((uint32_t)(got[i][j] >> 32)),
                          __uint_as_float((uint32_t)got[i][j]), e[j]);
         }
-      if (needed && hands_on && live) {
+      if (needed && hands_on && me.live) {
 #pragma unroll
         for (int j = 0; j < V; ++j) publish(slot + j, -0.f, enter(p[j], h[j], e[j]));
       }
@@ -447,17 +461,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
     for (int i = 0; i < T; ++i)
       H[i][j] = PACKED ? enter(P[i][j], H[i][j], e[j]) : fmaf(P[i][j], e[j], H[i][j]);
   }
-  if (!live) return;
+  if (!me.live) return;
   IO* out = y + (int64_t)at.first * q.C;
-  if (at.n == T && (!PACKED || mk.plain)) {
-#pragma unroll
-    for (int i = 0; i < T; ++i) store_word<IO>(out + (int64_t)i * q.C, off, H[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-      if (i < at.n && (!PACKED || (mk.inside >> i & 1)))
-        store_word<IO>(out + (int64_t)i * q.C, off, H[i]);
-  }
+  for_rows<T>(plain, at.n, [&](int i) {
+    if (!PACKED || (mk.inside >> i & 1))
+      store_word<IO, B>(out + (int64_t)i * q.C, off, H[i], q.stream);
+  });
   if (!fin) return;
   if (PACKED) {
     if (mk.ends) {
@@ -478,12 +487,17 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec(RecArgs q, Plan pl, int til
   }
 }
 
+// Sums of the runs, [units, C] each.
+struct Sums {
+  float *P, *H, *G;
+};
+
 // Chain over the chunks, in place: sums.H from a chunk's end state to the state entering it
 // (blockIdx.y 0), sums.G from what leaves the chunk to the left to what enters it from the right
 // (blockIdx.y 1). Bound by the latency of its loads, which are issued kAhead chunks at a time.
 __global__ __launch_bounds__(256) void k_rec_chain(RecArgs q, Plan pl, Sums sums,
                                                    const float* __restrict__ dfinal) {
-  constexpr int kAhead = 16;
+  constexpr int kAhead = 32;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= (q.rows.starts ? 1 : (int64_t)q.rows.S) * q.C) return;
   const int64_t s = id / q.C;
@@ -515,39 +529,118 @@ __global__ __launch_bounds__(256) void k_rec_chain(RecArgs q, Plan pl, Sums sums
 //   dx = l m s, dinput_gate = l m v (1 - s), s = sigmoid(input_gate);
 //   dlog a = l (a h_{t-1} - a^2 / m v), dgate = -dlog a u (1 - r), ddecay = -sum dlog a r times
 //   sharpness sigmoid(decay); without a decay dgate = l (h_{t-1} - v) a (1 - a).
-// ENDS: the runs' sums in both directions. Otherwise the gradients; part [units, C]: each block's
-// sums for ddecay.
-template <typename IO, bool DECAY, bool GATED, bool PACKED, bool ENDS>
-__global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
+// Two passes and a chain between them: what enters a chunk from the left needs all before it, what enters
+// from the right all behind it. First pass: the chunks' sums in both directions.
+template <typename X, typename IO, bool DECAY, bool GATED, bool PACKED>
+__global__ __launch_bounds__(64 * X::W) void k_rec_sums(RecArgs q, Plan pl, int tiles, Sums sums,
+                                                        const IO* __restrict__ dy,
+                                                        const float* __restrict__ dfinal) {
+  constexpr int V = kV<IO, X>, T = X::T, B = X::B;
+  __shared__ float2 runs[X::W][V][64];
+  __shared__ float left[X::W][V][64];
+  const Lane<V> me(q, (int)(blockIdx.x % tiles));
+  const Place at(q.rows, pl, T, (int)(blockIdx.x / tiles));
+  const int c = me.c, lane = me.lane;
+  const unsigned off = (unsigned)c * sizeof(IO);
+  Word<IO, B> rx[T], rg[T], ri[T], rd[T];
+  Source<IO, B> sg(q.g, q.gs, at.first), si(q.gi, q.is, at.first), sx(q.x, q.xs, at.first),
+      sd(dy, q.C, at.first);
+  for_rows<T>(at.n == T, at.n, [&](int i) {
+    sg.next(rg[i], off);
+    if (GATED) si.next(ri[i], off);
+    sx.next(rx[i], off);
+    sd.next(rd[i], off);
+  });
+  Marks mk;
+  if (PACKED && at.n > 0) mk.find(q.rows, at.first, at.n);
+  float p[V], h[V], g[V], k[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    k[j] = DECAY ? decay_rate(q, c + j) : 0.f;
+    p[j] = 1.f, h[j] = 0.f, g[j] = 0.f;
+  }
+  for_rows<T>(at.n == T && (!PACKED || mk.plain), at.n, [&](int i) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const Step t = step_of<DECAY>(rg[i][j], k[j]);
+      float v = rx[i][j], d = rd[i][j];
+      if (GATED) v *= one_side(ri[i][j]);
+      if (PACKED && !mk.plain) {
+        const int64_t o = (int64_t)max(seq_at(mk.seq, i), 0) * q.C + c + j;
+        if (!(mk.inside >> i & 1)) {
+          p[j] = -0.f;
+          h[j] = 0.f;
+          continue;
+        }
+        if ((mk.ends >> i & 1) && dfinal) d += dfinal[o];
+        if (mk.starts >> i & 1) {
+          p[j] = -0.f;
+          h[j] = fmaf(t.a, q.h0 ? q.h0[o] : 0.f, t.m * v);
+          continue;
+        }
+      }
+      p[j] = PACKED ? join(p[j], t.a) : p[j] * t.a;
+      h[j] = fmaf(t.a, h[j], t.m * v);
+      // (behind a start nothing reaches the left end)
+      if (!PACKED || !cut(p[j])) g[j] = fmaf(p[j], d, g[j]);
+    }
+  });
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    runs[at.wave][j][lane] = make_float2(p[j], h[j]);
+    left[at.wave][j][lane] = g[j];
+  }
+  __syncthreads();
+  if (at.wave || !me.live) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    for (int w = 1; w < pl.waves; ++w) {
+      const float2 r = runs[w][j][lane];
+      if (!cut(p[j])) g[j] = fmaf(p[j], left[w][j][lane], g[j]);
+      h[j] = enter(r.x, r.y, h[j]);
+      p[j] = join(p[j], r.x);
+    }
+    const int64_t o = (int64_t)at.unit * q.C + c + j;
+    sums.P[o] = p[j];
+    sums.H[o] = h[j];
+    sums.G[o] = g[j];
+  }
+}
+
+// Second pass (or the only one): the gradients; part [units, C]: each block's sums for ddecay. Forward
+// through the rows, then back; what the way back needs of the way forward stays in registers, the
+// gates by their exponentials, from which both sides of a sigmoid come exactly.
+template <typename X, typename IO, bool DECAY, bool GATED, bool PACKED>
+__global__ __launch_bounds__(64 * X::W, 4) void k_rec_bwd(
     RecArgs q, Plan pl, int tiles, Sums sums, int chained, const IO* __restrict__ dy,
     const float* __restrict__ dfinal, IO* __restrict__ dx, IO* __restrict__ dg,
     IO* __restrict__ dgi, float* __restrict__ dh0, float* __restrict__ part) {
-  constexpr int V = kV<IO>;
-  __shared__ float2 runs[kWaves][V][64];
-  __shared__ float left[kWaves][V][64];  // G of each wave; then the waves' sums for ddecay
+  constexpr int V = kV<IO, X>, T = X::T, B = X::B;
+  __shared__ float2 runs[X::W][V][64];
+  __shared__ float left[X::W][V][64];  // G of each wave; then the waves' sums for ddecay
   const int64_t main_blocks = (int64_t)tiles * pl.units;
   if (PACKED && blockIdx.x >= main_blocks) {
     pass_empty(q.rows, q.C, (int)(blockIdx.x - main_blocks), (int)(gridDim.x - main_blocks), dfinal,
                dh0);
     return;
   }
-  const int tile = (int)(blockIdx.x % tiles), lane = threadIdx.x & 63;
-  const Place at(q.rows, pl, (int)(blockIdx.x / tiles));
-  const int c0 = (tile * 64 + lane) * V;
-  const bool live = c0 < q.C;
-  const int c = live ? c0 : q.C - V;
+  const Lane<V> me(q, (int)(blockIdx.x % tiles));
+  // from the end, where the first pass left what it read in the last-level cache
+  const Place at(q.rows, pl, T, pl.units - 1 - (int)(blockIdx.x / tiles));
+  const int c = me.c, lane = me.lane;
   const unsigned off = (unsigned)c * sizeof(IO);
-  uint32_t rx[T], rg[T], ri[T], rd[T];
-  Source<IO> sg(q.g, q.gs, at.first), si(q.gi, q.is, at.first), sx(q.x, q.xs, at.first),
+  Word<IO, B> rx[T], rg[T], ri[T], rd[T];
+  Source<IO, B> sg(q.g, q.gs, at.first), si(q.gi, q.is, at.first), sx(q.x, q.xs, at.first),
       sd(dy, q.C, at.first);
-  for_rows(at.n, [&](int i) {
-    rg[i] = sg.next(off);
-    if (GATED) ri[i] = si.next(off);
-    rx[i] = sx.next(off);
-    rd[i] = sd.next(off);
+  for_rows<T>(at.n == T, at.n, [&](int i) {
+    sg.next(rg[i], off);
+    if (GATED) si.next(ri[i], off);
+    sx.next(rx[i], off);
+    sd.next(rd[i], off);
   });
   Marks mk;
   if (PACKED && at.n > 0) mk.find(q.rows, at.first, at.n);
+  const bool plain = at.n == T && (!PACKED || mk.plain);
   float k[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) k[j] = DECAY ? decay_rate(q, c + j) : 0.f;
@@ -558,18 +651,26 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
     return dfinal ? dfinal[(int64_t)seq_at(mk.seq, i) * q.C + c + j] : 0.f;
   };
 
-  float P[T][V], H[T][V];  // of the rows before each
+  float eg[T][V], es[T][V], ka[T][V], km[T][V];  // exp(-gate), exp(-input_gate), a, m
+  float b[T][V];                                 // m v, then the state before each row
   float p[V], h[V], g[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) p[j] = 1.f, h[j] = 0.f, g[j] = 0.f;
-  auto row = [&](int i) {
+  for_rows<T>(plain, at.n, [&](int i) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      if (!ENDS) P[i][j] = p[j], H[i][j] = h[j];
-      const Step t = step_of<DECAY>(word<IO>(rg[i], j), k[j]);
-      float v = word<IO>(rx[i], j);
-      if (GATED) v *= one_side(word<IO>(ri[i], j));
-      float d = word<IO>(rd[i], j);
+      eg[i][j] = exp_minus(rg[i][j]);
+      const Sig r(eg[i][j]);
+      Step t{r.p, r.n};
+      if constexpr (DECAY) t = decayed(r.p, k[j]);
+      ka[i][j] = t.a;
+      km[i][j] = t.m;
+      float v = rx[i][j], d = rd[i][j];
+      if (GATED) {
+        es[i][j] = exp_minus(ri[i][j]);
+        v *= Sig(es[i][j]).p;
+      }
+      b[i][j] = t.m * v;
       if (PACKED && !mk.plain) {
         if (!(mk.inside >> i & 1)) {
           p[j] = -0.f;
@@ -579,122 +680,97 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
         if (mk.ends >> i & 1) d += end_grad(i, j);
         if (mk.starts >> i & 1) {
           p[j] = -0.f;
-          h[j] = fmaf(t.a, start_state(i, j), t.m * v);
+          h[j] = fmaf(t.a, start_state(i, j), b[i][j]);
           continue;
         }
       }
       p[j] = PACKED ? join(p[j], t.a) : p[j] * t.a;
-      h[j] = fmaf(t.a, h[j], t.m * v);
-      // (behind a start nothing reaches the left end)
+      h[j] = fmaf(t.a, h[j], b[i][j]);
       if (!PACKED || !cut(p[j])) g[j] = fmaf(p[j], d, g[j]);
     }
-  };
-  if (at.n == T && (!PACKED || mk.plain)) {
-#pragma unroll
-    for (int i = 0; i < T; ++i) row(i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-      if (i < at.n) row(i);
-  }
+  });
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     runs[at.wave][j][lane] = make_float2(p[j], h[j]);
     left[at.wave][j][lane] = g[j];
   }
   __syncthreads();
-  if (ENDS) {
-    if (at.wave == 0 && live) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        for (int w = 1; w < pl.waves; ++w) {
-          const float2 r = runs[w][j][lane];
-          if (!cut(p[j])) g[j] = fmaf(p[j], left[w][j][lane], g[j]);
-          h[j] = enter(r.x, r.y, h[j]);
-          p[j] = join(p[j], r.x);
-        }
-        const int64_t o = (int64_t)at.unit * q.C + c + j;
-        sums.P[o] = p[j];
-        sums.H[o] = h[j];
-        sums.G[o] = g[j];
-      }
-    }
-    return;
-  }
   float sum[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) sum[j] = 0.f;
   if (at.n > 0) {
-    float cl[V];  // c of the row to the right
+    float cl[V], e[V];  // c of the row to the right; the state that enters
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int64_t o = (int64_t)at.unit * q.C + c + j, so = (int64_t)at.s * q.C + c + j;
-      float e = 0.f, r = 0.f;
-      if (chained) e = sums.H[o], r = sums.G[o];
-      else if (!PACKED) e = q.h0 ? q.h0[so] : 0.f, r = dfinal ? dfinal[so] : 0.f;
+      e[j] = cl[j] = 0.f;
+      if (chained) e[j] = sums.H[o], cl[j] = sums.G[o];
+      else if (!PACKED) e[j] = q.h0 ? q.h0[so] : 0.f, cl[j] = dfinal ? dfinal[so] : 0.f;
       for (int w = at.lo; w < at.wave; ++w) {
         const float2 t = runs[w][j][lane];
-        e = enter(t.x, t.y, e);
+        e[j] = enter(t.x, t.y, e[j]);
       }
-      for (int w = at.hi - 1; w > at.wave; --w) r = enter(runs[w][j][lane].x, left[w][j][lane], r);
-#pragma unroll
-      for (int i = 0; i < T; ++i)
-        H[i][j] = PACKED ? enter(P[i][j], H[i][j], e) : fmaf(P[i][j], e, H[i][j]);
-      cl[j] = r;
+      for (int w = at.hi - 1; w > at.wave; --w)
+        cl[j] = enter(runs[w][j][lane].x, left[w][j][lane], cl[j]);
     }
-    auto row_back = [&](int i) {
-      float ox[V], og[V], oi[V];
-      bool in = true;
-      if (PACKED && !mk.plain) in = mk.inside >> i & 1;
+    for_rows<T>(plain, at.n, [&](int i) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const Gate<DECAY> t(word<IO>(rg[i], j), k[j]);
-        const float x = word<IO>(rx[i], j);
-        Sig s{1.f, 0.f};
-        if (GATED) s = both_sides(word<IO>(ri[i], j));
-        const float v = GATED ? x * s.p : x;
-        float before = H[i][j];
         if (PACKED && !mk.plain) {
-          if (!in) {
+          if (mk.starts >> i & 1) e[j] = start_state(i, j);
+          if (!(mk.inside >> i & 1)) e[j] = 0.f;
+        }
+        const float before = e[j];
+        e[j] = fmaf(ka[i][j], e[j], b[i][j]);
+        b[i][j] = before;
+      }
+    });
+    for_rows_back<T>(plain, at.n, [&](int i) {
+      float ox[V], og[V], oi[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (PACKED && !mk.plain) {
+          if (!(mk.inside >> i & 1)) {
             ox[j] = og[j] = oi[j] = 0.f;
             cl[j] = 0.f;
             continue;
           }
           if (mk.ends >> i & 1) cl[j] = end_grad(i, j);
-          if (mk.starts >> i & 1) before = start_state(i, j);
         }
-        const float l = word<IO>(rd[i], j) + cl[j], lm = l * t.m;
-        ox[j] = GATED ? lm * s.p : lm;
-        oi[j] = lm * v * s.n;
+        const Sig r(eg[i][j]);
+        const float a = ka[i][j], m = km[i][j], before = b[i][j];
+        const float l = rd[i][j] + cl[j], lm = l * m;
+        float v = rx[i][j];
+        ox[j] = lm;
+        if (GATED) {
+          const Sig s(es[i][j]);
+          v *= s.p;
+          ox[j] = lm * s.p;
+          oi[j] = lm * (v * s.n);
+        }
         if constexpr (DECAY) {
-          const float d = l * fmaf(t.a * t.a * v, t.inv, -t.a * before);  // -dL/dlog a
-          og[j] = d * (t.r.n * (k[j] * t.r.p)) * kLn2;
-          sum[j] = fmaf(d, t.r.p, sum[j]);
+          // 1 / m at most 2^63, so that u / m is 0 where u is
+          const float inv = __builtin_amdgcn_rcpf(fmaxf(m, 0x1p-63f));
+          const float d = l * fmaf(a * a, v * inv, -a * before);  // -dL/dlog a
+          og[j] = d * (r.n * (k[j] * kLn2 * r.p));
+          sum[j] = fmaf(d, r.p, sum[j]);
         } else {
-          og[j] = l * (before - v) * (t.a * t.m);
+          og[j] = l * (before - v) * (a * m);
         }
-        cl[j] = t.a * l;
+        cl[j] = a * l;
         if (PACKED && !mk.plain && (mk.starts >> i & 1)) {
-          if (dh0 && live) dh0[(int64_t)seq_at(mk.seq, i) * q.C + c + j] = cl[j];
+          if (dh0 && me.live) dh0[(int64_t)seq_at(mk.seq, i) * q.C + c + j] = cl[j];
           cl[j] = 0.f;
         }
       }
-      if (live) {
+      if (me.live) {
         const int64_t o = (int64_t)(at.first + i) * q.C;
-        store_word<IO>(dx + o, off, ox);
-        store_word<IO>(dg + o, off, og);
-        if (GATED) store_word<IO>(dgi + o, off, oi);
+        store_word<IO, B>(dx + o, off, ox, q.stream);
+        store_word<IO, B>(dg + o, off, og, q.stream);
+        if (GATED) store_word<IO, B>(dgi + o, off, oi, q.stream);
       }
-    };
-    if (at.n == T && (!PACKED || mk.plain)) {
-#pragma unroll
-      for (int i = T - 1; i >= 0; --i) row_back(i);
-    } else {
-#pragma unroll
-      for (int i = T - 1; i >= 0; --i)
-        if (i < at.n) row_back(i);
-    }
-    if (!PACKED && dh0 && live && at.part == 0 && (pl.chunks == 1 || at.unit % pl.chunks == 0)) {
+    });
+    if (!PACKED && dh0 && me.live && at.part == 0 && (pl.chunks == 1 || at.unit % pl.chunks == 0)) {
 #pragma unroll
       for (int j = 0; j < V; ++j) dh0[(int64_t)at.s * q.C + c + j] = cl[j];
     }
@@ -704,7 +780,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_rec_bwd(
 #pragma unroll
     for (int j = 0; j < V; ++j) left[at.wave][j][lane] = sum[j];
     __syncthreads();
-    if (at.wave == 0 && live) {
+    if (at.wave == 0 && me.live) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float t = sum[j];
@@ -744,8 +820,11 @@ __global__ __launch_bounds__(256) void k_rec_step(RecArgs q, float* state_out, I
 
 template <typename F>
 hipError_t by_kind(const RecArgs& a, F f) {
+  auto packed = [&](auto io, auto decay, auto gated) {
+    return a.rows.starts ? f(io, decay, gated, std::true_type{}) : f(io, decay, gated, std::false_type{});
+  };
   auto gated = [&](auto io, auto decay) {
-    return a.gi ? f(io, decay, std::true_type{}) : f(io, decay, std::false_type{});
+    return a.gi ? packed(io, decay, std::true_type{}) : packed(io, decay, std::false_type{});
   };
   auto decays = [&](auto io) {
     return a.decay ? gated(io, std::true_type{}) : gated(io, std::false_type{});
@@ -753,37 +832,49 @@ hipError_t by_kind(const RecArgs& a, F f) {
   return a.io == kIoBf16 ? decays(u16{}) : decays(float{});
 }
 
+template <typename X>
 int tiles_of(const RecArgs& a) {
-  const int v = a.io == kIoBf16 ? 2 : 1;
-  return (a.C / v + 63) / 64;
+  const int width = 64 * X::B / (a.io == kIoBf16 ? 2 : 4);
+  return (a.C + width - 1) / width;
 }
 int64_t sum_floats(const RecArgs& a, const Plan& p) {
   return ((int64_t)p.units * a.C + 63) / 64 * 64;
 }
-int64_t counters_of(const RecArgs& a) { return (int64_t)tiles_of(a) * (a.rows.starts ? 1 : a.rows.S); }
+int64_t counters_of(const RecArgs& a) {
+  return (int64_t)tiles_of<Fwd>(a) * (a.rows.starts ? 1 : a.rows.S);
+}
 dim3 chain_grid(const RecArgs& a) {  // both directions
   const int64_t n = (a.rows.starts ? 1 : (int64_t)a.rows.S) * a.C;
   return dim3((unsigned)((n + 255) / 256), 2);
+}
+
+// Outputs past the caches: once they are a quarter of the last-level cache, what a call reads and the next
+// call wants stays there instead.
+int stream_of(const RecArgs& a) {
+  return (double)a.rows.R * a.C * (a.io == kIoBf16 ? 2 : 4) > 67108864.;
 }
 
 }  // namespace
 
 bool recurrence_fits(const RecArgs& a) {
   auto fits = [](double blocks, int threads) { return blocks * threads < 4294967296.0; };
-  const Plan p = plan(a.rows);
-  return fits(double(tiles_of(a)) * p.units + 4096, threads_of(p)) &&
+  const Plan f = plan<Fwd>(a.rows), b = plan<Bwd>(a.rows);
+  return fits(double(tiles_of<Fwd>(a)) * f.units + 4096, threads_of(f)) &&
+         fits(double(tiles_of<Bwd>(a)) * b.units + 4096, threads_of(b)) &&
          fits(double(a.rows.starts ? 1 : a.rows.S) * a.C / 256 + 1, 256);
 }
 
 // Chained: the tickets, then the slots.
 int64_t recurrence_bytes(const RecArgs& a) {
-  const Plan p = plan(a.rows);
+  const Plan p = plan<Fwd>(a.rows);
   return p.chunks > 1 ? 4 * kApart * counters_of(a) + 8 * (int64_t)p.units * a.C : 0;
 }
 
-hipError_t launch_recurrence(const RecArgs& a, void* y, float* fin, float* ws, hipStream_t s) {
-  const Plan p = plan(a.rows);
-  const int tiles = tiles_of(a);
+hipError_t launch_recurrence(const RecArgs& given, void* y, float* fin, float* ws, hipStream_t s) {
+  RecArgs a = given;
+  a.stream = stream_of(a);
+  const Plan p = plan<Fwd>(a.rows);
+  const int tiles = tiles_of<Fwd>(a);
   const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, fin);
   const int64_t counters = counters_of(a);
   const Chain chain{ws ? (uint64_t*)(ws + kApart * counters) : nullptr, (uint32_t*)ws, (int)counters};
@@ -791,25 +882,22 @@ hipError_t launch_recurrence(const RecArgs& a, void* y, float* fin, float* ws, h
     const int64_t n = (int64_t)p.units * a.C;  // more than counters
     hipLaunchKernelGGL(k_rec_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, chain, n);
   }
-  return by_kind(a, [&](auto io, auto decay, auto gated) {
+  return by_kind(a, [&](auto io, auto decay, auto gated, auto packed) {
     using IO = decltype(io);
-    constexpr bool D = decltype(decay)::value, G = decltype(gated)::value;
-    auto run = [&](auto packed, auto chained) {
-      hipLaunchKernelGGL((k_rec<IO, D, G, decltype(packed)::value, decltype(chained)::value>),
+    auto run = [&](auto chained) {
+      hipLaunchKernelGGL((k_rec<Fwd, IO, decltype(decay)::value, decltype(gated)::value,
+                                decltype(packed)::value, decltype(chained)::value>),
                          dim3(blocks + more), dim3(threads_of(p)), 0, s, a, p, tiles, chain, (IO*)y,
                          fin);
       return hipGetLastError();
     };
-    auto chains = [&](auto packed) {
-      return p.chunks > 1 ? run(packed, std::true_type{}) : run(packed, std::false_type{});
-    };
-    return a.rows.starts ? chains(std::true_type{}) : chains(std::false_type{});
+    return p.chunks > 1 ? run(std::true_type{}) : run(std::false_type{});
   });
 }
 
 hipError_t launch_recurrence_step(const RecArgs& a, float* state_out, void* y, hipStream_t s) {
   const unsigned blocks = (unsigned)(((int64_t)a.rows.R * (a.C / 4) + 255) / 256);
-  return by_kind(a, [&](auto io, auto decay, auto gated) {
+  return by_kind(a, [&](auto io, auto decay, auto gated, auto) {
     using IO = decltype(io);
     hipLaunchKernelGGL((k_rec_step<IO, decltype(decay)::value, decltype(gated)::value>),
                        dim3(blocks), dim3(256), 0, s, a, state_out, (IO*)y);
@@ -818,14 +906,16 @@ hipError_t launch_recurrence_step(const RecArgs& a, float* state_out, void* y, h
 }
 
 int64_t recurrence_backward_bytes(const RecArgs& a) {
-  const Plan p = plan(a.rows);
+  const Plan p = plan<Bwd>(a.rows);
   return 4 * sum_floats(a, p) * ((p.chunks > 1 ? 3 : 0) + (a.decay ? 1 : 0));
 }
 
-hipError_t launch_recurrence_backward(const RecArgs& a, const void* dy, const float* dfinal,
+hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, const float* dfinal,
                                       const RecGrads& g, float* ws, hipStream_t s) {
-  const Plan p = plan(a.rows);
-  const int tiles = tiles_of(a), chained = p.chunks > 1;
+  RecArgs a = given;
+  a.stream = stream_of(a);
+  const Plan p = plan<Bwd>(a.rows);
+  const int chained = p.chunks > 1;
   const int64_t n = sum_floats(a, p);
   Sums sums{nullptr, nullptr, nullptr};
   float* part = ws;
@@ -833,24 +923,22 @@ hipError_t launch_recurrence_backward(const RecArgs& a, const void* dy, const fl
     sums = Sums{ws, ws + n, ws + 2 * n};
     part = ws + 3 * n;
   }
-  const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, g.dh0);
-  const hipError_t e = by_kind(a, [&](auto io, auto decay, auto gated) {
+  const hipError_t e = by_kind(a, [&](auto io, auto decay, auto gated, auto packed) {
     using IO = decltype(io);
-    constexpr bool D = decltype(decay)::value, G = decltype(gated)::value;
-    auto run = [&](auto packed) {
-      constexpr bool K = decltype(packed)::value;
-      if (chained) {
-        hipLaunchKernelGGL((k_rec_bwd<IO, D, G, K, true>), dim3(blocks), dim3(threads_of(p)), 0, s, a,
-                           p, tiles, sums, 0, (const IO*)dy, dfinal, (IO*)nullptr, (IO*)nullptr,
-                           (IO*)nullptr, (float*)nullptr, (float*)nullptr);
-        hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(256), 0, s, a, p, sums, dfinal);
-      }
-      hipLaunchKernelGGL((k_rec_bwd<IO, D, G, K, false>), dim3(blocks + more), dim3(threads_of(p)), 0,
-                         s, a, p, tiles, sums, chained, (const IO*)dy, dfinal, (IO*)g.dx, (IO*)g.dg,
-                         (IO*)g.dgi, g.dh0, part);
-      return hipGetLastError();
-    };
-    return a.rows.starts ? run(std::true_type{}) : run(std::false_type{});
+    constexpr bool D = decltype(decay)::value, G = decltype(gated)::value, K = decltype(packed)::value;
+    if (chained) {
+      const Plan f = plan<Sum>(a.rows);  // the same chunks
+      const int tiles = tiles_of<Sum>(a);
+      hipLaunchKernelGGL((k_rec_sums<Sum, IO, D, G, K>), dim3((unsigned)((int64_t)tiles * f.units)),
+                         dim3(threads_of(f)), 0, s, a, f, tiles, sums, (const IO*)dy, dfinal);
+      hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(256), 0, s, a, p, sums, dfinal);
+    }
+    const int tiles = tiles_of<Bwd>(a);
+    const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, g.dh0);
+    hipLaunchKernelGGL((k_rec_bwd<Bwd, IO, D, G, K>), dim3(blocks + more), dim3(threads_of(p)), 0, s, a,
+                       p, tiles, sums, chained, (const IO*)dy, dfinal, (IO*)g.dx, (IO*)g.dg,
+                       (IO*)g.dgi, g.dh0, part);
+    return hipGetLastError();
   });
   if (e != hipSuccess || !a.decay) return e;
   return launch_column_sums(part, p.units, a.C, g.ddecay, a.C, 0, 1, 0, nullptr, 0, nullptr, s);

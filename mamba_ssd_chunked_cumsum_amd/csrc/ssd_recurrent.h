@@ -14,6 +14,7 @@ struct RecArgs {
   const float* decay;  // null: the gate is the decay
   float sharp;
   const float* h0;
+  int stream = 0;  // outputs are written past the caches
 };
 struct RecGrads {
   void *dx, *dg, *dgi;

@@ -29,7 +29,7 @@ class SSDRotation(ctypes.Structure):
                 ("interleaved", _i32), ("inverse", _i32), ("io_dtype", _i32), ("reserved", _i64)]
 
 
-_R = ctypes.POINTER(SSDRecurrent)
+_R, _Sections = ctypes.POINTER(SSDRecurrent), _i64 * 4
 _MORE = {
     "ssd_recurrence_workspace": [_T, _R, _PI],
     "ssd_recurrence": [_T, _R, _vp, _vp, _vp, _i64, _vp],
@@ -49,6 +49,15 @@ EXPORTS = tuple(_MORE)
 
 def _address(t):
     return None if t is None else t.data_ptr()
+
+
+def _like(given, name, like):
+    """(tensor, address) of the given output, checked, or of a new dense one of `like`'s shape and
+    type (empty_like is the cheapest call there is for that, where `like` is dense)."""
+    if given is None:
+        given = torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
+        return given, given.data_ptr()
+    return given, _tensor(given, name, like.shape, like.dtype, like.device)
 
 
 # ---- gated linear recurrence ---------------------------------------------------------------------
@@ -78,7 +87,7 @@ def recurrence(x, gate, decay=None, input_gate=None, initial_state=None, *, shar
     dev = x.device
     tok, S = _tokens(x, cu_seqlens)
     q = _recurrent(x, gate, decay, input_gate, initial_state, sharpness, S, x.shape[:2])
-    y, yp = _output(out, "out", x, x.shape, x.dtype)
+    y, yp = _like(out, "out", x)
     fin = fp = None
     if want_final:
         fin, fp = _output(final_out, "final_out", x, (S, x.shape[2]), torch.float32)
@@ -98,8 +107,8 @@ def recurrence_step(state, x, gate, decay=None, input_gate=None, *, sharpness=8.
         raise ValueError("state must be [batch, channels]")
     tok = SSDTokens(Bt, 1, C, Bt, None, io, 0)
     q = _recurrent(x, gate, decay, input_gate, state, sharpness, Bt, (Bt,))
-    y, yp = _output(out, "out", x, (Bt, C), x.dtype)
-    so, sop = _output(out_state, "out_state", x, (Bt, C), torch.float32)
+    y, yp = _like(out, "out", x)
+    so, sop = _like(out_state, "out_state", state)
     _run("ssd_recurrence_step", dev, ctypes.byref(tok), ctypes.byref(q), sop, yp)
     return y, so
 
@@ -116,10 +125,11 @@ def recurrence_backward(x, gate, decay, input_gate, dy, initial_state=None, dfin
     q = _recurrent(x, gate, decay, input_gate, initial_state, sharpness, S, x.shape[:2])
     dyp = _tensor(dy, "dy", x.shape, x.dtype, dev)
     dfp = _tensor(dfinal, "dfinal", (S, C), torch.float32, dev)
-    io, f32 = dict(dtype=x.dtype, device=dev), dict(dtype=torch.float32, device=dev)
-    g = dict(dx=torch.empty(x.shape, **io), dgate=torch.empty(x.shape, **io),
-             dinput_gate=None if input_gate is None else torch.empty(x.shape, **io),
-             ddecay=None if decay is None else torch.empty((C,), **f32),
+    f32 = dict(dtype=torch.float32, device=dev)
+    # (dy is dense, of x's shape and type)
+    g = dict(dx=torch.empty_like(dy), dgate=torch.empty_like(dy),
+             dinput_gate=None if input_gate is None else torch.empty_like(dy),
+             ddecay=None if decay is None else torch.empty_like(decay),
              dinitial_state=torch.empty((S, C), **f32) if want_initial_grad else None)
     t, qr = ctypes.byref(tok), ctypes.byref(q)
     ws, wp, n = _workspace("ssd_recurrence_backward_workspace", dev, t, qr)
@@ -154,10 +164,10 @@ def _rotate(B, C, names, positions, frequencies, sections, interleaved, inverse,
     bp, bs = _rows(B, names[0], B.shape, B.dtype, dev, n)
     cp, cs = _rows(C, names[1], B.shape, B.dtype, dev, n)
     given = (None, None) if out is None else out
-    Bo, bo = _output(given[0], "out", B, B.shape, B.dtype)
-    Co, co = (None, None) if C is None else _output(given[1], "out", B, B.shape, B.dtype)
+    Bo, bo = _like(given[0], "out", B)
+    Co, co = (None, None) if C is None else _like(given[1], "out", C)
     q = SSDRotation(
-        lead.numel(), G, N, nf, (_i64 * 4)(*sections),
+        lead.numel(), G, N, nf, _Sections(*sections),
         _tensor(positions, "positions", (axes, *lead), torch.int32, dev),
         _tensor(frequencies, "frequencies", (nf,), torch.float32, dev), bp, cp, bs, cs, axes,
         1 if interleaved else 0, inverse, DTYPES[B.dtype], 0)
@@ -197,7 +207,7 @@ def group_norm(x, weight=None, bias=None, *, ngroups, eps=1e-5, activation="silu
     xp, xs = _rows(x, "x", x.shape, x.dtype, dev)
     w = _tensor(weight, "weight", x.shape[2:], torch.float32, dev)
     b = _tensor(bias, "bias", x.shape[2:], torch.float32, dev)
-    y, yp = _output(out, "out", x, x.shape, x.dtype)
+    y, yp = _like(out, "out", x)
     stats = sp = None
     if want_stats and ngroups > 0:
         stats, sp = _output(None, "stats", x, (S, ngroups, 2), torch.float32)
@@ -219,10 +229,8 @@ def group_norm_backward(x, weight, bias, stats, dy, *, ngroups, activation="silu
     b = _tensor(bias, "bias", x.shape[2:], torch.float32, dev)
     st = _tensor(stats, "stats", (S, ngroups, 2), torch.float32, dev)
     dyp = _tensor(dy, "dy", x.shape, x.dtype, dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    g = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=dev),
-             dweight=None if weight is None else torch.empty(x.shape[2:], **f32),
-             dbias=None if bias is None else torch.empty(x.shape[2:], **f32))
+    g = dict(dx=torch.empty_like(dy), dweight=None if weight is None else torch.empty_like(weight),
+             dbias=None if bias is None else torch.empty_like(bias))
     t = ctypes.byref(tok)
     ws, wp, n = _workspace("ssd_group_norm_backward_workspace", dev, t, ngroups)
     _run("ssd_group_norm_backward", dev, t, xp, xs, w, b, ngroups, act, st, dyp,
