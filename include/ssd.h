@@ -439,7 +439,7 @@ ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* resi
  * a phase where B and C are rotated by their positions; and behind either stands a norm over groups of
  * channels. Tokens, strides, alignment, arithmetic, workspaces and errors as for the operators around
  * the scan above, and their limits; of launches below 2^32 threads: the recurrence takes rows (dense:
- * of sequences rounded up to 16) times channels / 128 (fp32: / 64), rounded up, below about 2^30, the
+ * of sequences rounded up to 28) times channels / 128 (fp32: / 64), rounded up, below 2^28, the
  * rotation rows times ngroups / 4 and nfreq / 4 + (dstate - 2 nfreq) / 8 below 2^32, the group norm
  * sequences times ngroups below 2^26 where a sequence may have more than 8 tokens. */
 

@@ -29,8 +29,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Rows of a wave (at most 31), waves of a block, bytes of a lane: of the forward, and of the backward's
 // two passes, whose chunks have the same rows.
 struct Fwd { static constexpr int T = 16, W = 8, B = 4; };
-struct Sum { static constexpr int T = 8, W = 4, B = 4; };
-struct Bwd { static constexpr int T = 8, W = 4, B = 4; };
+struct Tall { static constexpr int T = 16, W = 16, B = 4; };  // forward where that is one block a unit
+struct Sum { static constexpr int T = 7, W = 4, B = 4; };
+struct Bwd { static constexpr int T = 7, W = 4, B = 4; };  // (eight rows would take 134 registers of 128)
 static_assert(Sum::T * Sum::W == Bwd::T * Bwd::W, "");
 template <typename IO, typename X>
 constexpr int kV = X::B / (int)sizeof(IO);  // channels of a lane
@@ -390,17 +391,25 @@ __global__ __launch_bounds__(64 * X::W) void k_rec(RecArgs q, Plan pl, int tiles
 #pragma unroll
   for (int j = 0; j < V; ++j) runs[at.wave][j][lane] = make_float2(p[j], h[j]);
   __syncthreads();
+  // the run of the waves in front of this one; of wave 0 with a chain: of all the block's
+  const int to = CHAIN && at.wave == 0 ? pl.waves : at.wave;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float2 r[X::W];
+#pragma unroll
+    for (int w = 0; w < X::W; ++w) r[w] = runs[w][j][lane];
+    p[j] = 1.f, h[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < X::W; ++w)
+      if (w >= at.lo && w < to) {
+        h[j] = enter(r[w].x, r[w].y, h[j]);
+        p[j] = join(p[j], r[w].x);
+      }
+  }
   float e[V];  // the state that enters
   if (CHAIN) {
     const int chunk = PACKED ? at.unit : at.unit % pl.chunks;
     if (at.wave == 0) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        for (int w = 1; w < pl.waves; ++w) {
-          const float2 r = runs[w][j][lane];
-          h[j] = enter(r.x, r.y, h[j]);
-          p[j] = join(p[j], r.x);
-        }
       uint64_t* slot = chain.slots + (int64_t)at.unit * q.C + c;
       const bool hands_on = chunk % kGroup == kGroup - 1, needed = chunk + 1 < pl.chunks;
       if (needed && !hands_on && me.live) {
@@ -453,10 +462,7 @@ __global__ __launch_bounds__(64 * X::W) void k_rec(RecArgs q, Plan pl, int tiles
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    for (int w = at.lo; w < at.wave; ++w) {
-      const float2 r = runs[w][j][lane];
-      e[j] = enter(r.x, r.y, e[j]);
-    }
+    if (!CHAIN || at.wave) e[j] = enter(p[j], h[j], e[j]);
 #pragma unroll
     for (int i = 0; i < T; ++i)
       H[i][j] = PACKED ? enter(P[i][j], H[i][j], e[j]) : fmaf(P[i][j], e[j], H[i][j]);
@@ -843,6 +849,14 @@ int64_t sum_floats(const RecArgs& a, const Plan& p) {
 int64_t counters_of(const RecArgs& a) {
   return (int64_t)tiles_of<Fwd>(a) * (a.rows.starts ? 1 : a.rows.S);
 }
+// Blocks of sixteen waves where all of them run at once, one a compute unit: half as many chunks wait for
+// one another (5003 packed x 1536 bf16: 28 -> 25 us; with more blocks than that, 2 x 8192 x 5120, two of
+// eight waves a unit overlap better: 160 against 187 us).
+bool tall(const RecArgs& a) {
+  const Plan p = plan<Tall>(a.rows);
+  return p.chunks > 1 && (int64_t)tiles_of<Tall>(a) * p.units <= 256 &&
+         (int64_t)tiles_of<Fwd>(a) * plan<Fwd>(a.rows).units > 256;
+}
 dim3 chain_grid(const RecArgs& a) {  // both directions
   const int64_t n = (a.rows.starts ? 1 : (int64_t)a.rows.S) * a.C;
   return dim3((unsigned)((n + 255) / 256), 2);
@@ -866,14 +880,15 @@ bool recurrence_fits(const RecArgs& a) {
 
 // Chained: the tickets, then the slots.
 int64_t recurrence_bytes(const RecArgs& a) {
-  const Plan p = plan<Fwd>(a.rows);
+  const Plan p = tall(a) ? plan<Tall>(a.rows) : plan<Fwd>(a.rows);
   return p.chunks > 1 ? 4 * kApart * counters_of(a) + 8 * (int64_t)p.units * a.C : 0;
 }
 
 hipError_t launch_recurrence(const RecArgs& given, void* y, float* fin, float* ws, hipStream_t s) {
   RecArgs a = given;
   a.stream = stream_of(a);
-  const Plan p = plan<Fwd>(a.rows);
+  const bool high = tall(a);
+  const Plan p = high ? plan<Tall>(a.rows) : plan<Fwd>(a.rows);
   const int tiles = tiles_of<Fwd>(a);
   const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, fin);
   const int64_t counters = counters_of(a);
@@ -884,14 +899,15 @@ hipError_t launch_recurrence(const RecArgs& given, void* y, float* fin, float* w
   }
   return by_kind(a, [&](auto io, auto decay, auto gated, auto packed) {
     using IO = decltype(io);
-    auto run = [&](auto chained) {
-      hipLaunchKernelGGL((k_rec<Fwd, IO, decltype(decay)::value, decltype(gated)::value,
+    auto run = [&](auto shape, auto chained) {
+      hipLaunchKernelGGL((k_rec<decltype(shape), IO, decltype(decay)::value, decltype(gated)::value,
                                 decltype(packed)::value, decltype(chained)::value>),
                          dim3(blocks + more), dim3(threads_of(p)), 0, s, a, p, tiles, chain, (IO*)y,
                          fin);
       return hipGetLastError();
     };
-    return p.chunks > 1 ? run(std::true_type{}) : run(std::false_type{});
+    if (high) return run(Tall{}, std::true_type{});
+    return p.chunks > 1 ? run(Fwd{}, std::true_type{}) : run(Fwd{}, std::false_type{});
   });
 }
 

@@ -67,8 +67,8 @@ def test_recurrence_valid_requests_report_no_device():
     assert Recurrence(t=one()).step() == Recurrence(t=one(), fin=addr(4)).step() == NO_DEVICE
     assert Recurrence(fin=None, ws=None, n=0, gate_stride=72, sharpness=0.0, **BARE).forward() == \
         NO_DEVICE
-    assert Recurrence(di=None, dd=None, df=None, dh=None, ws=None, n=0, **BARE).backward() == \
-        NO_DEVICE
+    assert Recurrence(t=tokens(seqlen=28), di=None, dd=None, df=None, dh=None, ws=None, n=0,
+                      **BARE).backward() == NO_DEVICE
 
 
 @no_gpu
@@ -190,7 +190,7 @@ def test_group_norm_valid_and_rejected():
 
 def test_workspace_queries():
     n = ctypes.c_int64()
-    long, short = tokens(batch=1, nseq=1, seqlen=1000), tokens(batch=2, nseq=2, seqlen=50)
+    long, short = tokens(batch=1, nseq=1, seqlen=1000), tokens(batch=2, nseq=2, seqlen=28)
     for name in ("ssd_recurrence_workspace", "ssd_recurrence_backward_workspace"):
         f = block._function(name)
         q = Recurrence()._args()[1]
@@ -230,8 +230,8 @@ def groups_of_norm(n):
 @no_gpu
 @pytest.mark.parametrize("call,taken,refused", [
     (lambda n: Recurrence(t=tokens(seqlen=1, channels=8 * n)).forward(), 2 ** 17, 2 ** 17 + 1),
-    (rows_of_recurrence, 2 ** 30 - 2 ** 20, 2 ** 30),
-    (lambda n: rows_of_recurrence(n, 1024), 2 ** 27 - 2 ** 20, 2 ** 27),
+    (rows_of_recurrence, 2 ** 28, 2 ** 29),
+    (lambda n: rows_of_recurrence(n, 1024), 2 ** 25, 2 ** 26),
     (rows_of_rotation, 2 ** 31 - 4097, 2 ** 31 - 4096),
     (lambda n: rows_of_rotation(n, 16), 2 ** 30 - 65, 2 ** 30),
     (groups_of_norm, 2 ** 20 - 1, 2 ** 20)])
