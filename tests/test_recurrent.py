@@ -610,7 +610,8 @@ def test_offsets_beyond_32_bits():
 
 def test_many_empty_sequences():
     """A million packed sequences, all but three empty: states pass through, the rest is what the three
-    give alone."""
+    give alone; the group norm's rows are divided otherwise there, so its sums of some hundred values are
+    in another order: to 2^-17 of the largest value, some tens of fp32 roundings."""
     note("many empty sequences")
     S, C, rows = 1_000_003, 64, 300
     ends = [100, 250, 300]
@@ -637,7 +638,8 @@ def test_many_empty_sequences():
     assert all(torch.equal(g[k], g2[k]) for k in ("dx", "dgate", "ddecay"))
     n, st = ssd.group_norm(t["x"], ngroups=8, cu_seqlens=cu)
     n2, st2 = ssd.group_norm(t["x"], ngroups=8, cu_seqlens=few)
-    assert torch.equal(n, n2) and torch.equal(st[at], st2)
+    for a, b in ((n, n2), (st[at], st2)):
+        assert (a - b).abs().max() <= 2.0 ** -17 * b.abs().max()
 
 
 # ---- together --------------------------------------------------------------------------------------

@@ -162,15 +162,18 @@ def test_rotation_checks(kw, status):
 def test_group_norm_valid_and_rejected():
     F, B = block._function("ssd_group_norm"), block._function("ssd_group_norm_backward")
 
-    def forward(t=tokens(), x=addr(0), xs=0, w=addr(1), b=addr(2), g=4, eps=1e-5, y=addr(3),
+    long = tokens(seqlen=50000)
+
+    def forward(t=long, x=addr(0), xs=0, w=addr(1), b=addr(2), g=4, eps=1e-5, y=addr(3),
                 st=addr(4), ws=addr(5), n=1 << 33):
         return F(ctypes.byref(t), x, xs, w, b, g, eps, 1, y, st, ws, n, None)
 
-    def backward(t=tokens(), w=addr(1), b=addr(2), g=4, st=addr(4), dy=addr(6), dx=addr(7),
+    def backward(t=long, w=addr(1), b=addr(2), g=4, st=addr(4), dy=addr(6), dx=addr(7),
                  dw=addr(8), db=addr(9), ws=addr(5), n=1 << 33):
         return B(ctypes.byref(t), addr(0), 0, w, b, g, 1, st, dy, dx, dw, db, ws, n, None)
 
     few = tokens(seqlen=3)
+    assert forward(t=tokens(), ws=None, n=0) == backward(t=tokens()) == NO_DEVICE
     assert forward() == forward(w=None, b=None, st=None, xs=72, g=64) == NO_DEVICE
     assert forward(t=few, ws=None, n=0) == forward(t=tokens(**PACKED), eps=0.0) == NO_DEVICE
     assert backward() == backward(w=None, dw=None) == backward(b=None, db=None) == NO_DEVICE
@@ -202,6 +205,7 @@ def test_workspace_queries():
         assert block._function(name)(ctypes.byref(short), q, ctypes.byref(n)) == OK and n.value == 0
     for name in ("ssd_group_norm_workspace", "ssd_group_norm_backward_workspace"):
         f = block._function(name)
+        long.seqlen = 50000
         assert f(ctypes.byref(long), 4, ctypes.byref(n)) == OK and n.value > 0
         assert f(ctypes.byref(long), 4, None) == f(ctypes.byref(long), 0, ctypes.byref(n)) == INVALID
 
