@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const
              o[j] = fmaf((v[k].get(j) - st[j].x) * st[j].y, af.w[j], af.b[j]);
              if (q.act) o[j] *= sigmoid(o[j]);
            }
-           if (live) store_vec<IO, V>(y + (int64_t)row * q.C + c, o);
+           if (live) store_vec<IO, V>(y + (int64_t)row * q.C + c, o, q.stream);
          });
   });
 }
@@ -552,7 +552,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_few(GroupArgs q, Few f, float* 
         o[j] = fmaf((v[i].get(j) - mean) * rstd, af.w[j], af.b[j]);
         if (q.act) o[j] *= sigmoid(o[j]);
       }
-      store_vec<IO, V>(y + (s * L + i) * q.C + c, o);
+      store_vec<IO, V>(y + (s * L + i) * q.C + c, o, q.stream);
     }
 }
 
@@ -749,7 +749,7 @@ __global__ __launch_bounds__(kWhole) void k_gn_whole(GroupArgs q, Whole w, float
       o[j] = fmaf((v[k].get(j) - mean) * rstd, af.w[j], af.b[j]);
       if (q.act) o[j] *= sigmoid(o[j]);
     }
-    store_vec<IO, V>(y + r * q.C + p.c, o);
+    store_vec<IO, V>(y + r * q.C + p.c, o, q.stream);
   });
 }
 
@@ -883,7 +883,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_tokens(GroupArgs q, float2* sta
       o[j] = fmaf((v[i].get(j) - mean) * rstd, af.w[j], af.b[j]);
       if (q.act) o[j] *= sigmoid(o[j]);
     }
-    store_vec<IO, V>(y + (s0 + i) * q.C + c, o);
+    store_vec<IO, V>(y + (s0 + i) * q.C + c, o, q.stream);
   }
 }
 
@@ -984,8 +984,10 @@ int64_t group_norm_bytes(const GroupArgs& a) {
   return 8 * (up64(t.slots * t.pieces) + (int64_t)a.rows.S * a.G);
 }
 
-hipError_t launch_group_norm(const GroupArgs& a, void* y, float* stats, float* ws,
+hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, float* ws,
                              hipStream_t s) {
+  GroupArgs a = given;
+  a.stream = past_caches((double)a.rows.R * a.C * (a.io == kIoBf16 ? 2 : 4));
   auto run = [&](auto io) {
     using IO = decltype(io);
     if (single_tokens(a)) {

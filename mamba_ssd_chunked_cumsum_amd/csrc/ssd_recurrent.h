@@ -5,6 +5,10 @@
 
 namespace ssd {
 
+// Whether outputs of so many bytes are written past the caches: from a quarter of the last-level cache on,
+// so that what a call reads twice, and what the next one reads, stays there instead.
+inline bool past_caches(double bytes) { return bytes > 67108864.; }
+
 // ---- gated linear recurrence ---------------------------------------------------------------------
 struct RecArgs {
   Rows rows;
@@ -40,6 +44,7 @@ struct RotArgs {
   const void *b, *c;  // c null: b alone
   int64_t bs, cs;
   void *ob, *oc;
+  int stream = 0;  // outputs are written past the caches
 };
 bool rotate_fits(const RotArgs& a);
 hipError_t launch_rotate(const RotArgs& a, hipStream_t s);
@@ -52,6 +57,7 @@ struct GroupArgs {
   const void* x;
   int64_t xs;
   const float *w, *b;  // null: 1, 0
+  int stream = 0;      // outputs are written past the caches
 };
 bool group_norm_fits(const GroupArgs& a);  // whether its launches do
 int64_t group_norm_bytes(const GroupArgs& a);

@@ -97,8 +97,8 @@ __global__ __launch_bounds__(256) void k_rotate(RotArgs q, int units, int splits
         }
       }
       IO* to = (IO*)(t ? q.oc : q.ob) + (row * q.G + g) * q.N;
-      store_vec<IO, F>(to + p0, o[0]);
-      store_vec<IO, F>(to + p1, o[1]);
+      store_vec<IO, F>(to + p0, o[0], q.stream);
+      store_vec<IO, F>(to + p1, o[1], q.stream);
     }
   }
 }
@@ -110,7 +110,9 @@ bool rotate_fits(const RotArgs& a) {
          4294967296.0;
 }
 
-hipError_t launch_rotate(const RotArgs& a, hipStream_t s) {
+hipError_t launch_rotate(const RotArgs& given, hipStream_t s) {
+  RotArgs a = given;
+  a.stream = past_caches((double)a.rows * a.G * a.N * (a.io == kIoBf16 ? 2 : 4));
   auto run = [&](auto io, auto freqs) {
     using IO = decltype(io);
     constexpr int F = decltype(freqs)::value;

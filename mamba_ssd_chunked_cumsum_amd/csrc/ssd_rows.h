@@ -77,7 +77,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ void store_io(float* p, int i, float v) { p[i] = v; }
 __device__ __forceinline__ void store_io(u16* p, int i, float v) { p[i] = (u16)pack_bf16(v, v); }
 
-// stream: past the caches, for outputs far larger than they are.
+// stream: past the caches, for outputs far larger than they are. The empty statements keep the two
+// stores from becoming one, which would be a plain one.
+template <typename W>
+__device__ __forceinline__ void store_words(W* p, W w, bool stream) {
+  if (stream) {
+    asm volatile("" ::: "memory");
+    __builtin_nontemporal_store(w, p);
+    asm volatile("" ::: "memory");
+  } else {
+    *p = w;
+  }
+}
 template <typename IO, int V>
 __device__ __forceinline__ void store_vec(IO* p, const float (&v)[V], bool stream = false) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -93,11 +104,11 @@ __device__ __forceinline__ void store_vec(IO* p, const float (&v)[V], bool strea
 #pragma unroll
     for (int i = 0; i < Vec<IO, V>::kWords / 4; ++i) {
       const u32x4 w = {u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]};
-      if (stream) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p) + i);
-      else reinterpret_cast<u32x4*>(p)[i] = w;
+      store_words(reinterpret_cast<u32x4*>(p) + i, w, stream);
     }
   } else {
-    *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    store_words(reinterpret_cast<u32x2*>(p), u32x2{u[0], u[1]}, stream);
   }
 }
 
