@@ -98,14 +98,16 @@ __device__ __forceinline__ Step step_of(float g, float rate) {
 
 // sharpness softplus(decay) log2(e), to a few roundings: exp(-|d|) with the product's rounding made
 // good, log(1 + e) by its series where e is small, else from the hardware's log2 of the rounded sum and
-// what the rounding lost.
+// what the rounding lost. Finite for an infinite decay (at most 2^126), so that nothing times it is NaN;
+// the minima keep NaN.
 __device__ __forceinline__ float decay_rate(const RecArgs& q, int c) {
-  const float d = q.decay[c], v = -fabsf(d), hi = v * kLog2e;
+  const float d = q.decay[c], v = -__builtin_elementwise_minimum(fabsf(d), 200.f), hi = v * kLog2e;
   const float lo = fmaf(v, kLog2e, -hi) + v * 1.9259629911e-8f;  // log2(e) is 1.9e-8 above kLog2e
   const float e = exp2_fast(hi), x = fmaf(e, lo * kLn2, e), w = 1.f + x;
   const float small = x * fmaf(x, fmaf(x, fmaf(x, -0.25f, 1.f / 3.f), -0.5f), 1.f);
   const float large = fmaf(__builtin_amdgcn_logf(w), kLn2, x - (w - 1.f));
-  return q.sharp * (fmaxf(d, 0.f) + (x < 0x1p-6f ? small : large)) * kLog2e;
+  const float rate = q.sharp * (fmaxf(d, 0.f) + (x < 0x1p-6f ? small : large)) * kLog2e;
+  return __builtin_elementwise_minimum(rate, 0x1p126f);
 }
 
 // P of a run with a sequence's start in it is -0 (products of decays are never negative): what

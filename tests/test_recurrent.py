@@ -168,6 +168,33 @@ def test_recurrence_extremes():
         check(g["ddecay"][torch.from_numpy(m).to(DEV)], pick(wg["ddecay"], m), "ddecay")
 
 
+def test_recurrence_infinite_decays():
+    """An infinite decay parameter forgets all and takes the input whole, one of minus infinity keeps all
+    and takes nothing; gates at both infinities; NaN stays NaN; gradients are finite but for NaN's."""
+    note("recurrence infinite decays")
+    inf, L, C = float("inf"), 40, 64
+    g = torch.Generator(DEV).manual_seed(68)
+    x, gate, dy = (torch.randn(1, L, C, device=DEV, generator=g) for _ in range(3))
+    decay = torch.zeros(C, device=DEV)
+    decay[0], decay[1], decay[2] = inf, -inf, float("nan")
+    gate[0, :, 3], gate[0, :, 4] = inf, -inf
+    h0 = torch.randn(1, C, device=DEV, generator=g)
+    y, f = ssd.recurrence(x, gate, decay, None, h0)
+    assert torch.equal(y[0, :, 0], x[0, :, 0]) and torch.equal(f[0, 0], x[0, -1, 0])
+    assert torch.all(y[0, :, 1] == h0[0, 1]) and torch.all(y[0, :, 4] == h0[0, 4])
+    a = 2.0 ** -8  # softplus(0) = log 2, the gate wide open
+    want, w64 = torch.empty(L, dtype=torch.float64), h0[0, 3].double().cpu()
+    for t in range(L):
+        w64 = a * w64 + (1 - a * a) ** 0.5 * x[0, t, 3].double().cpu()
+        want[t] = w64
+    assert torch.all((y[0, :, 3].double().cpu() - want).abs() <= 2.0 ** -24 * 64 * want.abs().max())
+    assert torch.isnan(y[0, :, 2]).all() and torch.isnan(y).sum() == L
+    grads = ssd.recurrence_backward(x, gate, decay, None, dy, h0)
+    for k in ("dx", "dgate", "ddecay", "dinitial_state"):
+        v = grads[k].reshape(-1, C)
+        assert torch.isnan(v[:, 2]).all() and torch.isnan(v).sum() == v.shape[0], k
+
+
 def test_recurrence_nan_and_infinity_stay_in_their_channel():
     rng = np.random.default_rng(64)
     L, C = 400, 64
