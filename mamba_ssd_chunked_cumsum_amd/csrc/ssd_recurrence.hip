@@ -27,12 +27,12 @@ constexpr int kGroup = 8;  // chunks between those that hand on their end state
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Rows of a wave (at most 31), waves of a block, bytes of a lane: of the forward, and of the backward's
-// two passes, whose chunks have the same rows.
+// two passes (bf16, fp32).
 struct Fwd { static constexpr int T = 16, W = 8, B = 4; };
 struct Tall { static constexpr int T = 16, W = 16, B = 4; };  // forward where that is one block a unit
-struct Sum { static constexpr int T = 7, W = 4, B = 4; };
-struct Bwd { static constexpr int T = 7, W = 4, B = 4; };  // (eight rows would take 134 registers of 128)
-static_assert(Sum::T * Sum::W == Bwd::T * Bwd::W, "");
+// As many rows as fit 128 registers (eight of bf16 would take 134).
+struct Bwd { static constexpr int T = 7, W = 4, B = 4; };
+struct Bwd32 { static constexpr int T = 12, W = 4, B = 4; };
 template <typename IO, typename X>
 constexpr int kV = X::B / (int)sizeof(IO);  // channels of a lane
 
@@ -832,6 +832,12 @@ hipError_t by_kind(const RecArgs& a, F f) {
   return a.io == kIoBf16 ? decays(u16{}) : decays(float{});
 }
 
+// The backward's shape and plan.
+template <typename F>
+auto by_shape(const RecArgs& a, F f) {
+  return a.io == kIoBf16 ? f(Bwd{}, plan<Bwd>(a.rows)) : f(Bwd32{}, plan<Bwd32>(a.rows));
+}
+
 template <typename X>
 int tiles_of(const RecArgs& a) {
   const int width = 64 * X::B / (a.io == kIoBf16 ? 2 : 4);
@@ -866,7 +872,7 @@ int stream_of(const RecArgs& a) {
 
 bool recurrence_fits(const RecArgs& a) {
   auto fits = [](double blocks, int threads) { return blocks * threads < 4294967296.0; };
-  const Plan f = plan<Fwd>(a.rows), b = plan<Bwd>(a.rows);
+  const Plan f = plan<Fwd>(a.rows), b = by_shape(a, [](auto, Plan p) { return p; });
   return fits(double(tiles_of<Fwd>(a)) * f.units + 4096, threads_of(f)) &&
          fits(double(tiles_of<Bwd>(a)) * b.units + 4096, threads_of(b)) &&
          fits(double(a.rows.starts ? 1 : a.rows.S) * a.C / 256 + 1, 256);
@@ -916,7 +922,7 @@ hipError_t launch_recurrence_step(const RecArgs& a, float* state_out, void* y, h
 }
 
 int64_t recurrence_backward_bytes(const RecArgs& a) {
-  const Plan p = plan<Bwd>(a.rows);
+  const Plan p = by_shape(a, [](auto, Plan b) { return b; });
   return 4 * sum_floats(a, p) * ((p.chunks > 1 ? 3 : 0) + (a.decay ? 1 : 0));
 }
 
@@ -924,8 +930,8 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
                                       const RecGrads& g, float* ws, hipStream_t s) {
   RecArgs a = given;
   a.stream = stream_of(a);
-  const Plan p = plan<Bwd>(a.rows);
-  const int chained = p.chunks > 1;
+  const Plan p = by_shape(a, [](auto, Plan b) { return b; });
+  const int tiles = tiles_of<Bwd>(a), chained = p.chunks > 1;
   const int64_t n = sum_floats(a, p);
   Sums sums{nullptr, nullptr, nullptr};
   float* part = ws;
@@ -933,19 +939,17 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
     sums = Sums{ws, ws + n, ws + 2 * n};
     part = ws + 3 * n;
   }
+  const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, g.dh0);
   const hipError_t e = by_kind(a, [&](auto io, auto decay, auto gated, auto packed) {
     using IO = decltype(io);
+    using X = std::conditional_t<sizeof(IO) == 2, Bwd, Bwd32>;
     constexpr bool D = decltype(decay)::value, G = decltype(gated)::value, K = decltype(packed)::value;
     if (chained) {
-      const Plan f = plan<Sum>(a.rows);  // the same chunks
-      const int tiles = tiles_of<Sum>(a);
-      hipLaunchKernelGGL((k_rec_sums<Sum, IO, D, G, K>), dim3((unsigned)((int64_t)tiles * f.units)),
-                         dim3(threads_of(f)), 0, s, a, f, tiles, sums, (const IO*)dy, dfinal);
+      hipLaunchKernelGGL((k_rec_sums<X, IO, D, G, K>), dim3(blocks), dim3(threads_of(p)), 0, s, a, p,
+                         tiles, sums, (const IO*)dy, dfinal);
       hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(256), 0, s, a, p, sums, dfinal);
     }
-    const int tiles = tiles_of<Bwd>(a);
-    const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, g.dh0);
-    hipLaunchKernelGGL((k_rec_bwd<Bwd, IO, D, G, K>), dim3(blocks + more), dim3(threads_of(p)), 0, s, a,
+    hipLaunchKernelGGL((k_rec_bwd<X, IO, D, G, K>), dim3(blocks + more), dim3(threads_of(p)), 0, s, a,
                        p, tiles, sums, chained, (const IO*)dy, dfinal, (IO*)g.dx, (IO*)g.dg,
                        (IO*)g.dgi, g.dh0, part);
     return hipGetLastError();
