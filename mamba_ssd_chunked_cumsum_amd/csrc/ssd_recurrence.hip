@@ -494,33 +494,51 @@ struct Sums {
 
 // Chain over the chunks, in place: sums.H from a chunk's end state to the state entering it
 // (blockIdx.y 0), sums.G from what leaves the chunk to the left to what enters it from the right
-// (blockIdx.y 1). Bound by the latency of its loads, which are issued kAhead chunks at a time.
-__global__ __launch_bounds__(256) void k_rec_chain(RecArgs q, Plan pl, Sums sums,
-                                                   const float* __restrict__ dfinal) {
-  constexpr int kAhead = 32;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= (q.rows.starts ? 1 : (int64_t)q.rows.S) * q.C) return;
-  const int64_t s = id / q.C;
-  const int c = (int)(id % q.C);
-  const bool back = blockIdx.y;
+// (blockIdx.y 1). Bound by the latency of its loads: the kParts waves of a block take a run of chunks of
+// the same 64 channels each, up to kAhead of them, whose loads are issued together, and join their runs
+// through LDS (147 chunks of 2 x 5120 channels: 15 -> 11 us against one thread for all of a channel's).
+constexpr int kParts = 8, kAhead = 32;
+__global__ __launch_bounds__(64 * kParts) void k_rec_chain(RecArgs q, Plan pl, Sums sums,
+                                                           const float* __restrict__ dfinal) {
+  __shared__ float2 runs[kParts][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t all = (q.rows.starts ? 1 : (int64_t)q.rows.S) * q.C;
+  const bool live = (int64_t)blockIdx.x * 64 + lane < all, back = blockIdx.y;
+  const int64_t id = live ? (int64_t)blockIdx.x * 64 + lane : all - 1;
+  const int64_t base = id / q.C * pl.chunks * q.C + id % q.C;
   const float* start = q.rows.starts ? nullptr : back ? dfinal : q.h0;
-  float h = start ? start[id] : 0.f;
-  const int64_t base = s * pl.chunks * q.C + c;
   float* io = back ? sums.G : sums.H;
-  for (int u = 0; u < pl.chunks; u += kAhead) {
-    float P[kAhead], H[kAhead];
+  float carry = start ? start[id] : 0.f;
+  const int each = min((pl.chunks + kParts - 1) / kParts, kAhead);
+  for (int u0 = 0; u0 < pl.chunks; u0 += kParts * each) {
+    const int first = u0 + wave * each, n = min(pl.chunks - first, each);
+    auto place = [&](int i) { return base + (int64_t)(back ? pl.chunks - 1 - first - i : first + i) * q.C; };
+    float P[kAhead], H[kAhead], p = 1.f, h = 0.f;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int v = min(u + i, pl.chunks - 1);
-      const int64_t o = base + (int64_t)(back ? pl.chunks - 1 - v : v) * q.C;
-      P[i] = sums.P[o];
-      H[i] = io[o];
+    for (int i = 0; i < kAhead; ++i)
+      if (i < n) P[i] = sums.P[place(i)], H[i] = io[place(i)];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < n) {
+        h = enter(P[i], H[i], h);
+        p = join(p, P[i]);
+      }
+    __syncthreads();  // what was here has been read
+    runs[wave][lane] = make_float2(p, h);
+    __syncthreads();
+    float e = carry;
+#pragma unroll
+    for (int w = 0; w < kParts; ++w) {
+      const float2 r = runs[w][lane];
+      if (w == wave) e = carry;
+      carry = enter(r.x, r.y, carry);
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (u + i < pl.chunks) io[base + (int64_t)(back ? pl.chunks - 1 - u - i : u + i) * q.C] = h;
-      h = enter(P[i], H[i], h);
-    }
+    for (int i = 0; i < kAhead; ++i)
+      if (i < n) {
+        if (live) io[place(i)] = e;
+        e = enter(P[i], H[i], e);
+      }
   }
 }
 
@@ -859,7 +877,7 @@ bool tall(const RecArgs& a) {
 }
 dim3 chain_grid(const RecArgs& a) {  // both directions
   const int64_t n = (a.rows.starts ? 1 : (int64_t)a.rows.S) * a.C;
-  return dim3((unsigned)((n + 255) / 256), 2);
+  return dim3((unsigned)((n + 63) / 64), 2);
 }
 
 // (The backward's first pass finds more of its inputs there: 2 x 4096 x 5120 88 -> 72 us; the forward of
@@ -875,7 +893,7 @@ bool recurrence_fits(const RecArgs& a) {
   const Plan f = plan<Fwd>(a.rows), b = by_shape(a, [](auto, Plan p) { return p; });
   return fits(double(tiles_of<Fwd>(a)) * f.units + 4096, threads_of(f)) &&
          fits(double(tiles_of<Bwd>(a)) * b.units + 4096, threads_of(b)) &&
-         fits(double(a.rows.starts ? 1 : a.rows.S) * a.C / 256 + 1, 256);
+         fits(double(a.rows.starts ? 1 : a.rows.S) * a.C / 64 + 1, 64 * kParts);
 }
 
 // Chained: the tickets, then the slots.
@@ -947,7 +965,7 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
     if (chained) {
       hipLaunchKernelGGL((k_rec_sums<X, IO, D, G, K>), dim3(blocks), dim3(threads_of(p)), 0, s, a, p,
                          tiles, sums, (const IO*)dy, dfinal);
-      hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(256), 0, s, a, p, sums, dfinal);
+      hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(64 * kParts), 0, s, a, p, sums, dfinal);
     }
     hipLaunchKernelGGL((k_rec_bwd<X, IO, D, G, K>), dim3(blocks + more), dim3(threads_of(p)), 0, s, a,
                        p, tiles, sums, chained, (const IO*)dy, dfinal, (IO*)g.dx, (IO*)g.dg,
