@@ -30,6 +30,11 @@ __device__ __forceinline__ float act_slope(float v) {  // of v sigmoid(v)
   return s * fmaf(v, 1.f - s, 1.f);
 }
 
+// 1 / sqrt(v), to a unit in the last place (below 2^-126 the instruction would take v as zero).
+__device__ __forceinline__ float inverse_root(float v) {
+  return v < 0x1p-126f ? 1.f / sqrtf(v) : __builtin_amdgcn_rsqf(v);
+}
+
 // ---- how a problem is cut --------------------------------------------------------------------------
 // Strips of `rows` rows, of each sequence or (packed) of all rows, where the part of each sequence in a
 // strip has a slot of its own: strip + sequence, which grows by one from each part to the next. In the
@@ -276,18 +281,28 @@ struct Affine {
   }
 };
 
+// A pair for each of a thread's channels, or (ONE: groups of a multiple of 8 channels) one for all.
+template <bool ONE>
+struct Pair {
+  float2 v[ONE ? 1 : V];
+  __device__ __forceinline__ float2 operator[](int j) const { return v[ONE ? 0 : j]; }
+  __device__ __forceinline__ void load(const GroupArgs& q, const float2* from, int s, int c) {
+#pragma unroll
+    for (int j = 0; j < (ONE ? 1 : V); ++j) v[j] = from[(int64_t)s * q.G + (c + j) / (q.C / q.G)];
+  }
+};
+
 // A pair a group of the tile (statistics, or means of the backward pass), of sequence s: read, or added
-// up here (`add`); to v of this thread's channels.
+// up here; to v of this thread's channels.
 struct Pairs {
   float2 of[kTile];
-  template <bool BACK>
+  template <bool BACK, bool ONE>
   __device__ __forceinline__ void get(const GroupArgs& q, const Cut& t, const float2* part,
-                                      const float2* ready, int s, int tile, int c, float2 (&v)[V],
+                                      const float2* ready, int s, int tile, int c, Pair<ONE>& v,
                                       float2* out) {
     const int cg = q.C / q.G;
     if (ready) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = ready[(int64_t)s * q.G + (c + j) / cg];
+      v.load(q, ready, s, c);
       return;
     }
     const int g0 = tile * kTile / cg;
@@ -301,12 +316,12 @@ struct Pairs {
     });
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = of[(c + j) / cg - g0];
+    for (int j = 0; j < (ONE ? 1 : V); ++j) v.v[j] = of[(c + j) / cg - g0];
   }
 };
 
 // stats: written where given and not `ready` (by each strip alike: the same bits).
-template <typename IO>
+template <typename IO, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const float2* part,
                                                        const float2* ready, float2* stats, IO* y) {
   __shared__ Pairs pairs;
@@ -316,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const
   const IO* x = (const IO*)q.x + c;
   const Affine af(q, c);
   parts(q.rows, t, (int)(blockIdx.x / t.tiles), [&](int s, int64_t, int r, int n) {
-    float2 st[V];
+    Pair<ONE> st;
     float o[V];
     Vec<IO, V> v[kAhead];
     pairs.get<false>(q, t, part, ready, s, tile, c, st, stats);
@@ -334,13 +349,13 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const
 
 // ---- backward ----------------------------------------------------------------------------------------
 // part [slots, pieces]: sums of g = w dv and of g n. chan [strips, 2, C]: sums of dv (db), of dv n (dw).
-template <typename IO>
+template <typename IO, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, Cut t, const float2* stats,
                                                            const IO* dy, float2* part, float* chan) {
   __shared__ Columns col;
   const int lane = threadIdx.x & 63, tile = (int)(blockIdx.x % t.tiles);
   const int strip = (int)(blockIdx.x / t.tiles);
-  const int c = min(tile * kTile + lane * V, q.C - V), cg = q.C / q.G;
+  const int c = min(tile * kTile + lane * V, q.C - V);
   const IO* x = (const IO*)q.x + c;
   const IO* d = dy + c;
   const Affine af(q, c);
@@ -348,14 +363,12 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, Cut t, c
 #pragma unroll
   for (int i = 0; i < kTile / kThreads; ++i) db[i] = dw[i] = 0.f;
   parts(q.rows, t, strip, [&](int s, int64_t slot, int r, int n) {
-    float2 st[V];
+    Pair<ONE> st;
     float a[V], b[V];
     Vec<IO, V> v[kAhead], e[kAhead];
+    st.load(q, stats, s, c);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      st[j] = stats[(int64_t)s * q.G + (c + j) / cg];
-      a[j] = b[j] = 0.f;
-    }
+    for (int j = 0; j < V; ++j) a[j] = b[j] = 0.f;
     walk(r, n,
          [&](int k, int row) {
            v[k].load(x + row * q.xs);
@@ -402,7 +415,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, Cut t, c
 
 // dx = rstd (g - mean(g) - n mean(g n)); zero in rows of no sequence. The blocks behind the strips' add
 // up the columns of chan, 64 each, in a fixed order.
-template <typename IO>
+template <typename IO, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, Cut t, const float2* stats,
                                                            const float2* part, const float2* ready,
                                                            const float* chan, const IO* dy, IO* dx,
@@ -430,7 +443,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, Cut t, c
     }
     return;
   }
-  const int tile = (int)(blockIdx.x % t.tiles), strip = (int)(blockIdx.x / t.tiles), cg = q.C / q.G;
+  const int tile = (int)(blockIdx.x % t.tiles), strip = (int)(blockIdx.x / t.tiles);
   const int c0 = tile * kTile + lane * V, c = min(c0, q.C - V);
   const bool live = c0 < q.C;
   const IO* x = (const IO*)q.x + c;
@@ -446,14 +459,13 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, Cut t, c
       for (int i = done + wave; i < to; i += kWaves) store_vec<IO, V>(dx + (int64_t)i * q.C + c, o);
   };
   parts(q.rows, t, strip, [&](int s, int64_t, int r, int n) {
-    float2 st[V], m[V];
+    Pair<ONE> st, m;
     Vec<IO, V> v[kAhead], e[kAhead];
     if (q.rows.starts) {
       clear(r);
       done = r + n;
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) st[j] = stats[(int64_t)s * q.G + (c + j) / cg];
+    st.load(q, stats, s, c);
     pairs.get<true>(q, t, part, ready, s, tile, c, m, nullptr);
     walk(r, n,
          [&](int k, int row) {
@@ -860,6 +872,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_tokens(GroupArgs q, float2* sta
   const int64_t s0 = f.row * NV;
   if (s0 >= q.rows.S) return;  // whole groups
   const int c = f.at * V;
+  const float share = 1.f / cg;
   Vec<IO, V> v[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i].load((const IO*)q.x + min(s0 + i, (int64_t)q.rows.S - 1) * q.xs + c);
@@ -870,13 +883,13 @@ __global__ __launch_bounds__(kThreads) void k_gn_tokens(GroupArgs q, float2* sta
     float sum = 0.f, dev = 0.f, o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) sum += v[i].get(j);
-    const float mean = lanes_sum(sum, vg) / cg;
+    const float mean = lanes_sum(sum, vg) * share;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float d = v[i].get(j) - mean;
       dev = fmaf(d, d, dev);
     }
-    const float rstd = 1.f / sqrtf(lanes_sum(dev, vg) / cg + q.eps);
+    const float rstd = inverse_root(fmaf(lanes_sum(dev, vg), share, q.eps));
     if (stats && f.at % vg == 0) stats[(s0 + i) * q.G + c / cg] = make_float2(mean, rstd);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -895,6 +908,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_tokens_bwd(GroupArgs q, int wal
   const Flat f(q.C / V);
   if (f.row >= walkers) return;
   const int c = f.at * V, g = c / cg;
+  const float share = 1.f / cg;
   const Affine af(q, c);
   float dw[V], db[V];
 #pragma unroll
@@ -925,7 +939,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_tokens_bwd(GroupArgs q, int wal
         a += e[j];
         b = fmaf(e[j], n[j], b);
       }
-      const float m1 = lanes_sum(a, vg) / cg, m2 = lanes_sum(b, vg) / cg;
+      const float m1 = lanes_sum(a, vg) * share, m2 = lanes_sum(b, vg) * share;
 #pragma unroll
       for (int j = 0; j < V; ++j) e[j] = st[i].y * (e[j] - m1 - n[j] * m2);
       store_vec<IO, V>(dx + s * q.C + c, e);
@@ -1025,9 +1039,12 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
                          dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
                          dim3(kThreads), 0, s, a, t, part, ready);
     }
-    hipLaunchKernelGGL((k_gn_apply<IO>), grid, dim3(kThreads), 0, s, a, t, part, ready,
-                       (float2*)stats, (IO*)y);
-    return hipGetLastError();
+    auto apply = [&](auto one) {
+      hipLaunchKernelGGL((k_gn_apply<IO, decltype(one)::value>), grid, dim3(kThreads), 0, s, a, t, part,
+                         ready, (float2*)stats, (IO*)y);
+      return hipGetLastError();
+    };
+    return a.C / a.G % V ? apply(std::false_type{}) : apply(std::true_type{});
   };
   return a.io == kIoBf16 ? run(u16{}) : run(float{});
 }
@@ -1080,17 +1097,21 @@ hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, co
     float* chan = dw || db ? (float*)(mid + up64((int64_t)a.rows.S * a.G)) : nullptr;
     const unsigned blocks = (unsigned)((int64_t)t.strips * t.tiles);
     const unsigned more = chan ? (2 * a.C + 63) / 64 : 0;
-    hipLaunchKernelGGL((k_gn_bwd_parts<IO>), dim3(blocks), dim3(kThreads), 0, s, a, t,
-                       (const float2*)stats, (const IO*)dy, part, chan);
-    if (!adds_itself(a, t, false)) {
-      ready = mid;
-      hipLaunchKernelGGL((k_gn_totals<true>),
-                         dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
-                         dim3(kThreads), 0, s, a, t, part, ready);
-    }
-    hipLaunchKernelGGL((k_gn_bwd_apply<IO>), dim3(blocks + more), dim3(kThreads), 0, s, a, t,
-                       (const float2*)stats, part, ready, chan, (const IO*)dy, (IO*)dx, dw, db);
-    return hipGetLastError();
+    auto passes = [&](auto one) {
+      constexpr bool ONE = decltype(one)::value;
+      hipLaunchKernelGGL((k_gn_bwd_parts<IO, ONE>), dim3(blocks), dim3(kThreads), 0, s, a, t,
+                         (const float2*)stats, (const IO*)dy, part, chan);
+      if (!adds_itself(a, t, false)) {
+        ready = mid;
+        hipLaunchKernelGGL((k_gn_totals<true>),
+                           dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
+                           dim3(kThreads), 0, s, a, t, part, ready);
+      }
+      hipLaunchKernelGGL((k_gn_bwd_apply<IO, ONE>), dim3(blocks + more), dim3(kThreads), 0, s, a, t,
+                         (const float2*)stats, part, ready, chan, (const IO*)dy, (IO*)dx, dw, db);
+      return hipGetLastError();
+    };
+    return a.C / a.G % V ? passes(std::false_type{}) : passes(std::true_type{});
   };
   return a.io == kIoBf16 ? run(u16{}) : run(float{});
 }
