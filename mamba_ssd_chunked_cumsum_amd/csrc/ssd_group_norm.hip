@@ -23,7 +23,6 @@ constexpr int V = 8, kTile = 64 * V, kThreads = 256, kWaves = kThreads / 64;
 constexpr int kBlocks = 512;   // two for each of the card's 256 compute units
 constexpr int kAhead = 4;      // rows of a wave that are loaded together
 constexpr int kHeld = 8;       // tokens that a thread holds
-constexpr int kBlockC = 2048;  // channels of a block that holds whole groups
 
 __device__ __forceinline__ float act_slope(float v) {  // of v sigmoid(v)
   const float s = sigmoid(v);
@@ -487,158 +486,320 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, Cut t, c
 }
 
 // ---- sequences of a few tokens -----------------------------------------------------------------------
-// Dense sequences of up to kHeld tokens, groups of a multiple of 8 up to kBlockC channels: a block
-// takes `groups` whole groups of `seqs` sequences at a time, a thread eight channels and all tokens.
-struct Few {
-  int groups, slices, width, seqs;  // slices of a sequence; threads of a slice
+// Dense sequences of up to kHeld tokens, groups of a multiple of 8 channels. A group's vectors of eight
+// have lanes of their own, `per` of them: the next power of two within a wave, or whole waves, which are
+// then a block; the lanes behind the group's vectors idle. Sums run over lanes, without LDS within a
+// wave, and what a thread needs of weight and bias serves all its tokens. One read and one write: 80
+// groups of 64 channels at 16384 single tokens in bf16 take 62 us (5.4 TB/s), backward 109 (4.6); one
+// group of 5120 takes 84 and 134, of 2048 25 and 46. (A thread for each vector without gaps, and sums
+// over neighbours in LDS: 118 and 335 us for the last.)
+constexpr int kWide = 1024;  // lanes of a group, at most
+struct Lanes {
+  int per, block;
 };
-bool few_tokens(const GroupArgs& a) {
-  const int cg = a.C / a.G;
-  return !a.rows.starts && a.rows.L <= kHeld && cg % V == 0 && cg <= kBlockC;
-}
-Few few_of(const GroupArgs& a) {
-  Few f;
-  const int cg = a.C / a.G;
-  f.groups = kBlockC / cg < a.G ? kBlockC / cg : a.G;
-  f.slices = (a.G + f.groups - 1) / f.groups;
-  f.groups = (a.G + f.slices - 1) / f.slices;  // even slices
-  f.width = f.groups * cg / V;
-  f.seqs = kThreads / f.width;
-  return f;
+Lanes lanes_of(const GroupArgs& a) {
+  const int vg = a.C / a.G / V;
+  Lanes l = {1, kThreads};
+  if (vg > kWave)
+    l.per = l.block = (vg + kWave - 1) / kWave * kWave;
+  else
+    while (l.per < vg) l.per *= 2;
+  return l;
 }
 
-// Sum over a group, whose threads are neighbours: from one value of each.
-__device__ __forceinline__ float group_sum(float v, float* red, int first, int n) {
-  __syncthreads();
-  red[threadIdx.x] = v;
-  __syncthreads();
-  float sum = 0.f;
-  for (int i = 0; i < n; ++i) sum += red[first + i];
-  return sum;
+// The n-th of this launch's threads as (row, group, vector of the group).
+struct Place {
+  int64_t row;
+  int g, at, c;
+  bool live;
+  __device__ __forceinline__ Place(const GroupArgs& q, int per) {
+    const int64_t first = (int64_t)blockIdx.x * blockDim.x;
+    const unsigned width = (unsigned)q.G * per, rest = (unsigned)(first % width) + threadIdx.x;
+    row = first / width + rest / width;
+    g = (int)(rest % width / per);
+    at = (int)(rest % width % per);
+    const int cg = q.C / q.G;
+    live = at * V < cg;
+    c = g * cg + (live ? at * V : 0);
+  }
+};
+
+__device__ __forceinline__ float lanes_sum(float v, int per) {  // per: uniform
+  if (per >= 2) v = add_dpp<0xB1>(v);    // quad_perm [1,0,3,2]
+  if (per >= 4) v = add_dpp<0x4E>(v);    // quad_perm [2,3,0,1]
+  if (per >= 8) v = add_dpp<0x141>(v);   // row_half_mirror
+  if (per >= 16) v = add_dpp<0x140>(v);  // row_mirror
+  if (per >= 32) v += __shfl_xor(v, 16, kWave);
+  if (per >= 64) v += __shfl_xor(v, 32, kWave);
+  return v;
 }
 
-template <typename IO>
-__global__ __launch_bounds__(kThreads) void k_gn_few(GroupArgs q, Few f, float* stats, IO* y) {
-  __shared__ float red[kThreads];
-  const int cg = q.C / q.G, vg = cg / V, L = q.rows.L;
-  const int t = threadIdx.x % f.width, at = threadIdx.x / f.width;
-  const int slice = (int)(blockIdx.x % f.slices);
-  const int64_t s = (int64_t)(blockIdx.x / f.slices) * f.seqs + at;
-  const int c = slice * f.groups * cg + t * V;
-  const bool live = at < f.seqs && s < q.rows.S && c < q.C;
-  const int first = threadIdx.x - t % vg;
-  Vec<IO, V> v[kHeld];
-  float sum = 0.f;
+// Sums of N values over a group's lanes, in each of them. Across waves through LDS, in two halves in
+// turn: who writes one again has passed the other's barrier, behind all that read the first.
+template <bool WIDE, int N>
+struct Group {
+  float of[WIDE ? 2 : 1][WIDE ? kWide / kWave : 1][N];
+  __device__ __forceinline__ void add(float (&v)[N], int per, int half) {
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (i < L) {
-      v[i].zero();
-      if (live) v[i].load((const IO*)q.x + (s * L + i) * q.xs + c);
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum(v[i], WIDE ? kWave : per);
+    if (!WIDE) return;
+    const int waves = per / kWave;
 #pragma unroll
-      for (int j = 0; j < V; ++j) sum += v[i].get(j);
+    for (int i = 0; i < N; ++i)
+      if ((threadIdx.x & 63) == 0) of[half][threadIdx.x / kWave][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+    for (int w = 0; w < waves; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += of[half][w][i];
+  }
+};
+
+// NV sequences of one token a thread. A block of a wide group is one row, so that all of it returns or reaches a barrier.
+template <typename IO, int NV, bool WIDE>
+__global__ __launch_bounds__(WIDE ? kWide : kThreads) void k_gn_tokens(GroupArgs q, int per, float2* stats,
+                                                                       IO* y) {
+  __shared__ Group<WIDE, NV> group;
+  const Place p(q, per);
+  const int64_t s0 = p.row * NV;
+  if (s0 >= q.rows.S) return;  // whole groups
+  const float share = 1.f / (q.C / q.G);
+  Vec<IO, V> v[NV];
+  float mean[NV], rstd[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    v[i].load((const IO*)q.x + min(s0 + i, (int64_t)q.rows.S - 1) * q.xs + p.c);
+  const Affine af(q, p.c);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    mean[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) mean[i] += v[i].get(j);
+    if (!p.live) mean[i] = 0.f;
+  }
+  group.add(mean, per, 0);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    mean[i] *= share;
+    rstd[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = v[i].get(j) - mean[i];
+      rstd[i] = fmaf(d, d, rstd[i]);
     }
-  // (threads past the last slice's groups, and of no sequence, add up zeros of their own)
-  const int n = min(vg, kThreads - first);
-  const float mean = group_sum(sum, red, first, n) / (float)(L * cg);
-  float dev = 0.f;
+    if (!p.live) rstd[i] = 0.f;
+  }
+  group.add(rstd, per, 1);
+  if (!p.live) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (s0 + i >= q.rows.S) break;
+    const float r = inverse_root(fmaf(rstd[i], share, q.eps));
+    if (stats && p.at == 0) stats[(s0 + i) * q.G + p.g] = make_float2(mean[i], r);
+    float o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      o[j] = fmaf((v[i].get(j) - mean[i]) * r, af.w[j], af.b[j]);
+      if (q.act) o[j] *= sigmoid(o[j]);
+    }
+    store_vec<IO, V>(y + (s0 + i) * q.C + p.c, o, q.stream);
+  }
+}
+
+template <typename IO, bool WIDE>
+__global__ __launch_bounds__(WIDE ? kWide : kThreads) void k_gn_few(GroupArgs q, int per, float2* stats,
+                                                                    IO* y) {
+  __shared__ Group<WIDE, 1> group;
+  const Place p(q, per);
+  const int64_t s = p.row;
+  if (s >= q.rows.S) return;
+  const int L = q.rows.L;
+  const float count = (float)(L * (q.C / q.G));
+  Vec<IO, V> v[kHeld];
+  float mean[1] = {0.f}, rstd[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
-    if (i < L) {
+    if (i < L) v[i].load((const IO*)q.x + (s * L + i) * q.xs + p.c);
+  const Affine af(q, p.c);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (i < L && p.live) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) mean[0] += v[i].get(j);
+    }
+  group.add(mean, per, 0);
+  mean[0] /= count;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (i < L && p.live) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float d = v[i].get(j) - mean;
-        dev = fmaf(d, d, dev);
+        const float d = v[i].get(j) - mean[0];
+        rstd[0] = fmaf(d, d, rstd[0]);
       }
     }
-  const float rstd = 1.f / sqrtf(group_sum(dev, red, first, n) / (float)(L * cg) + q.eps);
-  if (!live) return;
-  if (stats && t % vg == 0)
-    reinterpret_cast<float2*>(stats)[s * q.G + c / cg] = make_float2(mean, rstd);
-  const Affine af(q, c);
+  group.add(rstd, per, 1);
+  if (!p.live) return;
+  const float r = inverse_root(rstd[0] / count + q.eps);
+  if (stats && p.at == 0) stats[s * q.G + p.g] = make_float2(mean[0], r);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
     if (i < L) {
       float o[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        o[j] = fmaf((v[i].get(j) - mean) * rstd, af.w[j], af.b[j]);
+        o[j] = fmaf((v[i].get(j) - mean[0]) * r, af.w[j], af.b[j]);
         if (q.act) o[j] *= sigmoid(o[j]);
       }
-      store_vec<IO, V>(y + (s * L + i) * q.C + c, o, q.stream);
+      store_vec<IO, V>(y + (s * L + i) * q.C + p.c, o, q.stream);
     }
 }
 
-// Backward: a block walks sequences and keeps the sums for dw and db of its channels in registers.
-// part [walkers, 2, C]: db, dw.
-template <typename IO>
-__global__ __launch_bounds__(kThreads) void k_gn_few_bwd(GroupArgs q, Few f, int walkers,
-                                                         const float* stats, const IO* dy, IO* dx,
-                                                         float* part) {
-  __shared__ float red[2][kThreads];
-  const int cg = q.C / q.G, vg = cg / V, L = q.rows.L;
-  const int t = threadIdx.x % f.width, at = threadIdx.x / f.width;
-  const int slice = (int)(blockIdx.x % f.slices), walker = (int)(blockIdx.x / f.slices);
-  const int c = slice * f.groups * cg + t * V;
-  const bool mine = at < f.seqs && c < q.C;
-  const int first = threadIdx.x - t % vg, n = min(vg, kThreads - first);
-  const Affine af(q, mine ? c : 0);
+// Backward: a thread walks every walkers-th sequence and keeps the sums for dw and db of its channels in
+// registers. part [walkers, 2, C]: sums of dv (db) and of dv n (dw).
+template <typename IO, int NV, bool WIDE>
+__global__ __launch_bounds__(WIDE ? kWide : kThreads) void k_gn_tokens_bwd(GroupArgs q, int per,
+                                                                           int walkers,
+                                                                           const float2* stats,
+                                                                           const IO* dy, IO* dx,
+                                                                           float* part) {
+  __shared__ Group<WIDE, 2 * NV> group;
+  const Place p(q, per);
+  if (p.row >= walkers) return;
+  const float share = 1.f / (q.C / q.G);
+  const Affine af(q, p.c);
   float dw[V], db[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.f;
-  for (int64_t s0 = (int64_t)walker * f.seqs; s0 < q.rows.S; s0 += (int64_t)walkers * f.seqs) {
-    const int64_t s = s0 + at;
-    const bool live = mine && s < q.rows.S;
-    Vec<IO, V> v[kHeld], d[kHeld];
-    float2 st = make_float2(0.f, 0.f);
+  int half = 0;
+  for (int64_t s0 = p.row; s0 < q.rows.S; s0 += (int64_t)NV * walkers) {
+    Vec<IO, V> v[NV], d[NV];
+    float2 st[NV];
+    float m[2 * NV];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (i < L) {
-        v[i].zero();
-        d[i].zero();
-        if (live) {
-          v[i].load((const IO*)q.x + (s * L + i) * q.xs + c);
-          d[i].load(dy + (s * L + i) * q.C + c);
-        }
+    for (int i = 0; i < NV; ++i) {
+      const int64_t s = min(s0 + (int64_t)i * walkers, (int64_t)q.rows.S - 1);
+      v[i].load((const IO*)q.x + s * q.xs + p.c);
+      d[i].load(dy + s * q.C + p.c);
+      st[i] = stats[s * q.G + p.g];
+    }
+    // the gradient of n, and n: once for the sums and once for dx
+    auto each = [&](int i, auto f) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float n = (v[i].get(j) - st[i].x) * st[i].y;
+        float e = d[i].get(j);
+        if (q.act) e *= act_slope(fmaf(n, af.w[j], af.b[j]));
+        f(j, n, e);
       }
-    if (live) st = reinterpret_cast<const float2*>(stats)[s * q.G + c / cg];
-    float a = 0.f, b = 0.f;
+    };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (i < L) {
+    for (int i = 0; i < NV; ++i) {
+      m[2 * i] = m[2 * i + 1] = 0.f;
+      if (!p.live || s0 + (int64_t)i * walkers >= q.rows.S) continue;
+      each(i, [&](int j, float n, float e) {
+        db[j] += e;
+        dw[j] = fmaf(e, n, dw[j]);
+        e *= af.w[j];
+        m[2 * i] += e;
+        m[2 * i + 1] = fmaf(e, n, m[2 * i + 1]);
+      });
+    }
+    group.add(m, per, half);
+    half ^= 1;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float nv = (v[i].get(j) - st.x) * st.y;
-          float dv = d[i].get(j);
-          if (q.act) dv *= act_slope(fmaf(nv, af.w[j], af.b[j]));
-          db[j] += dv;
-          dw[j] = fmaf(dv, nv, dw[j]);
-          a = fmaf(dv, af.w[j], a);
-          b = fmaf(dv * af.w[j], nv, b);
-        }
-      }
-    const float m1 = group_sum(a, red[0], first, n) / (float)(L * cg);
-    const float m2 = group_sum(b, red[1], first, n) / (float)(L * cg);
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (i < L) {
-          float o[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float nv = (v[i].get(j) - st.x) * st.y;
-            float g = d[i].get(j) * af.w[j];
-            if (q.act) g *= act_slope(fmaf(nv, af.w[j], af.b[j]));
-            o[j] = st.y * (g - m1 - nv * m2);
-          }
-          store_vec<IO, V>(dx + (s * L + i) * q.C + c, o);
-        }
+    for (int i = 0; i < NV; ++i) {
+      const int64_t s = s0 + (int64_t)i * walkers;
+      if (!p.live || s >= q.rows.S) continue;
+      float o[V];
+      each(i, [&](int j, float n, float e) {
+        o[j] = st[i].y * (e * af.w[j] - m[2 * i] * share - n * (m[2 * i + 1] * share));
+      });
+      store_vec<IO, V>(dx + s * q.C + p.c, o);
     }
   }
-  if (mine) {
-    float* p = part + ((int64_t)walker * f.seqs + at) * 2 * q.C + c;
-    store_vec<float, V>(p, db);
-    store_vec<float, V>(p + q.C, dw);
+  if (!p.live) return;
+  float* to = part + p.row * 2 * q.C + p.c;
+  store_vec<float, V>(to, db);
+  store_vec<float, V>(to + q.C, dw);
+}
+
+template <typename IO, bool WIDE>
+__global__ __launch_bounds__(WIDE ? kWide / 2 : kThreads) void k_gn_few_bwd(GroupArgs q, int per,
+                                                                            int walkers,
+                                                                            const float2* stats,
+                                                                            const IO* dy, IO* dx,
+                                                                            float* part) {
+  __shared__ Group<WIDE, 2> group;
+  const Place p(q, per);
+  if (p.row >= walkers) return;
+  const int L = q.rows.L;
+  const float count = (float)(L * (q.C / q.G));
+  const Affine af(q, p.c);
+  float dw[V], db[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.f;
+  int half = 0;
+  for (int64_t s = p.row; s < q.rows.S; s += walkers) {
+    Vec<IO, V> v[kHeld], d[kHeld];
+    float m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < L) {
+        v[i].load((const IO*)q.x + (s * L + i) * q.xs + p.c);
+        d[i].load(dy + (s * L + i) * q.C + p.c);
+      }
+    const float2 st = stats[s * q.G + p.g];
+    auto each = [&](int i, auto f) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float n = (v[i].get(j) - st.x) * st.y;
+        float e = d[i].get(j);
+        if (q.act) e *= act_slope(fmaf(n, af.w[j], af.b[j]));
+        f(j, n, e);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < L && p.live)
+        each(i, [&](int j, float n, float e) {
+          db[j] += e;
+          dw[j] = fmaf(e, n, dw[j]);
+          e *= af.w[j];
+          m[0] += e;
+          m[1] = fmaf(e, n, m[1]);
+        });
+    group.add(m, per, half);
+    half ^= 1;
+    const float m1 = m[0] / count, m2 = m[1] / count;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < L && p.live) {
+        float o[V];
+        each(i, [&](int j, float n, float e) { o[j] = st.y * (e * af.w[j] - m1 - n * m2); });
+        store_vec<IO, V>(dx + (s * L + i) * q.C + p.c, o);
+      }
   }
+  if (!p.live) return;
+  float* to = part + p.row * 2 * q.C + p.c;
+  store_vec<float, V>(to, db);
+  store_vec<float, V>(to + q.C, dw);
+}
+
+bool few_tokens(const GroupArgs& a) {
+  const int cg = a.C / a.G;
+  return !a.rows.starts && a.rows.L <= kHeld && cg % V == 0 &&
+         cg <= V * (a.rows.L == 1 ? kWide : kWide / 2);
+}
+
+// Sequences side by side in the backward pass: 131072 threads, two waves a SIMD (twice as many cost up to
+// 19% more where groups are wide), and at least four tokens each.
+int walkers_of(const GroupArgs& a) {
+  const int64_t turn = 4 / a.rows.L > 1 ? 4 / a.rows.L : 1;
+  const int64_t want = ((int64_t)a.rows.S + turn - 1) / turn;
+  const int64_t most = 131072 / ((int64_t)a.G * lanes_of(a).per);
+  return (int)(want < most ? want : most < 1 ? 1 : most);
 }
 
 // ---- whole sequences in a block ----------------------------------------------------------------------
@@ -834,135 +995,6 @@ __global__ __launch_bounds__(kWhole) void k_gn_whole_bwd(GroupArgs q, Whole w, c
   }
 }
 
-// ---- single tokens -----------------------------------------------------------------------------------
-// Sequences of one token whose groups are 1, 2, 4 .. 64 vectors: the lanes of a group are neighbours in a
-// wave, and a thread takes the same eight channels of NV tokens (backward: of every walkers-th), whose
-// loads it issues together and which share weight and bias. No LDS and no barrier.
-bool single_tokens(const GroupArgs& a) {
-  const int cg = a.C / a.G, vg = cg / V;
-  return !a.rows.starts && a.rows.L == 1 && cg % V == 0 && vg <= 64 && (vg & (vg - 1)) == 0;
-}
-
-__device__ __forceinline__ float lanes_sum(float v, int vg) {  // vg: uniform
-  if (vg >= 2) v = add_dpp<0xB1>(v);    // quad_perm [1,0,3,2]
-  if (vg >= 4) v = add_dpp<0x4E>(v);    // quad_perm [2,3,0,1]
-  if (vg >= 8) v = add_dpp<0x141>(v);   // row_half_mirror
-  if (vg >= 16) v = add_dpp<0x140>(v);  // row_mirror
-  if (vg >= 32) v += __shfl_xor(v, 16, kWave);
-  if (vg >= 64) v += __shfl_xor(v, 32, kWave);
-  return v;
-}
-
-// The n-th of this launch's threads as (row of `width`, place in it).
-struct Flat {
-  int64_t row;
-  int at;
-  __device__ __forceinline__ Flat(int width) {
-    const int64_t first = (int64_t)blockIdx.x * kThreads;
-    const unsigned rest = (unsigned)(first % width) + threadIdx.x;
-    row = first / width + rest / width;
-    at = (int)(rest % width);
-  }
-};
-
-template <typename IO, int NV>
-__global__ __launch_bounds__(kThreads) void k_gn_tokens(GroupArgs q, float2* stats, IO* y) {
-  const int cg = q.C / q.G, vg = cg / V;
-  const Flat f(q.C / V);
-  const int64_t s0 = f.row * NV;
-  if (s0 >= q.rows.S) return;  // whole groups
-  const int c = f.at * V;
-  const float share = 1.f / cg;
-  Vec<IO, V> v[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) v[i].load((const IO*)q.x + min(s0 + i, (int64_t)q.rows.S - 1) * q.xs + c);
-  const Affine af(q, c);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (s0 + i >= q.rows.S) break;
-    float sum = 0.f, dev = 0.f, o[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) sum += v[i].get(j);
-    const float mean = lanes_sum(sum, vg) * share;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float d = v[i].get(j) - mean;
-      dev = fmaf(d, d, dev);
-    }
-    const float rstd = inverse_root(fmaf(lanes_sum(dev, vg), share, q.eps));
-    if (stats && f.at % vg == 0) stats[(s0 + i) * q.G + c / cg] = make_float2(mean, rstd);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      o[j] = fmaf((v[i].get(j) - mean) * rstd, af.w[j], af.b[j]);
-      if (q.act) o[j] *= sigmoid(o[j]);
-    }
-    store_vec<IO, V>(y + (s0 + i) * q.C + c, o, q.stream);
-  }
-}
-
-// part [walkers, 2, C]: sums of dv (db) and of dv n (dw).
-template <typename IO, int NV>
-__global__ __launch_bounds__(kThreads) void k_gn_tokens_bwd(GroupArgs q, int walkers, const float2* stats,
-                                                            const IO* dy, IO* dx, float* part) {
-  const int cg = q.C / q.G, vg = cg / V;
-  const Flat f(q.C / V);
-  if (f.row >= walkers) return;
-  const int c = f.at * V, g = c / cg;
-  const float share = 1.f / cg;
-  const Affine af(q, c);
-  float dw[V], db[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.f;
-  for (int64_t s0 = f.row; s0 < q.rows.S; s0 += (int64_t)NV * walkers) {
-    Vec<IO, V> v[NV], d[NV];
-    float2 st[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t s = min(s0 + (int64_t)i * walkers, (int64_t)q.rows.S - 1);
-      v[i].load((const IO*)q.x + s * q.xs + c);
-      d[i].load(dy + s * q.C + c);
-      st[i] = stats[s * q.G + g];
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t s = s0 + (int64_t)i * walkers;
-      if (s >= q.rows.S) break;
-      float n[V], e[V], a = 0.f, b = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        n[j] = (v[i].get(j) - st[i].x) * st[i].y;
-        e[j] = d[i].get(j);
-        if (q.act) e[j] *= act_slope(fmaf(n[j], af.w[j], af.b[j]));
-        db[j] += e[j];
-        dw[j] = fmaf(e[j], n[j], dw[j]);
-        e[j] *= af.w[j];
-        a += e[j];
-        b = fmaf(e[j], n[j], b);
-      }
-      const float m1 = lanes_sum(a, vg) * share, m2 = lanes_sum(b, vg) * share;
-#pragma unroll
-      for (int j = 0; j < V; ++j) e[j] = st[i].y * (e[j] - m1 - n[j] * m2);
-      store_vec<IO, V>(dx + s * q.C + c, e);
-    }
-  }
-  float* p = part + f.row * 2 * q.C + c;
-  store_vec<float, V>(p, db);
-  store_vec<float, V>(p + q.C, dw);
-}
-
-// Walkers of every vector of channels: 131072 threads, two waves a SIMD, and at least 4 tokens each.
-int token_walkers(const GroupArgs& a) {
-  const int64_t want = ((int64_t)a.rows.S + 3) / 4, most = 131072 / (a.C / V);
-  return (int)(want < most ? want : most < 1 ? 1 : most);
-}
-
-// Blocks of a slice that walk the sequences: at most 1024 in all, at least 4 turns each.
-int walkers_of(const GroupArgs& a, const Few& f) {
-  const int64_t turns = ((int64_t)a.rows.S + f.seqs - 1) / f.seqs;
-  const int64_t want = (turns + 3) / 4, most = 1024 / f.slices;
-  return (int)(want < most ? want : most < 1 ? 1 : most);
-}
-
 int64_t up64(int64_t floats) { return (floats + 63) / 64 * 64; }
 
 // A block of the second pass adds up its groups' pieces by itself up to 16 values a thread. (Sums of
@@ -978,11 +1010,7 @@ bool adds_itself(const GroupArgs& a, const Cut& t, bool stats) {
 
 bool group_norm_fits(const GroupArgs& a) {
   auto fits = [](double blocks) { return blocks * kThreads < 4294967296.0; };
-  if (single_tokens(a)) return fits(double(a.rows.S) * (a.C / V) / kThreads + 1);
-  if (few_tokens(a)) {
-    const Few f = few_of(a);
-    return fits((double(a.rows.S) / f.seqs + 1) * f.slices);
-  }
+  if (few_tokens(a)) return fits(double(a.rows.S) * a.G * lanes_of(a).per / kThreads + 1);
   Whole w;
   if (whole_of(a, &w)) return true;
   const double tiles = a.C / kTile + 1, rows = a.rows.starts ? a.rows.R : a.rows.L;
@@ -993,7 +1021,7 @@ bool group_norm_fits(const GroupArgs& a) {
 
 int64_t group_norm_bytes(const GroupArgs& a) {
   Whole w;
-  if (single_tokens(a) || few_tokens(a) || whole_of(a, &w)) return 0;
+  if (few_tokens(a) || whole_of(a, &w)) return 0;
   const Cut t = cut_of(a);
   return 8 * (up64(t.slots * t.pieces) + (int64_t)a.rows.S * a.G);
 }
@@ -1004,24 +1032,21 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
   a.stream = past_caches((double)a.rows.R * a.C * (a.io == kIoBf16 ? 2 : 4));
   auto run = [&](auto io) {
     using IO = decltype(io);
-    if (single_tokens(a)) {
-      auto go = [&](auto tokens) {
-        constexpr int NV = decltype(tokens)::value;
-        const int64_t n = ((int64_t)a.rows.S + NV - 1) / NV * (a.C / V);
-        hipLaunchKernelGGL((k_gn_tokens<IO, NV>), dim3((unsigned)((n + kThreads - 1) / kThreads)),
-                           dim3(kThreads), 0, s, a, (float2*)stats, (IO*)y);
+    if (few_tokens(a)) {
+      const Lanes l = lanes_of(a);
+      const int64_t lanes = (int64_t)a.G * l.per;
+      // Sequences of one token: four a thread once that leaves four waves a SIMD; two of a wide group
+      // (16384 x 5120 in one group: 84 us; four 100, one 118).
+      const int nv = a.rows.L > 1 || a.rows.S * lanes < 4 * 262144 ? 1 : l.per > kWave ? 2 : 4;
+      const int64_t n = ((int64_t)a.rows.S + nv - 1) / nv * lanes;
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((n + l.block - 1) / l.block)), dim3(l.block), 0, s, a,
+                           l.per, (float2*)stats, (IO*)y);
         return hipGetLastError();
       };
-      // four tokens a thread once that leaves four waves a SIMD
-      if ((int64_t)a.rows.S * (a.C / V) >= 4 * 262144) return go(std::integral_constant<int, 4>{});
-      return go(std::integral_constant<int, 1>{});
-    }
-    if (few_tokens(a)) {
-      const Few f = few_of(a);
-      const int64_t blocks = ((int64_t)a.rows.S + f.seqs - 1) / f.seqs * f.slices;
-      hipLaunchKernelGGL((k_gn_few<IO>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a, f, stats,
-                         (IO*)y);
-      return hipGetLastError();
+      if (a.rows.L > 1) return l.per > kWave ? go(k_gn_few<IO, true>) : go(k_gn_few<IO, false>);
+      if (nv > 1) return l.per > kWave ? go(k_gn_tokens<IO, 2, true>) : go(k_gn_tokens<IO, 4, false>);
+      return l.per > kWave ? go(k_gn_tokens<IO, 1, true>) : go(k_gn_tokens<IO, 1, false>);
     }
     Whole w;
     if (whole_of(a, &w)) {
@@ -1050,11 +1075,7 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
 }
 
 int64_t group_norm_backward_bytes(const GroupArgs& a) {
-  if (single_tokens(a)) return 4 * (int64_t)token_walkers(a) * 2 * a.C;
-  if (few_tokens(a)) {
-    const Few f = few_of(a);
-    return 4 * (int64_t)walkers_of(a, f) * f.seqs * 2 * a.C;
-  }
+  if (few_tokens(a)) return 4 * (int64_t)walkers_of(a) * 2 * a.C;
   Whole w;
   if (whole_of(a, &w)) return 8 * (int64_t)a.rows.S * a.C;
   const Cut t = cut_of(a);
@@ -1065,23 +1086,20 @@ hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, co
                                       float* dw, float* db, float* ws, hipStream_t s) {
   auto run = [&](auto io) {
     using IO = decltype(io);
-    if (single_tokens(a)) {
-      const int w = token_walkers(a);
-      const int64_t n = (int64_t)w * (a.C / V);
-      hipLaunchKernelGGL((k_gn_tokens_bwd<IO, 4>), dim3((unsigned)((n + kThreads - 1) / kThreads)),
-                         dim3(kThreads), 0, s, a, w, (const float2*)stats, (const IO*)dy, (IO*)dx, ws);
-      const hipError_t e = hipGetLastError();
+    if (few_tokens(a)) {
+      const Lanes l = lanes_of(a);
+      const int w = walkers_of(a);
+      const int64_t n = (int64_t)w * a.G * l.per;
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((n + l.block - 1) / l.block)), dim3(l.block), 0, s, a,
+                           l.per, w, (const float2*)stats, (const IO*)dy, (IO*)dx, ws);
+        return hipGetLastError();
+      };
+      const hipError_t e =
+          a.rows.L > 1 ? l.per > kWave ? go(k_gn_few_bwd<IO, true>) : go(k_gn_few_bwd<IO, false>)
+                       : l.per > kWave ? go(k_gn_tokens_bwd<IO, 2, true>) : go(k_gn_tokens_bwd<IO, 4, false>);
       if (e != hipSuccess || !(dw || db)) return e;
       return launch_column_sums(ws, w, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
-    }
-    if (few_tokens(a)) {
-      const Few f = few_of(a);
-      const int w = walkers_of(a, f);
-      hipLaunchKernelGGL((k_gn_few_bwd<IO>), dim3((unsigned)((int64_t)w * f.slices)), dim3(kThreads), 0,
-                         s, a, f, w, stats, (const IO*)dy, (IO*)dx, ws);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess || !(dw || db)) return e;
-      return launch_column_sums(ws, w * f.seqs, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
     }
     Whole whole;
     if (whole_of(a, &whole)) {

@@ -448,6 +448,22 @@ def test_group_norm(lay, io, C, G, pad, act, affine):
     run_group_norm(lay, io, C, G, pad, act, affine)
 
 
+# groups of fewer vectors than lanes, of a wave and one vector more, of several waves, of the widest block
+# and one vector more, for one token and for several; more tokens than one round of threads takes
+@pytest.mark.parametrize("io,C,G", [("bf16", 72, 3), ("f32", 40, 1), ("bf16", 512, 1), ("f32", 1040, 2),
+                                    ("bf16", 4104, 3), ("f32", 4096, 1), ("bf16", 4104, 1),
+                                    ("f32", 8192, 1), ("bf16", 8200, 1)])
+@pytest.mark.parametrize("lay", [dict(batch=3, L=1), dict(batch=7, L=5), dict(batch=2, L=8),
+                                 dict(batch=2, L=9)], ids=name_of)
+def test_group_norm_of_a_few_tokens(lay, io, C, G):
+    run_group_norm(lay, io, C, G, 8, True, "both")
+
+
+@pytest.mark.parametrize("tokens,C,G", [(1031, 8192, 8), (2051, 4096, 1), (9001, 1000, 25), (33001, 24, 3)])
+def test_group_norm_of_many_single_tokens(tokens, C, G):
+    run_group_norm(dict(batch=tokens, L=1), "bf16", C, G, 0, False, "both")
+
+
 @pytest.mark.parametrize("lay", [dict(batch=5, L=2), dict(batch=2, L=200), dict(lens=[90, 3, 40], spare=5)],
                          ids=name_of)
 def test_group_norm_of_values_far_from_zero(lay):
