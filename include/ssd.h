@@ -440,8 +440,10 @@ ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* resi
  * channels. Tokens, strides, alignment, arithmetic, workspaces and errors as for the operators around
  * the scan above, and their limits; of launches below 2^32 threads: the recurrence takes rows (dense:
  * of sequences rounded up to 28) times channels / 128 (fp32: / 64), rounded up, below 2^28, the
- * rotation rows times ngroups / 4 and nfreq / 4 + (dstate - 2 nfreq) / 8 below 2^32, the group norm
- * sequences times ngroups below 2^26 where a sequence may have more than 8 tokens. */
+ * rotation rows times ngroups / 4 and nfreq / 4 (fp32 in pairs: / 2) + (dstate - 2 nfreq) / 8 below 2^32,
+ * the group norm sequences times ngroups below 2^26 where a sequence may have more than 8 tokens, and
+ * otherwise sequences times ngroups times a group's channels / 8, rounded up to a power of two (past 64:
+ * to a multiple of 64), below 2^32. */
 
 /* Gated linear recurrence. For every channel of each sequence, with v = sigmoid(input_gate) x (x where
  * input_gate is NULL):
