@@ -308,6 +308,12 @@ __global__ __launch_bounds__(256) void k_rec_clear(Chain chain, int64_t n) {
   if (id < n) chain.slots[id] = kEmpty;
 }
 
+// One pass: each element is read once. 2 x 8192 x 5120 bf16 with gates and decay takes 160 us (4.2 TB/s; the
+// bytes alone 129 at a large copy's rate, the same loads and stores without the arithmetic 138, which
+// keeps the vector units busy for 90 of them); 5003 packed x 1536 takes 25. Two passes over the rows with
+// a chain between took 319 and 53. Without gain: 8, 10 or 12 rows a wave, 8 bytes a lane, chunks of one
+// sequence next to one another in the grid, end states handed on every 4 (16 or 32: more registers,
+// slower), and rows of the tensors loaded in turn.
 // CHAIN: sequences of several chunks. A block belongs to a tile and sequence and takes the next chunk of
 // them by a ticket. It waits only for chunks before its own, whose blocks have lower tickets: those are
 // running or done, and the first of them waits for none, so every wait ends.
@@ -627,7 +633,9 @@ __global__ __launch_bounds__(64 * X::W) void k_rec_sums(RecArgs q, Plan pl, int 
 
 // Second pass (or the only one): the gradients; part [units, C]: each block's sums for ddecay. Forward
 // through the rows, then back; what the way back needs of the way forward stays in registers, the
-// gates by their exponentials, from which both sides of a sigmoid come exactly.
+// gates by their exponentials, from which both sides of a sigmoid come exactly. 2 x 4096 x 5120 bf16 with
+// gates and decay: first pass 72 us, chain 10, this one 115 to 120, sums for ddecay 5; the bytes read and
+// written once take 113, and this pass alone moves them all. 4 x 2048 x 768 fp32 without: 15, 4, 20.
 template <typename X, typename IO, bool DECAY, bool GATED, bool PACKED>
 __global__ __launch_bounds__(64 * X::W, 4) void k_rec_bwd(
     RecArgs q, Plan pl, int tiles, Sums sums, int chained, const IO* __restrict__ dy,
@@ -810,8 +818,8 @@ __global__ __launch_bounds__(64 * X::W, 4) void k_rec_bwd(
 }
 
 // ---- single token ----------------------------------------------------------------------------------
-// Four channels of a sequence a thread: bound by the launch and, for large batches, by the state read
-// and written once.
+// Four channels of a sequence a thread: bound by the launch (64 x 2560 bf16: 3 us) and, for large batches,
+// by the state read and written once.
 template <typename IO, bool DECAY, bool GATED>
 __global__ __launch_bounds__(256) void k_rec_step(RecArgs q, float* state_out, IO* y) {
   const int per = q.C / 4;
