@@ -33,6 +33,8 @@ struct Tall { static constexpr int T = 16, W = 16, B = 4; };  // forward where t
 // As many rows as fit 128 registers (eight of bf16 would take 134).
 struct Bwd { static constexpr int T = 7, W = 4, B = 4; };
 struct Bwd32 { static constexpr int T = 12, W = 4, B = 4; };
+struct BwdTall { static constexpr int T = 7, W = 16, B = 4; };  // where that is one chunk a sequence
+struct BwdTall32 { static constexpr int T = 12, W = 16, B = 4; };
 template <typename IO, typename X>
 constexpr int kV = X::B / (int)sizeof(IO);  // channels of a lane
 
@@ -858,10 +860,17 @@ hipError_t by_kind(const RecArgs& a, F f) {
   return a.io == kIoBf16 ? decays(u16{}) : decays(float{});
 }
 
-// The backward's shape and plan.
+// The backward's shape and plan: f(shape, plan). Sixteen waves where they hold a whole sequence (packed:
+// all rows) and four do not: the rows are read once, and there is no first pass and no chain (87 x 104 bf16 28 -> 18 us,
+// 64 x 100 x 5120 222 -> 141, 256 x 30 x 5120 421 -> 151).
+template <typename Low, typename High, typename F>
+auto by_height(const RecArgs& a, F f) {
+  const Plan low = plan<Low>(a.rows), high = plan<High>(a.rows);
+  return low.chunks > 1 && high.chunks == 1 ? f(High{}, high) : f(Low{}, low);
+}
 template <typename F>
 auto by_shape(const RecArgs& a, F f) {
-  return a.io == kIoBf16 ? f(Bwd{}, plan<Bwd>(a.rows)) : f(Bwd32{}, plan<Bwd32>(a.rows));
+  return a.io == kIoBf16 ? by_height<Bwd, BwdTall>(a, f) : by_height<Bwd32, BwdTall32>(a, f);
 }
 
 template <typename X>
@@ -949,7 +958,7 @@ hipError_t launch_recurrence_step(const RecArgs& a, float* state_out, void* y, h
 
 int64_t recurrence_backward_bytes(const RecArgs& a) {
   const Plan p = by_shape(a, [](auto, Plan b) { return b; });
-  return 4 * sum_floats(a, p) * ((p.chunks > 1 ? 3 : 0) + (a.decay ? 1 : 0));
+  return 4 * sum_floats(a, p) * ((p.chunks > 1 ? 3 : 0) + (a.decay && p.units > 1 ? 1 : 0));
 }
 
 hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, const float* dfinal,
@@ -960,7 +969,7 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
   const int tiles = tiles_of<Bwd>(a), chained = p.chunks > 1;
   const int64_t n = sum_floats(a, p);
   Sums sums{nullptr, nullptr, nullptr};
-  float* part = ws;
+  float* part = p.units > 1 ? ws : g.ddecay;  // of a single unit its sums are all
   if (chained) {
     sums = Sums{ws, ws + n, ws + 2 * n};
     part = ws + 3 * n;
@@ -968,19 +977,26 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
   const unsigned blocks = (unsigned)((int64_t)tiles * p.units), more = empty_blocks(a, p, g.dh0);
   const hipError_t e = by_kind(a, [&](auto io, auto decay, auto gated, auto packed) {
     using IO = decltype(io);
-    using X = std::conditional_t<sizeof(IO) == 2, Bwd, Bwd32>;
     constexpr bool D = decltype(decay)::value, G = decltype(gated)::value, K = decltype(packed)::value;
-    if (chained) {
-      hipLaunchKernelGGL((k_rec_sums<X, IO, D, G, K>), dim3(blocks), dim3(threads_of(p)), 0, s, a, p,
-                         tiles, sums, (const IO*)dy, dfinal);
-      hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(64 * kParts), 0, s, a, p, sums, dfinal);
-    }
-    hipLaunchKernelGGL((k_rec_bwd<X, IO, D, G, K>), dim3(blocks + more), dim3(threads_of(p)), 0, s, a,
-                       p, tiles, sums, chained, (const IO*)dy, dfinal, (IO*)g.dx, (IO*)g.dg,
-                       (IO*)g.dgi, g.dh0, part);
-    return hipGetLastError();
+    constexpr bool half = sizeof(IO) == 2;
+    using Low = std::conditional_t<half, Bwd, Bwd32>;
+    using High = std::conditional_t<half, BwdTall, BwdTall32>;
+    return by_height<Low, High>(a, [&](auto shape, Plan) {
+      using X = decltype(shape);
+      if constexpr (std::is_same_v<X, Low>) {
+        if (chained) {
+          hipLaunchKernelGGL((k_rec_sums<X, IO, D, G, K>), dim3(blocks), dim3(threads_of(p)), 0, s, a, p,
+                             tiles, sums, (const IO*)dy, dfinal);
+          hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(64 * kParts), 0, s, a, p, sums, dfinal);
+        }
+      }
+      hipLaunchKernelGGL((k_rec_bwd<X, IO, D, G, K>), dim3(blocks + more), dim3(threads_of(p)), 0, s, a,
+                         p, tiles, sums, chained, (const IO*)dy, dfinal, (IO*)g.dx, (IO*)g.dg,
+                         (IO*)g.dgi, g.dh0, part);
+      return hipGetLastError();
+    });
   });
-  if (e != hipSuccess || !a.decay) return e;
+  if (e != hipSuccess || !a.decay || p.units == 1) return e;
   return launch_column_sums(part, p.units, a.C, g.ddecay, a.C, 0, 1, 0, nullptr, 0, nullptr, s);
 }
 

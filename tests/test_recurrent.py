@@ -100,6 +100,19 @@ def test_recurrence(lay, io, C, pad, decay, gated, init):
     run_recurrence(lay, io, C, pad, decay, gated, init)
 
 
+# around the backward's blocks: four waves of 7 (fp32 12) rows, sixteen, several sequences in one
+@pytest.mark.parametrize("io,lay", [
+    ("bf16", dict(batch=1, L=28)), ("bf16", dict(batch=1, L=29)), ("bf16", dict(batch=7, L=29)),
+    ("bf16", dict(batch=3, L=112)), ("bf16", dict(batch=1, L=113)), ("f32", dict(batch=1, L=48)),
+    ("f32", dict(batch=5, L=49)), ("f32", dict(batch=1, L=192)), ("f32", dict(batch=2, L=193)),
+    ("bf16", dict(lens=[40, 0, 1, 60], spare=11)), ("bf16", dict(lens=[40, 0, 1, 60], spare=12)),
+    ("f32", dict(lens=[0, 99, 93], spare=0)), ("f32", dict(lens=[0, 99, 94], spare=0))],
+    ids=lambda v: v if isinstance(v, str) else name_of(v))
+@pytest.mark.parametrize("decay,gated", [(True, True), (False, False)])
+def test_recurrence_of_one_block(io, lay, decay, gated):
+    run_recurrence(lay, io, 136, 8, decay, gated, True)
+
+
 @pytest.mark.parametrize("io,decay,lay", [
     ("f32", True, dict(batch=1, L=5000)), ("bf16", False, dict(batch=2, L=3000)),
     ("f32", True, dict(lens=[1700, 0, 1, 2650, 300], spare=33))])

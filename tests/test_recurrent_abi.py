@@ -108,8 +108,10 @@ def test_recurrence_step_rejects(kw):
 @pytest.mark.parametrize("kw", [
     dict(dy=None), dict(dx=None), dict(dg=None), dict(di=None), dict(dd=None),
     dict(input_gate=None), dict(decay=None), dict(dx=addr(0)), dict(dg=addr(9)), dict(dd=addr(3)),
-    dict(dh=addr(8)), dict(ws=None), dict(n=16), dict(ws=addr(10)), dict(df=addr(8, 4)),
-    dict(dy=addr(7, 8)), dict(sharpness=0.0)])
+    dict(dh=addr(8)), dict(df=addr(8, 4)), dict(dy=addr(7, 8)), dict(sharpness=0.0),
+    # (rows of several chunks need a workspace)
+    dict(t=tokens(seqlen=5000), ws=None), dict(t=tokens(seqlen=5000), n=16),
+    dict(t=tokens(seqlen=5000), ws=addr(10))])
 def test_recurrence_backward_rejects(kw):
     assert Recurrence(**kw).backward() == INVALID
 
