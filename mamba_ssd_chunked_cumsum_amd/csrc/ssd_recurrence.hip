@@ -29,7 +29,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Rows of a wave (at most 31), waves of a block, bytes of a lane: of the forward, and of the backward's
 // two passes (bf16, fp32).
 struct Fwd { static constexpr int T = 16, W = 8, B = 4; };
-struct Tall { static constexpr int T = 16, W = 16, B = 4; };  // forward where that is one block a unit
+struct Tall { static constexpr int T = 16, W = 16, B = 4; };  // forward: see tall()
 // As many rows as fit 128 registers (eight of bf16 would take 134).
 struct Bwd { static constexpr int T = 7, W = 4, B = 4; };
 struct Bwd32 { static constexpr int T = 12, W = 4, B = 4; };
@@ -884,13 +884,14 @@ int64_t sum_floats(const RecArgs& a, const Plan& p) {
 int64_t counters_of(const RecArgs& a) {
   return (int64_t)tiles_of<Fwd>(a) * (a.rows.starts ? 1 : a.rows.S);
 }
-// Blocks of sixteen waves where all of them run at once, one a compute unit: half as many chunks wait for
-// one another (5003 packed x 1536 bf16: 28 -> 25 us; with more blocks than that, 2 x 8192 x 5120, two of
-// eight waves a unit overlap better: 160 against 187 us).
+// Blocks of sixteen waves where they hold a whole sequence and eight do not (200 x 104 bf16 18 -> 14 us,
+// 64 x 256 x 5120 157 -> 148), and where all of them run at once, one a compute unit: half as many chunks
+// wait for one another (5003 packed x 1536 bf16: 28 -> 25 us; with more blocks than that, 2 x 8192 x 5120,
+// two of eight waves a unit overlap better: 160 against 187 us).
 bool tall(const RecArgs& a) {
-  const Plan p = plan<Tall>(a.rows);
-  return p.chunks > 1 && (int64_t)tiles_of<Tall>(a) * p.units <= 256 &&
-         (int64_t)tiles_of<Fwd>(a) * plan<Fwd>(a.rows).units > 256;
+  const Plan p = plan<Tall>(a.rows), f = plan<Fwd>(a.rows);
+  if (f.chunks == 1 || p.chunks == 1) return f.chunks > 1;
+  return (int64_t)tiles_of<Tall>(a) * p.units <= 256 && (int64_t)tiles_of<Fwd>(a) * f.units > 256;
 }
 dim3 chain_grid(const RecArgs& a) {  // both directions
   const int64_t n = (a.rows.starts ? 1 : (int64_t)a.rows.S) * a.C;
@@ -941,8 +942,8 @@ hipError_t launch_recurrence(const RecArgs& given, void* y, float* fin, float* w
                          fin);
       return hipGetLastError();
     };
-    if (high) return run(Tall{}, std::true_type{});
-    return p.chunks > 1 ? run(Fwd{}, std::true_type{}) : run(Fwd{}, std::false_type{});
+    if (p.chunks > 1) return high ? run(Tall{}, std::true_type{}) : run(Fwd{}, std::true_type{});
+    return high ? run(Tall{}, std::false_type{}) : run(Fwd{}, std::false_type{});
   });
 }
 

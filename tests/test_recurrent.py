@@ -100,13 +100,16 @@ def test_recurrence(lay, io, C, pad, decay, gated, init):
     run_recurrence(lay, io, C, pad, decay, gated, init)
 
 
-# around the backward's blocks: four waves of 7 (fp32 12) rows, sixteen, several sequences in one
+# around the backward's blocks: four waves of 7 (fp32 12) rows, sixteen, several sequences in one; and the
+# forward's: sixteen waves of 16 rows
 @pytest.mark.parametrize("io,lay", [
     ("bf16", dict(batch=1, L=28)), ("bf16", dict(batch=1, L=29)), ("bf16", dict(batch=7, L=29)),
     ("bf16", dict(batch=3, L=112)), ("bf16", dict(batch=1, L=113)), ("f32", dict(batch=1, L=48)),
     ("f32", dict(batch=5, L=49)), ("f32", dict(batch=1, L=192)), ("f32", dict(batch=2, L=193)),
     ("bf16", dict(lens=[40, 0, 1, 60], spare=11)), ("bf16", dict(lens=[40, 0, 1, 60], spare=12)),
-    ("f32", dict(lens=[0, 99, 93], spare=0)), ("f32", dict(lens=[0, 99, 94], spare=0))],
+    ("f32", dict(lens=[0, 99, 93], spare=0)), ("f32", dict(lens=[0, 99, 94], spare=0)),
+    ("bf16", dict(batch=3, L=256)), ("f32", dict(batch=2, L=257)),
+    ("bf16", dict(lens=[100, 0, 150], spare=6)), ("f32", dict(lens=[100, 0, 150], spare=7))],
     ids=lambda v: v if isinstance(v, str) else name_of(v))
 @pytest.mark.parametrize("decay,gated", [(True, True), (False, False)])
 def test_recurrence_of_one_block(io, lay, decay, gated):
