@@ -813,11 +813,18 @@ template <typename IO>
 constexpr int kRows = sizeof(IO) == 2 ? 8 : 4;  // tokens of a thread
 struct Whole {
   int groups, slices, width, par;  // slices of a sequence; threads of a token; tokens side by side
+  bool deep;
 };
-bool whole_of(const GroupArgs& a, Whole* w) {
-  const int cg = a.C / a.G, vg = cg / V, held = a.io == kIoBf16 ? kRows<u16> : kRows<float>;
+// Deep blocks hold twice as many tokens a thread: in the forward, where no more of them than compute units
+// take the call (235 packed in 19 sequences x 832 fp32 28 -> 10 us, 8 x 700 x 2560 bf16 22 -> 21; 16 x 800 x
+// 2560 without that limit 41 -> 43; backward, 1 x 700 x 2560 bf16, 18 -> 28).
+bool whole_of(const GroupArgs& a, bool forward, Whole* w) {
+  const int cg = a.C / a.G, vg = cg / V;
+  int held = a.io == kIoBf16 ? kRows<u16> : kRows<float>;
   if (cg % V || vg > kWhole) return false;
   const int64_t fit = a.rows.starts ? a.rows.R : a.rows.L, seqs = a.rows.S;
+  w->deep = forward && fit > (int64_t)held * (kWhole / vg) && seqs * a.G <= 256;
+  if (w->deep) held *= 2;
   if (fit > (int64_t)held * (kWhole / vg) || seqs * a.G > 65536) return false;
   int64_t groups = (int64_t)held * kWhole / (fit * vg);  // of a block, at most
   const int64_t most = kWhole / vg, spread = (seqs * a.G + 255) / 256;  // a block each compute unit
@@ -888,9 +895,8 @@ struct Shares {
   }
 };
 
-template <typename IO>
+template <typename IO, int K>
 __global__ __launch_bounds__(kWhole) void k_gn_whole(GroupArgs q, Whole w, float2* stats, IO* y) {
-  constexpr int K = kRows<IO>;
   __shared__ Shares shares;
   const int cg = q.C / q.G, vg = cg / V;
   const Part p(q, w);
@@ -1012,7 +1018,7 @@ bool group_norm_fits(const GroupArgs& a) {
   auto fits = [](double blocks) { return blocks * kThreads < 4294967296.0; };
   if (few_tokens(a)) return fits(double(a.rows.S) * a.G * lanes_of(a).per / kThreads + 1);
   Whole w;
-  if (whole_of(a, &w)) return true;
+  if (whole_of(a, false, &w)) return true;
   const double tiles = a.C / kTile + 1, rows = a.rows.starts ? a.rows.R : a.rows.L;
   const double strips = (rows / 16 + 1) * (a.rows.starts ? 1 : a.rows.S);
   return fits(strips * tiles + a.C) && fits(double(a.rows.S) * a.G / kWaves + 1) &&
@@ -1021,7 +1027,7 @@ bool group_norm_fits(const GroupArgs& a) {
 
 int64_t group_norm_bytes(const GroupArgs& a) {
   Whole w;
-  if (few_tokens(a) || whole_of(a, &w)) return 0;
+  if (few_tokens(a) || whole_of(a, true, &w)) return 0;
   const Cut t = cut_of(a);
   return 8 * (up64(t.slots * t.pieces) + (int64_t)a.rows.S * a.G);
 }
@@ -1049,10 +1055,13 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
       return l.per > kWave ? go(k_gn_tokens<IO, 1, true>) : go(k_gn_tokens<IO, 1, false>);
     }
     Whole w;
-    if (whole_of(a, &w)) {
-      hipLaunchKernelGGL((k_gn_whole<IO>), dim3((unsigned)(a.rows.S * w.slices)), dim3(kWhole), 0, s, a,
-                         w, (float2*)stats, (IO*)y);
-      return hipGetLastError();
+    if (whole_of(a, true, &w)) {
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(a.rows.S * w.slices)), dim3(kWhole), 0, s, a, w,
+                           (float2*)stats, (IO*)y);
+        return hipGetLastError();
+      };
+      return w.deep ? go(k_gn_whole<IO, 2 * kRows<IO>>) : go(k_gn_whole<IO, kRows<IO>>);
     }
     const Cut t = cut_of(a);
     float2 *part = (float2*)ws, *ready = nullptr;
@@ -1077,7 +1086,7 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
 int64_t group_norm_backward_bytes(const GroupArgs& a) {
   if (few_tokens(a)) return 4 * (int64_t)walkers_of(a) * 2 * a.C;
   Whole w;
-  if (whole_of(a, &w)) return 8 * (int64_t)a.rows.S * a.C;
+  if (whole_of(a, false, &w)) return 8 * (int64_t)a.rows.S * a.C;
   const Cut t = cut_of(a);
   return 8 * (up64(t.slots * t.pieces) + up64((int64_t)a.rows.S * a.G) + (int64_t)t.strips * a.C);
 }
@@ -1102,7 +1111,7 @@ hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, co
       return launch_column_sums(ws, w, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
     }
     Whole whole;
-    if (whole_of(a, &whole)) {
+    if (whole_of(a, false, &whole)) {
       hipLaunchKernelGGL((k_gn_whole_bwd<IO>), dim3((unsigned)(a.rows.S * whole.slices)), dim3(kWhole),
                          0, s, a, whole, (const float2*)stats, (const IO*)dy, (IO*)dx,
                          dw || db ? ws : nullptr);
