@@ -932,10 +932,11 @@ __global__ __launch_bounds__(kWhole) void k_gn_whole(GroupArgs q, Whole w, float
   });
 }
 
-// chan [S, 2, C]: sums of dv (db), of dv n (dw) (null: not wanted).
+// Sums of dv and of dv n of sequence s to db + s step and dw + s step (each null: not wanted).
 template <typename IO>
 __global__ __launch_bounds__(kWhole) void k_gn_whole_bwd(GroupArgs q, Whole w, const float2* stats,
-                                                         const IO* dy, IO* dx, float* chan) {
+                                                         const IO* dy, IO* dx, float* db_out,
+                                                         float* dw_out, int64_t step) {
   constexpr int K = kRows<IO>;
   __shared__ Shares shares;
   __shared__ __attribute__((aligned(16))) float cols[kWhole * V];
@@ -987,16 +988,19 @@ __global__ __launch_bounds__(kWhole) void k_gn_whole_bwd(GroupArgs q, Whole w, c
     for (int64_t r = (int64_t)p.end + p.at; p.mine && r < to; r += w.par)
       store_vec<IO, V>(dx + r * q.C + p.c, o);
   }
-  if (!chan) return;
+  const int rows = min(w.par, p.end - p.begin);  // threads of a channel that took any
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
+    float* to = which ? dw_out : db_out;
+    if (!to) continue;
     __syncthreads();
     store_vec<float, V>(cols + threadIdx.x * V, which ? dw : db);
     __syncthreads();
     for (int i = threadIdx.x; i < w.width * V && p.c_slice + i < q.C; i += kWhole) {
       float sum = 0.f;
-      for (int r = 0; r < w.par; ++r) sum += cols[r * w.width * V + i];
-      chan[((int64_t)p.s * 2 + which) * q.C + p.c_slice + i] = sum;
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r) sum += cols[r * w.width * V + i];
+      to[p.s * step + p.c_slice + i] = sum;
     }
   }
 }
@@ -1086,7 +1090,7 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
 int64_t group_norm_backward_bytes(const GroupArgs& a) {
   if (few_tokens(a)) return 4 * (int64_t)walkers_of(a) * 2 * a.C;
   Whole w;
-  if (whole_of(a, false, &w)) return 8 * (int64_t)a.rows.S * a.C;
+  if (whole_of(a, false, &w)) return a.rows.S > 1 ? 8 * (int64_t)a.rows.S * a.C : 0;
   const Cut t = cut_of(a);
   return 8 * (up64(t.slots * t.pieces) + up64((int64_t)a.rows.S * a.G) + (int64_t)t.strips * a.C);
 }
@@ -1112,11 +1116,12 @@ hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, co
     }
     Whole whole;
     if (whole_of(a, false, &whole)) {
+      const bool add = a.rows.S > 1 && (dw || db);  // else they are the only sequence's
       hipLaunchKernelGGL((k_gn_whole_bwd<IO>), dim3((unsigned)(a.rows.S * whole.slices)), dim3(kWhole),
-                         0, s, a, whole, (const float2*)stats, (const IO*)dy, (IO*)dx,
-                         dw || db ? ws : nullptr);
+                         0, s, a, whole, (const float2*)stats, (const IO*)dy, (IO*)dx, add ? ws : db,
+                         add ? ws + a.C : dw, 2 * (int64_t)a.C);
       const hipError_t e = hipGetLastError();
-      if (e != hipSuccess || !(dw || db)) return e;
+      if (e != hipSuccess || !add) return e;
       return launch_column_sums(ws, a.rows.S, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
     }
     const Cut t = cut_of(a);
