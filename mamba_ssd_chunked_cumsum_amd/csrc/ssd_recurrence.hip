@@ -861,12 +861,14 @@ hipError_t by_kind(const RecArgs& a, F f) {
 }
 
 // The backward's shape and plan: f(shape, plan). Sixteen waves where they hold a whole sequence (packed:
-// all rows) and four do not: the rows are read once, and there is no first pass and no chain (87 x 104 bf16 28 -> 18 us,
+// all rows) and four do not: the rows are read once, and there is no first pass and no chain; and where they
+// hold the whole call, whose sums for ddecay then need no launch of their own (8 x 3 x 280 bf16 23 -> 19 us; 87 x 104 bf16 28 -> 18 us,
 // 64 x 100 x 5120 222 -> 141, 256 x 30 x 5120 421 -> 151).
 template <typename Low, typename High, typename F>
 auto by_height(const RecArgs& a, F f) {
   const Plan low = plan<Low>(a.rows), high = plan<High>(a.rows);
-  return low.chunks > 1 && high.chunks == 1 ? f(High{}, high) : f(Low{}, low);
+  const bool one = high.units == 1 && low.units > 1;
+  return high.chunks == 1 && (low.chunks > 1 || one) ? f(High{}, high) : f(Low{}, low);
 }
 template <typename F>
 auto by_shape(const RecArgs& a, F f) {
