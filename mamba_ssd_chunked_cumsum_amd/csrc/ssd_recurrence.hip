@@ -633,6 +633,10 @@ __global__ __launch_bounds__(64 * X::W) void k_rec_sums(RecArgs q, Plan pl, int 
   }
 }
 
+// How a chunk of the second pass finds what enters it: it is the only one; from the chain; or from the sums
+// of the others.
+enum { kAlone, kJoined, kSingly };
+
 // Second pass (or the only one): the gradients; part [units, C]: each block's sums for ddecay. Forward
 // through the rows, then back; what the way back needs of the way forward stays in registers, the
 // gates by their exponentials, from which both sides of a sigmoid come exactly. 2 x 4096 x 5120 bf16 with
@@ -666,6 +670,24 @@ __global__ __launch_bounds__(64 * X::W, 4) void k_rec_bwd(
     sx.next(rx[i], off);
     sd.next(rd[i], off);
   });
+  float cl[V], e[V];  // c of the row to the right; the state that enters
+  auto alone = [&](int j) {
+    const int64_t so = (int64_t)at.s * q.C + c + j;
+    e[j] = !PACKED && q.h0 ? q.h0[so] : 0.f, cl[j] = !PACKED && dfinal ? dfinal[so] : 0.f;
+  };
+  const int64_t o = (int64_t)at.unit * q.C + c;
+  if (chained == kSingly) {
+    const int chunk = PACKED ? at.unit : at.unit % pl.chunks;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      alone(j);
+#pragma unroll 4
+      for (int u = -chunk; u < 0; ++u) e[j] = enter(sums.P[o + u * q.C + j], sums.H[o + u * q.C + j], e[j]);
+#pragma unroll 4
+      for (int u = pl.chunks - 1 - chunk; u > 0; --u)
+        cl[j] = enter(sums.P[o + u * q.C + j], sums.G[o + u * q.C + j], cl[j]);
+    }
+  }
   Marks mk;
   if (PACKED && at.n > 0) mk.find(q.rows, at.first, at.n);
   const bool plain = at.n == T && (!PACKED || mk.plain);
@@ -727,13 +749,10 @@ __global__ __launch_bounds__(64 * X::W, 4) void k_rec_bwd(
 #pragma unroll
   for (int j = 0; j < V; ++j) sum[j] = 0.f;
   if (at.n > 0) {
-    float cl[V], e[V];  // c of the row to the right; the state that enters
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int64_t o = (int64_t)at.unit * q.C + c + j, so = (int64_t)at.s * q.C + c + j;
-      e[j] = cl[j] = 0.f;
-      if (chained) e[j] = sums.H[o], cl[j] = sums.G[o];
-      else if (!PACKED) e[j] = q.h0 ? q.h0[so] : 0.f, cl[j] = dfinal ? dfinal[so] : 0.f;
+      if (chained == kJoined) e[j] = sums.H[o + j], cl[j] = sums.G[o + j];
+      if (chained == kAlone) alone(j);
       for (int w = at.lo; w < at.wave; ++w) {
         const float2 t = runs[w][j][lane];
         e[j] = enter(t.x, t.y, e[j]);
@@ -969,7 +988,12 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
   RecArgs a = given;
   a.stream = stream_of(a);
   const Plan p = by_shape(a, [](auto, Plan b) { return b; });
-  const int tiles = tiles_of<Bwd>(a), chained = p.chunks > 1;
+  const int tiles = tiles_of<Bwd>(a);
+  // Chunks that look up the others' sums by themselves: few of them (32 x 128 x 5120 bf16 138 -> 119 us), or
+  // some more where all run at once and a launch counts (400 x 1536 28 -> 24; with 24 chunks and more
+  // blocks, 8 x 670 x 5120, 147 -> 191).
+  const bool few = p.chunks <= 8 || (p.chunks <= 24 && (int64_t)tiles * p.units <= 1024);
+  const int chained = p.chunks == 1 ? kAlone : few ? kSingly : kJoined;
   const int64_t n = sum_floats(a, p);
   Sums sums{nullptr, nullptr, nullptr};
   float* part = p.units > 1 ? ws : g.ddecay;  // of a single unit its sums are all
@@ -990,7 +1014,8 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
         if (chained) {
           hipLaunchKernelGGL((k_rec_sums<X, IO, D, G, K>), dim3(blocks), dim3(threads_of(p)), 0, s, a, p,
                              tiles, sums, (const IO*)dy, dfinal);
-          hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(64 * kParts), 0, s, a, p, sums, dfinal);
+          if (chained == kJoined)
+            hipLaunchKernelGGL(k_rec_chain, chain_grid(a), dim3(64 * kParts), 0, s, a, p, sums, dfinal);
         }
       }
       hipLaunchKernelGGL((k_rec_bwd<X, IO, D, G, K>), dim3(blocks + more), dim3(threads_of(p)), 0, s, a,
