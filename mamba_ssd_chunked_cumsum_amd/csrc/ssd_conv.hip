@@ -425,9 +425,10 @@ hipError_t by_width(int W, F f) {
 
 hipError_t launch_conv(const ConvArgs& given, void* fin, hipStream_t s) {
   ConvArgs a = given;
-  // outputs beyond 64 MiB would not be found in a cache by what reads them next anyway (2 x 8192 x
-  // 5376 bf16: 78 us with ordinary stores, 74 us past the caches)
-  a.stream = (int64_t)a.rows.R * a.C * (a.io == kIoBf16 ? 2 : 4) > (int64_t(64) << 20);
+  // bf16 outputs larger than the last-level cache (256 MiB) go past it: 8 x 8192 x 5376 263 -> 256 us, with
+  // the SSD scan that reads them 825 -> 814. What fits is left there for what reads it: 2 x 8192 x 5376 with
+  // the selective scan behind it 585 us, past the caches 591 (the convolution alone 80 and 78).
+  a.stream = (int64_t)a.rows.R * a.C * (a.io == kIoBf16 ? 2 : 4) > (int64_t(256) << 20);
   const int nvec = a.C / 8;
   // 16 rows a thread; 8 where that would leave fewer than four waves a SIMD
   const int strip = (int64_t)a.rows.R * nvec >= 16 * 262144 ? 16 : 8;
