@@ -152,12 +152,14 @@ struct Columns {
 };
 
 // f(group, first channel, channels, lane of K) for every group with channels in the tile, K threads
-// each: f adds up what it finds over the group's channels in this tile.
+// each: f adds up what it finds over the group's channels in this tile. K goes by the most groups that a tile
+// may hold, not by this one's: every tile of a group forms its sums in one order.
 template <typename F>
 __device__ __forceinline__ void groups_of_tile(const GroupArgs& q, int tile, F f) {
   const int cg = q.C / q.G, c0 = tile * kTile, c1 = min(c0 + kTile, q.C);
   const int g0 = c0 / cg, g1 = (c1 - 1) / cg + 1;
-  const int n = g1 - g0, per = n <= 4 ? 64 : n <= 8 ? 32 : n <= 16 ? 16 : n <= 32 ? 8 : n <= 64 ? 4 : 1;
+  const int n = min(q.G, kTile % cg ? (kTile - 2) / cg + 2 : kTile / cg);
+  const int per = n <= 4 ? 64 : n <= 8 ? 32 : n <= 16 ? 16 : n <= 32 ? 8 : n <= 64 ? 4 : 1;
   for (int g = g0 + (int)threadIdx.x / per; g < g1; g += kThreads / per) {
     const int a = max(g * cg, c0), b = min((g + 1) * cg, c1);
     f(g, a - c0, b - a, (int)threadIdx.x % per, per);
@@ -319,7 +321,7 @@ struct Pairs {
   }
 };
 
-// stats: written where given and not `ready` (by each strip alike: the same bits).
+// stats: written where given and not `ready` (by each strip and each tile of a group alike: the same bits).
 template <typename IO, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const float2* part,
                                                        const float2* ready, float2* stats, IO* y) {
