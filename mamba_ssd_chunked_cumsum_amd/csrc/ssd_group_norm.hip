@@ -37,13 +37,18 @@ __device__ __forceinline__ float inverse_root(float v) {
 // ---- how a problem is cut --------------------------------------------------------------------------
 // Strips of `rows` rows, of each sequence or (packed) of all rows, where the part of each sequence in a
 // strip has a slot of its own: strip + sequence, which grows by one from each part to the next. In the
-// same way the piece of a group in a tile of channels is piece tile + group.
+// same way the piece of a group in a tile of channels is piece tile + group. In the backward pass dense
+// sequences of which several fit a strip share it, `seqs` whole ones, each with its slot: what the strips leave
+// of every channel for dw and db is then small beside x and soon added up (2^20 single tokens x 1000 in groups
+// of 20: 0.1 GB where x has 2, not 8; 16384 x 2600 in groups of 650 1645 -> 1057 us). The forward leaves
+// nothing of the kind, and the loop over sequences costs it registers (20000 x 12 tokens x 1024 387 -> 434).
 struct Cut {
   int rows, per, strips;  // rows of a strip; strips of a sequence (packed: of all rows); strips
+  int seqs;               // sequences of a strip, where several may share one
   int tiles, pieces;
   int64_t slots;
 };
-Cut cut_of(const GroupArgs& a) {
+Cut cut_of(const GroupArgs& a, bool back) {
   Cut t;
   t.tiles = (a.C + kTile - 1) / kTile;
   t.pieces = t.tiles + a.G;
@@ -51,8 +56,11 @@ Cut cut_of(const GroupArgs& a) {
   t.rows = 64;  // (32, 128: slower) shorter where that leaves compute units without blocks
   while (t.rows > 16 && (rows + t.rows - 1) / t.rows * seqs * t.tiles < kBlocks) t.rows /= 2;
   t.per = (int)((rows + t.rows - 1) / t.rows);
-  t.strips = (int)(t.per * seqs);
-  t.slots = t.strips + (a.rows.starts ? (int64_t)a.rows.S : 0);
+  t.seqs = !back || a.rows.starts || t.per > 1 ? 1 : t.rows / a.rows.L;
+  // (as many blocks as run at once, eight a unit)
+  while (t.seqs > 1 && (seqs + t.seqs - 1) / t.seqs * t.tiles < 4 * kBlocks) --t.seqs;
+  t.strips = (int)(t.per * ((seqs + t.seqs - 1) / t.seqs));
+  t.slots = a.rows.starts ? t.strips + (int64_t)a.rows.S : t.per * seqs;
   return t;
 }
 
@@ -62,11 +70,18 @@ __device__ __forceinline__ int offset(const Rows& q, int i) {
 }
 
 // f(sequence, slot, first row, rows) for each part of a sequence in a strip; uniform over the block.
-template <typename F>
+// SHARED: strips of several dense sequences.
+template <bool SHARED, typename F>
 __device__ __forceinline__ void parts(const Rows& q, const Cut& t, int strip, F f) {
   if (!q.starts) {
-    const int s = strip / t.per, at = strip % t.per * t.rows;
-    f(s, (int64_t)strip, s * q.L + at, min(q.L - at, t.rows));
+    if constexpr (!SHARED) {
+      const int s = strip / t.per, at = strip % t.per * t.rows;
+      f(s, (int64_t)strip, s * q.L + at, min(q.L - at, t.rows));
+    } else {
+      const int s0 = strip / t.per * t.seqs, at = strip % t.per * t.rows, stop = min(s0 + t.seqs, q.S);
+      for (int s = s0; s < stop; ++s)
+        f(s, (int64_t)s * t.per + strip % t.per, s * q.L + at, min(q.L - at, t.rows));
+    }
     return;
   }
   const int front = offset(q, 0), begin = strip * t.rows, stop = min(q.R - begin, t.rows) + begin;
@@ -235,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_parts(GroupArgs q, Cut t, float
   const int lane = threadIdx.x & 63, tile = (int)(blockIdx.x % t.tiles);
   const int c = min(tile * kTile + lane * V, q.C - V);  // idle lanes load the last channels again
   const IO* x = (const IO*)q.x + c;
-  parts(q.rows, t, (int)(blockIdx.x / t.tiles), [&](int, int64_t slot, int r, int n) {
+  parts<false>(q.rows, t, (int)(blockIdx.x / t.tiles), [&](int, int64_t slot, int r, int n) {
     Vec<IO, V> first, v[kAhead];
     float sum[V], sq[V];
     first.load(x + r * q.xs);
@@ -331,7 +346,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const
   const bool live = c0 < q.C;
   const IO* x = (const IO*)q.x + c;
   const Affine af(q, c);
-  parts(q.rows, t, (int)(blockIdx.x / t.tiles), [&](int s, int64_t, int r, int n) {
+  parts<false>(q.rows, t, (int)(blockIdx.x / t.tiles), [&](int s, int64_t, int r, int n) {
     Pair<ONE> st;
     float o[V];
     Vec<IO, V> v[kAhead];
@@ -350,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const
 
 // ---- backward ----------------------------------------------------------------------------------------
 // part [slots, pieces]: sums of g = w dv and of g n. chan [strips, 2, C]: sums of dv (db), of dv n (dw).
-template <typename IO, bool ONE>
+template <typename IO, bool ONE, bool SHARED>
 __global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, Cut t, const float2* stats,
                                                            const IO* dy, float2* part, float* chan) {
   __shared__ Columns col;
@@ -363,7 +378,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, Cut t, c
   float db[kTile / kThreads], dw[kTile / kThreads];  // of channels tile * kTile + threadIdx.x + i 256
 #pragma unroll
   for (int i = 0; i < kTile / kThreads; ++i) db[i] = dw[i] = 0.f;
-  parts(q.rows, t, strip, [&](int s, int64_t slot, int r, int n) {
+  parts<SHARED>(q.rows, t, strip, [&](int s, int64_t slot, int r, int n) {
     Pair<ONE> st;
     float a[V], b[V];
     Vec<IO, V> v[kAhead], e[kAhead];
@@ -416,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_parts(GroupArgs q, Cut t, c
 
 // dx = rstd (g - mean(g) - n mean(g n)); zero in rows of no sequence. The blocks behind the strips' add
 // up the columns of chan, 64 each, in a fixed order.
-template <typename IO, bool ONE>
+template <typename IO, bool ONE, bool SHARED>
 __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, Cut t, const float2* stats,
                                                            const float2* part, const float2* ready,
                                                            const float* chan, const IO* dy, IO* dx,
@@ -459,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GroupArgs q, Cut t, c
     if (live)
       for (int i = done + wave; i < to; i += kWaves) store_vec<IO, V>(dx + (int64_t)i * q.C + c, o);
   };
-  parts(q.rows, t, strip, [&](int s, int64_t, int r, int n) {
+  parts<SHARED>(q.rows, t, strip, [&](int s, int64_t, int r, int n) {
     Pair<ONE> st, m;
     Vec<IO, V> v[kAhead], e[kAhead];
     if (q.rows.starts) {
@@ -1034,7 +1049,7 @@ bool group_norm_fits(const GroupArgs& a) {
 int64_t group_norm_bytes(const GroupArgs& a) {
   Whole w;
   if (few_tokens(a) || whole_of(a, true, &w)) return 0;
-  const Cut t = cut_of(a);
+  const Cut t = cut_of(a, false);
   return 8 * (up64(t.slots * t.pieces) + (int64_t)a.rows.S * a.G);
 }
 
@@ -1069,7 +1084,7 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
       };
       return w.deep ? go(k_gn_whole<IO, 2 * kRows<IO>>) : go(k_gn_whole<IO, kRows<IO>>);
     }
-    const Cut t = cut_of(a);
+    const Cut t = cut_of(a, false);
     float2 *part = (float2*)ws, *ready = nullptr;
     const dim3 grid((unsigned)((int64_t)t.strips * t.tiles));
     hipLaunchKernelGGL((k_gn_parts<IO>), grid, dim3(kThreads), 0, s, a, t, part);
@@ -1093,7 +1108,7 @@ int64_t group_norm_backward_bytes(const GroupArgs& a) {
   if (few_tokens(a)) return 4 * (int64_t)walkers_of(a) * 2 * a.C;
   Whole w;
   if (whole_of(a, false, &w)) return a.rows.S > 1 ? 8 * (int64_t)a.rows.S * a.C : 0;
-  const Cut t = cut_of(a);
+  const Cut t = cut_of(a, true);
   return 8 * (up64(t.slots * t.pieces) + up64((int64_t)a.rows.S * a.G) + (int64_t)t.strips * a.C);
 }
 
@@ -1126,14 +1141,14 @@ hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, co
       if (e != hipSuccess || !add) return e;
       return launch_column_sums(ws, a.rows.S, 0, nullptr, 1, 0, 0, a.C, db, a.C, dw, s);
     }
-    const Cut t = cut_of(a);
+    const Cut t = cut_of(a, true);
     float2 *part = (float2*)ws, *ready = nullptr, *mid = part + up64(t.slots * t.pieces);
     float* chan = dw || db ? (float*)(mid + up64((int64_t)a.rows.S * a.G)) : nullptr;
     const unsigned blocks = (unsigned)((int64_t)t.strips * t.tiles);
     const unsigned more = chan ? (2 * a.C + 63) / 64 : 0;
-    auto passes = [&](auto one) {
-      constexpr bool ONE = decltype(one)::value;
-      hipLaunchKernelGGL((k_gn_bwd_parts<IO, ONE>), dim3(blocks), dim3(kThreads), 0, s, a, t,
+    auto passes = [&](auto one, auto shared) {
+      constexpr bool ONE = decltype(one)::value, SHARED = decltype(shared)::value;
+      hipLaunchKernelGGL((k_gn_bwd_parts<IO, ONE, SHARED>), dim3(blocks), dim3(kThreads), 0, s, a, t,
                          (const float2*)stats, (const IO*)dy, part, chan);
       if (!adds_itself(a, t, false)) {
         ready = mid;
@@ -1141,11 +1156,14 @@ hipError_t launch_group_norm_backward(const GroupArgs& a, const float* stats, co
                            dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
                            dim3(kThreads), 0, s, a, t, part, ready);
       }
-      hipLaunchKernelGGL((k_gn_bwd_apply<IO, ONE>), dim3(blocks + more), dim3(kThreads), 0, s, a, t,
+      hipLaunchKernelGGL((k_gn_bwd_apply<IO, ONE, SHARED>), dim3(blocks + more), dim3(kThreads), 0, s, a, t,
                          (const float2*)stats, part, ready, chan, (const IO*)dy, (IO*)dx, dw, db);
       return hipGetLastError();
     };
-    return a.C / a.G % V ? passes(std::false_type{}) : passes(std::true_type{});
+    auto by_strip = [&](auto one) {
+      return t.seqs > 1 ? passes(one, std::true_type{}) : passes(one, std::false_type{});
+    };
+    return a.C / a.G % V ? by_strip(std::false_type{}) : by_strip(std::true_type{});
   };
   return a.io == kIoBf16 ? run(u16{}) : run(float{});
 }
