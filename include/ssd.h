@@ -441,9 +441,11 @@ ssd_status ssd_residual_norm_backward(const ssd_tokens* tokens, const void* resi
  * the scan above, and their limits; of launches below 2^32 threads: the recurrence takes rows (dense:
  * of sequences rounded up to 28) times channels / 128 (fp32: / 64), rounded up, below 2^28, the
  * rotation rows times ngroups / 4 and nfreq / 4 (fp32 in pairs: / 2) + (dstate - 2 nfreq) / 8 below 2^32,
- * the group norm sequences times ngroups below 2^26 where a sequence may have more than 8 tokens, and
- * otherwise sequences times ngroups times a group's channels / 8, rounded up to a power of two (past 64:
- * to a multiple of 64), below 2^32. */
+ * the group norm dense sequences of up to 8 tokens, in groups of a multiple of 8 channels up to 8192 (of
+ * more tokens than one: 4096), where sequences times ngroups times a group's channels / 8, rounded up to a
+ * power of two (past 64: to a multiple of 64), is below 2^32; of others, strips of 64 rows of each sequence
+ * (packed: of all rows) times channels / 512, both rounded up, below 2^24 - channels / 32 - 1, and sequences
+ * times ngroups below 2^26 - 4 (dense sequences of up to 192 tokens: any). */
 
 /* Gated linear recurrence. For every channel of each sequence, with v = sigmoid(input_gate) x (x where
  * input_gate is NULL):

@@ -1040,10 +1040,11 @@ bool group_norm_fits(const GroupArgs& a) {
   if (few_tokens(a)) return fits(double(a.rows.S) * a.G * lanes_of(a).per / kThreads + 1);
   Whole w;
   if (whole_of(a, false, &w)) return true;
-  const double tiles = a.C / kTile + 1, rows = a.rows.starts ? a.rows.R : a.rows.L;
-  const double strips = (rows / 16 + 1) * (a.rows.starts ? 1 : a.rows.S);
-  return fits(strips * tiles + a.C) && fits(double(a.rows.S) * a.G / kWaves + 1) &&
-         (strips + a.rows.S) * (tiles + a.G) < 1099511627776.0 && strips < 2147483648.0;
+  const Cut t = cut_of(a, true), f = cut_of(a, false);
+  // (k_gn_totals is launched where the second pass does not add up by itself)
+  return fits(double(t.strips) * t.tiles + (2 * a.C + 63) / 64) && fits(double(f.strips) * f.tiles + 1) &&
+         (fits(double(a.rows.S) * a.G / kWaves + 1) || (!a.rows.starts && adds_itself(a, t, false))) &&
+         double(t.slots) * t.pieces < 1099511627776.0;
 }
 
 int64_t group_norm_bytes(const GroupArgs& a) {
