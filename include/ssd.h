@@ -294,11 +294,13 @@ ssd_status ssd_backward(const ssd_problem* prob, const void* x, const float* dt,
  *
  * Arithmetic is fp32; activations and their gradients are rounded once to the io dtype;
  * parameters, their gradients, scan states and state gradients are fp32. Results are bitwise
- * reproducible (fixed reduction order, no atomics). Gradient outputs are overwritten. No output
+ * reproducible (every sum in a fixed order). Gradient outputs are overwritten. No output
  * may overlap an input or another output, but for the states of the single-token entry points
  * (state_out may be state_in). No call allocates: where a workspace is needed the caller gives
  * it (the matching _workspace query tells its bytes), and calls that overlap in time need one
- * each; so every entry point can be captured into a graph, which then holds that workspace.
+ * each: results of calls that share one are undefined (ssd_recurrence may then take some seconds,
+ * and gives NaN, or leaves outputs as they were, where it finds its workspace overwritten). So every
+ * entry point can be captured into a graph, which then holds that workspace.
  * The current device must be the one that holds the tensors.
  *
  * Limits (beyond them SSD_ERR_UNSUPPORTED): channels a multiple of 8 up to 2^20; rows, and

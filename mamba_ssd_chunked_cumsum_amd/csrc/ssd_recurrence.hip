@@ -298,6 +298,10 @@ struct Chain {
   int counters;
 };
 constexpr int kApart = 16;
+// Looks at the words of the chunks in front, each at least a load that passes the caches (over half a
+// microsecond): half a second or more where an ordinary wait is some microseconds. It runs out only where
+// another call uses the same workspace at the same time; what has not come then counts as NaN.
+constexpr int kLooks = 1 << 20;
 __device__ __forceinline__ void publish(uint64_t* slot, float P, float H) {
   uint32_t h = __float_as_uint(H);
   if (h == ~0u) h = 0x7fc00000u;  // (a NaN of a caller's, which would look empty)
@@ -318,7 +322,9 @@ __global__ __launch_bounds__(256) void k_rec_clear(Chain chain, int64_t n) {
 // slower), and rows of the tensors loaded in turn.
 // CHAIN: sequences of several chunks. A block belongs to a tile and sequence and takes the next chunk of
 // them by a ticket. It waits only for chunks before its own, whose blocks have lower tickets: those are
-// running or done, and the first of them waits for none, so every wait ends.
+// running or done, and the first of them waits for none, so every wait ends. (Calls that share a workspace
+// and overlap, against the contract, take tickets from one counter and clear each other's words: a ticket
+// past the last chunk is no work, and a wait ends after kLooks.)
 template <typename X, typename IO, bool DECAY, bool GATED, bool PACKED, bool CHAIN>
 __global__ __launch_bounds__(64 * X::W) void k_rec(RecArgs q, Plan pl, int tiles, Chain chain,
                                                    IO* __restrict__ y, float* __restrict__ fin) {
@@ -347,7 +353,9 @@ __global__ __launch_bounds__(64 * X::W) void k_rec(RecArgs q, Plan pl, int tiles
   if (CHAIN) {
     if (threadIdx.x == 0) place = ticket;
     __syncthreads();
-    unit = s * pl.chunks + __builtin_amdgcn_readfirstlane(place);
+    const unsigned turn = __builtin_amdgcn_readfirstlane(place);
+    if (turn >= (unsigned)pl.chunks) return;
+    unit = s * pl.chunks + (int)turn;
   }
   const Place at(q.rows, pl, T, unit);
   Word<IO, B> rx[T], rg[T], ri[T];
@@ -424,7 +432,8 @@ __global__ __launch_bounds__(64 * X::W) void k_rec(RecArgs q, Plan pl, int tiles
         e[j] = !PACKED && q.h0 ? q.h0[(int64_t)at.s * q.C + c + j] : 0.f;
       uint64_t got[kGroup][V];
       bool all;
-      do {  // (see above: it ends)
+      int looks = 0;
+      do {
         all = true;
 #pragma unroll
         for (int i = 0; i < kGroup; ++i)
@@ -436,7 +445,7 @@ __global__ __launch_bounds__(64 * X::W) void k_rec(RecArgs q, Plan pl, int tiles
               all = all && got[i][j] != kEmpty;
             }
           }
-      } while (!__all(all));
+      } while (!__all(all) && ++looks < kLooks);
 #pragma unroll
       for (int i = 0; i < kGroup; ++i)
         if (from + i < chunk) {
