@@ -941,7 +941,7 @@ bool recurrence_fits(const RecArgs& a) {
   const Plan f = plan<Fwd>(a.rows), b = by_shape(a, [](auto, Plan p) { return p; });
   return fits(double(tiles_of<Fwd>(a)) * f.units + 4096, threads_of(f)) &&
          fits(double(tiles_of<Bwd>(a)) * b.units + 4096, threads_of(b)) &&
-         fits(double(a.rows.starts ? 1 : a.rows.S) * a.C / 64 + 1, 64 * kParts);
+         (b.chunks == 1 || fits(double(a.rows.starts ? 1 : a.rows.S) * a.C / 64 + 1, 2 * 64 * kParts));
 }
 
 // Chained: the tickets, then the slots.
