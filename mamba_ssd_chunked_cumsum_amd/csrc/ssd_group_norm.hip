@@ -6,8 +6,8 @@
 // Longer sequences are cut into strips of rows and tiles of channels: one kernel leaves the mean and
 // squared deviations (backward: sums of g and g n, and what dw and db need) of every group's piece in
 // every strip; the second adds up those of its groups and finds what the last-level cache kept of x
-// (and dy). A group may have any number of channels. 2 x 8192 x 2560 bf16 in 32 groups: 17 and 35 us
-// (reading x twice and writing y at a copy's rate takes 47), backward 46 and 44 (84).
+// (and dy). A group may have any number of channels. 2 x 8192 x 2560 bf16 in 32 groups: 50 us in all
+// (reading x twice and writing y at a copy's rate takes 47), backward 89 (84).
 //
 // Squared deviations are taken from a value of the strip itself (its first row, channel by channel):
 // their sum about that value is at most n + 1 times the sum about the mean for n rows, so the

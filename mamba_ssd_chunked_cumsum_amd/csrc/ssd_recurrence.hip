@@ -1000,7 +1000,7 @@ hipError_t launch_recurrence_backward(const RecArgs& given, const void* dy, cons
   const int tiles = tiles_of<Bwd>(a);
   // Chunks that look up the others' sums by themselves: few of them (32 x 128 x 5120 bf16 138 -> 119 us), or
   // some more where all run at once and a launch counts (400 x 1536 28 -> 24; with 24 chunks and more
-  // blocks, 8 x 670 x 5120, 147 -> 191).
+  // blocks, 8 x 670 x 5120, 147 -> 191). The borders lie between these sizes, no nearer to either.
   const bool few = p.chunks <= 8 || (p.chunks <= 24 && (int64_t)tiles * p.units <= 1024);
   const int chained = p.chunks == 1 ? kAlone : few ? kSingly : kJoined;
   const int64_t n = sum_floats(a, p);

@@ -5,8 +5,9 @@
 // frequencies of a token, forms their sines and cosines once and turns the entries of up to kHeads heads,
 // of B and of C. Every load and store is 16 bytes where the sizes allow it and neighbours take neighbouring
 // ones: in halves that is two vectors of eight (fp32: four) frequencies each, in pairs one vector of four
-// (two). The angle is formed in 64 bits: position times frequency is exact there, and what a far position
-// leaves of a turn keeps 2^-53 of the whole angle.
+// (two). The angle is formed in 64 bits: position times frequency is exact there up to 2^29 positions
+// (29 and 24 bits), rounded to 53 bits beyond, and so is its product with 2 / pi, itself rounded: what a far
+// position leaves of a turn is off by a few 2^-53 of the whole angle.
 //
 // B and C of 2 x 16384 x 8 x 256 bf16: 94 us (5.7 TB/s) in halves, 91 in pairs (with two vectors a thread
 // there, whose stores leave every other 16 bytes to the next, 146; fp32 181, then 317).

@@ -139,7 +139,7 @@ def rotate(x, positions, frequencies, sections, interleaved=False, inverse=False
     """(values, bound) of x [rows, G, N] turned; positions [axes, rows]."""
     x, freq = np.asarray(x, np.float64), np.asarray(frequencies, np.float64)
     axis = np.repeat(np.arange(len(sections)), sections)
-    angle = np.asarray(positions)[axis].T.astype(np.float64) * freq  # exact: 31 and 24 bits
+    angle = np.asarray(positions)[axis].T.astype(np.float64) * freq  # exact up to 2^29 (29 and 24 bits)
     angle = angle[:, None, :] * (-1.0 if inverse else 1.0)
     n = len(freq)
     p, q = (np.arange(0, 2 * n, 2), np.arange(1, 2 * n, 2)) if interleaved else \
