@@ -11,7 +11,10 @@
 //
 // Squared deviations are taken from a value of the strip itself (its first row, channel by channel):
 // their sum about that value is at most n + 1 times the sum about the mean for n rows, so the
-// difference keeps all but a few bits wherever the mean lies.
+// difference keeps all but a few bits wherever the mean lies. A group's channels are put together as distances
+// from one of its values, too, and pieces in 64 bits from that value and the mean's distance to it.
+#include <type_traits>
+
 #include "ssd_recurrent.h"
 #include "ssd_selective.h"
 
@@ -187,10 +190,18 @@ __device__ __forceinline__ F sum_of(F v, int per) {  // over neighbouring thread
 }
 
 // ---- sums over a sequence and group ------------------------------------------------------------------
-// Mean and 1 / sqrt(variance + eps) of a group from its pieces (mean, squared deviations), or (BACK) the
-// means of g and g n from their sums. `per` threads share it; sums in 64 bits, in a fixed order.
+// What is left of a group's piece: a value of it, the mean's distance to that, the sum of squared deviations
+// from the mean; or (BACK) sums of g and of g n.
+struct Moments {
+  float value, mean, dev;
+};
 template <bool BACK>
-__device__ __forceinline__ float2 total_of(const GroupArgs& q, const Cut& t, const float2* part, int s,
+using Piece = std::conditional_t<BACK, float2, Moments>;
+
+// Mean and 1 / sqrt(variance + eps) of a group from its pieces, or (BACK) the means of g and g n. `per` threads
+// share it; sums in 64 bits, in a fixed order.
+template <bool BACK>
+__device__ __forceinline__ float2 total_of(const GroupArgs& q, const Cut& t, const Piece<BACK>* part, int s,
                                            int g, int lane, int per) {
   const int cg = q.C / q.G, t0 = g * cg / kTile, n = ((g + 1) * cg - 1) / kTile - t0 + 1;
   const Slots at(q.rows, t, s);
@@ -198,7 +209,7 @@ __device__ __forceinline__ float2 total_of(const GroupArgs& q, const Cut& t, con
   const int64_t all = (int64_t)at.n * n;
   constexpr int U = 4;  // loads issued together
   for (int64_t i0 = lane; i0 < all; i0 += U * per) {
-    float2 v[U];
+    Piece<BACK> v[U];
     int slot[U], tile[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -210,15 +221,15 @@ __device__ __forceinline__ float2 total_of(const GroupArgs& q, const Cut& t, con
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i0 + u * per >= all) break;
-      if (BACK) {
+      if constexpr (BACK) {
         a += v[u].x;
         b += v[u].y;
       } else {
         const int width = min((g + 1) * cg, (tile[u] + 1) * kTile) - max(g * cg, tile[u] * kTile);
-        const double m = v[u].x, k = (double)at.rows(q.rows, t, slot[u]) * width;
+        const double m = (double)v[u].value + v[u].mean, k = (double)at.rows(q.rows, t, slot[u]) * width;
         a += k * m;
         b += k * m * m;  // (in 64 bits the difference below loses nothing that 32 hold)
-        dev += v[u].y;
+        dev += v[u].dev;
       }
     }
   }
@@ -234,7 +245,7 @@ __device__ __forceinline__ float2 total_of(const GroupArgs& q, const Cut& t, con
 // out [S, G]: where a block of the second pass would have too much to add up, or stats are asked for
 // of sequences without tokens (0 and 1 / sqrt(eps)). A wave each.
 template <bool BACK>
-__global__ __launch_bounds__(kThreads) void k_gn_totals(GroupArgs q, Cut t, const float2* part,
+__global__ __launch_bounds__(kThreads) void k_gn_totals(GroupArgs q, Cut t, const Piece<BACK>* part,
                                                         float2* out) {
   const int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
   if (u >= (int64_t)q.rows.S * q.G) return;
@@ -243,9 +254,9 @@ __global__ __launch_bounds__(kThreads) void k_gn_totals(GroupArgs q, Cut t, cons
 }
 
 // ---- forward -----------------------------------------------------------------------------------------
-// part [slots, pieces]: mean and sum of squared deviations.
+// part [slots, pieces].
 template <typename IO>
-__global__ __launch_bounds__(kThreads) void k_gn_parts(GroupArgs q, Cut t, float2* part) {
+__global__ __launch_bounds__(kThreads) void k_gn_parts(GroupArgs q, Cut t, Moments* part) {
   __shared__ Columns col;
   const int lane = threadIdx.x & 63, tile = (int)(blockIdx.x % t.tiles);
   const int c = min(tile * kTile + lane * V, q.C - V);  // idle lanes load the last channels again
@@ -270,19 +281,20 @@ __global__ __launch_bounds__(kThreads) void k_gn_parts(GroupArgs q, Cut t, float
     const float rows = (float)n;
     const IO* top = (const IO*)q.x + r * q.xs + tile * kTile;
     groups_of_tile(q, tile, [&](int g, int c0, int width, int me, int per) {
+      const float value = Io<IO>::load(top, c0);
       float mean = 0.f, dev = 0.f;
       for (int i = c0 + me; i < c0 + width; i += per) {
         const float d = col.red[0][0][i] / rows;
-        mean += Io<IO>::load(top, i) + d;
+        mean += (Io<IO>::load(top, i) - value) + d;
         dev += fmaxf(fmaf(-d, col.red[0][0][i], col.red[0][1][i]), 0.f);
       }
       mean = sum_of(mean, per) / width;
       for (int i = c0 + me; i < c0 + width; i += per) {
-        const float d = Io<IO>::load(top, i) + col.red[0][0][i] / rows - mean;
+        const float d = (Io<IO>::load(top, i) - value) + col.red[0][0][i] / rows - mean;
         dev = fmaf(rows * d, d, dev);
       }
       dev = sum_of(dev, per);
-      if (me == 0) part[slot * t.pieces + tile + g] = make_float2(mean, dev);
+      if (me == 0) part[slot * t.pieces + tile + g] = Moments{value, mean, dev};
     });
   });
 }
@@ -313,7 +325,7 @@ struct Pair {
 struct Pairs {
   float2 of[kTile];
   template <bool BACK, bool ONE>
-  __device__ __forceinline__ void get(const GroupArgs& q, const Cut& t, const float2* part,
+  __device__ __forceinline__ void get(const GroupArgs& q, const Cut& t, const Piece<BACK>* part,
                                       const float2* ready, int s, int tile, int c, Pair<ONE>& v,
                                       float2* out) {
     const int cg = q.C / q.G;
@@ -338,7 +350,7 @@ struct Pairs {
 
 // stats: written where given and not `ready` (by each strip and each tile of a group alike: the same bits).
 template <typename IO, bool ONE>
-__global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const float2* part,
+__global__ __launch_bounds__(kThreads) void k_gn_apply(GroupArgs q, Cut t, const Moments* part,
                                                        const float2* ready, float2* stats, IO* y) {
   __shared__ Pairs pairs;
   const int lane = threadIdx.x & 63, tile = (int)(blockIdx.x % t.tiles);
@@ -1051,7 +1063,7 @@ int64_t group_norm_bytes(const GroupArgs& a) {
   Whole w;
   if (few_tokens(a) || whole_of(a, true, &w)) return 0;
   const Cut t = cut_of(a, false);
-  return 8 * (up64(t.slots * t.pieces) + (int64_t)a.rows.S * a.G);
+  return 4 * up64(3 * t.slots * t.pieces) + 8 * (int64_t)a.rows.S * a.G;
 }
 
 hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, float* ws,
@@ -1086,11 +1098,12 @@ hipError_t launch_group_norm(const GroupArgs& given, void* y, float* stats, floa
       return w.deep ? go(k_gn_whole<IO, 2 * kRows<IO>>) : go(k_gn_whole<IO, kRows<IO>>);
     }
     const Cut t = cut_of(a, false);
-    float2 *part = (float2*)ws, *ready = nullptr;
+    Moments* part = (Moments*)ws;
+    float2* ready = nullptr;
     const dim3 grid((unsigned)((int64_t)t.strips * t.tiles));
     hipLaunchKernelGGL((k_gn_parts<IO>), grid, dim3(kThreads), 0, s, a, t, part);
     if (!adds_itself(a, t, stats != nullptr)) {
-      ready = stats ? (float2*)stats : part + up64(t.slots * t.pieces);
+      ready = stats ? (float2*)stats : (float2*)(ws + up64(3 * t.slots * t.pieces));
       hipLaunchKernelGGL((k_gn_totals<false>),
                          dim3((unsigned)(((int64_t)a.rows.S * a.G + kWaves - 1) / kWaves)),
                          dim3(kThreads), 0, s, a, t, part, ready);
