@@ -6,7 +6,7 @@
 // Longer sequences are cut into strips of rows and tiles of channels: one kernel leaves the mean and
 // squared deviations (backward: sums of g and g n, and what dw and db need) of every group's piece in
 // every strip; the second adds up those of its groups and finds what the last-level cache kept of x
-// (and dy). A group may have any number of channels. 2 x 8192 x 2560 bf16 in 32 groups: 50 us in all
+// (and dy). A group may have any number of channels. 2 x 8192 x 2560 bf16 in 32 groups: 47 us in all
 // (reading x twice and writing y at a copy's rate takes 47), backward 89 (84).
 //
 // Squared deviations are taken from a value of the strip itself (its first row, channel by channel):
@@ -44,7 +44,7 @@ __device__ __forceinline__ float inverse_root(float v) {
 // sequences of which several fit a strip share it, `seqs` whole ones, each with its slot: what the strips leave
 // of every channel for dw and db is then small beside x and soon added up (2^20 single tokens x 1000 in groups
 // of 20: 0.1 GB where x has 2, not 8; 16384 x 2600 in groups of 650 1645 -> 1057 us). The forward leaves
-// nothing of the kind, and the loop over sequences costs it registers (20000 x 12 tokens x 1024 387 -> 434).
+// nothing of the kind, and the loop over sequences costs it registers (20000 x 12 tokens x 1024 387 -> 434 us).
 struct Cut {
   int rows, per, strips;  // rows of a strip; strips of a sequence (packed: of all rows); strips
   int seqs;               // sequences of a strip, where several may share one
